@@ -8,6 +8,10 @@ importing fails loudly when the library has not been built.
 
 Convenience wrappers ``forward`` / ``backward`` allocate outputs, the saved chunk
 states and the workspace with torch and call ``gdn_fwd`` / ``gdn_bwd``.
+
+The operators around the recurrence (``include/gdn_layer.h``: the selective state space scan,
+the conv1d with a carried window, the gated norm and the residual addition with its norm) are
+bound in ``layer`` and are names of this package too.
 """
 from __future__ import annotations
 
@@ -311,3 +315,11 @@ def backward(p, q, k, v, g, beta, S0, states, dO, dS_T=None, grads=None, want_dS
     gdn_bwd(p, q, k, v, g, beta, S0, states, dO, dS_T, grads["dq"], grads["dk"], grads["dv"], grads["dg"],
             grads["dbeta"], grads["dS0"], workspace, stream)
     return grads
+
+
+from .layer import (  # noqa: E402,F401  (the operators of gdn_layer.h)
+    LAYER_EXPORTED, add_norm_backward, add_norm_forward, gated_norm_backward, gated_norm_forward, gdn_add_norm_bwd,
+    gdn_add_norm_bwd_workspace_bytes, gdn_add_norm_fwd, gdn_conv1d_silu_decode, gdn_conv1d_silu_prompt,
+    gdn_gated_norm_bwd, gdn_gated_norm_bwd_workspace_bytes, gdn_gated_norm_fwd, gdn_norm_problem, gdn_ssm_bwd,
+    gdn_ssm_bwd_workspace_bytes, gdn_ssm_chunk_state_bytes, gdn_ssm_decode, gdn_ssm_fwd, gdn_ssm_fwd_workspace_bytes,
+    gdn_ssm_problem, make_norm_problem, make_ssm_problem, ssm_backward, ssm_forward)

@@ -14,7 +14,8 @@ OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 
 SOURCES = ["gdn_fwd.hip", "gdn_bwd.hip", "gdn_decode.hip", "gdn_conv.hip", "gdn_scratch.hip", "gdn_abi.cpp",
-           "gdn_trace.cpp"]
+           "gdn_trace.cpp", "layer/conv_carry.hip", "layer/norm.hip", "layer/ssm_decode.hip", "layer/ssm_sweep.hip",
+           "layer/ssm_grad.hip", "layer/layer_abi.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 # Packed-FP32 instructions are disabled for every device pass.
@@ -26,7 +27,7 @@ FLAGS = [
 
 
 def _compile(src: str) -> str:
-    obj = os.path.join(OBJDIR, os.path.splitext(src)[0] + ".o")
+    obj = os.path.join(OBJDIR, os.path.splitext(os.path.basename(src))[0] + ".o")
     cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
     if src.endswith(".cpp"):
         cmd.insert(1, "-xhip")

@@ -1,0 +1,188 @@
+// conv_carry.hip -- causal depthwise conv1d + SiLU with a carried window, on gfx950: prompts
+// that continue from the rows before them, and one token per sequence.
+//
+//   z[t] = bias + sum_{j < K} w[ch][j] ext[t + j],  y[t] = z[t] sigma(z[t])
+//
+// with ext the K - 1 carried rows followed by the sequence's rows. What a continuation needs is
+// the last K - 1 rows of ext, copied as they are. Pure streaming: each row is read and written
+// once (2 ch values per row), bound by HBM; the window lives in registers.
+#include "vec8.h"
+
+namespace gdn {
+
+// Rows [lo, hi) of sequence l, clamped into [0, rows] (a malformed table never leads outside).
+__device__ __forceinline__ void carry_clamp(const ConvCarryArgs& a, int l, int64_t& lo, int64_t& hi) {
+  if (!a.cu) {
+    lo = (int64_t)l * a.T;
+    hi = lo + a.T;
+    return;
+  }
+  int64_t x = a.cu[l], y = a.cu[l + 1];
+  x = x < 0 ? 0 : (x > a.rows ? a.rows : x);
+  y = y < x ? x : (y > a.rows ? a.rows : y);
+  lo = x;
+  hi = y;
+}
+
+// The sequence of row t and its rows [lo, hi). A row of no sequence (behind the last one, or in
+// front of cu[0] in a malformed table) gets one that does not hold it.
+__device__ __forceinline__ int carry_seq(const ConvCarryArgs& a, int64_t t, int64_t& lo, int64_t& hi) {
+  int l = 0;
+  if (!a.cu) {
+    l = (int)(t / a.T);
+  } else {
+    int r = a.N;  // largest n with cu[n] <= t
+    while (r - l > 1) {
+      const int m = (l + r) >> 1;
+      if (a.cu[m] <= t) l = m; else r = m;
+    }
+  }
+  carry_clamp(a, l, lo, hi);
+  return l;
+}
+
+// Each thread owns 8 adjacent channels and RUN consecutive rows, the next PF of them in flight.
+// Blocks past the runs copy one sequence's last rows each.
+template <typename TI, int K, int RUN, int PF>
+__global__ __launch_bounds__(256) void k_conv_prompt(ConvCarryArgs a) {
+  const int c0 = (int)(blockIdx.y * blockDim.x + threadIdx.x) * 8;
+  if (c0 >= a.ch) return;
+  const TI* x = (const TI*)a.x + c0;
+  const TI* first = a.first ? (const TI*)a.first + c0 : nullptr;
+  const int64_t runs = (a.rows + RUN - 1) / RUN;
+  int64_t lo, hi;
+  // Row s of sequence n's ext relative to the sequence (s < 0: carried rows).
+  auto carried = [&](int n, int64_t s) -> F8 {
+    return first ? ld8<TI>(first + ((int64_t)n * (K - 1) + (K - 1) + s) * a.ch) : zero8();
+  };
+  if ((int64_t)blockIdx.x >= runs) {
+    const int n = (int)(blockIdx.x - runs);
+    carry_clamp(a, n, lo, hi);
+    TI* last = (TI*)a.last + c0;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      const int64_t s = hi - lo - (K - 1) + j;
+      st8<TI>(last + ((int64_t)n * (K - 1) + j) * a.ch, s >= 0 ? ld8<TI>(x + (lo + s) * a.x_rs) : carried(n, s));
+    }
+    return;
+  }
+  const int64_t t0 = (int64_t)blockIdx.x * RUN;
+  const int64_t t1 = t0 + RUN < a.rows ? t0 + RUN : a.rows;
+  TI* y = (TI*)a.y + c0;
+  Raw8<TI> buf[PF];
+#pragma unroll
+  for (int u = 0; u < PF; ++u)
+    if (t0 + u < t1) buf[u] = ldraw8<true, TI>(x + (t0 + u) * a.x_rs);
+  float w[K][8], bias[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[j][i] = a.w[(int64_t)(c0 + i) * K + j];
+    bias[i] = a.bias ? a.bias[c0 + i] : 0.f;
+  }
+  F8 win[K > 1 ? K - 1 : 1];
+  auto enter = [&](int64_t t) {  // the window in front of row t
+    const int n = carry_seq(a, t, lo, hi);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      const int64_t s = t - lo - (K - 1) + j;
+      win[j] = t < lo || t >= hi ? zero8() : s >= 0 ? ld8<TI>(x + (lo + s) * a.x_rs) : carried(n, s);
+    }
+  };
+  enter(t0);
+  for (int64_t base = t0; base < t1; base += PF) {
+#pragma unroll
+    for (int u = 0; u < PF; ++u) {
+      const int64_t t = base + u;
+      if (t >= t1) break;
+      const F8 xt = cvt8<TI>(buf[u]);
+      if (t + PF < t1) buf[u] = ldraw8<true, TI>(x + (t + PF) * a.x_rs);
+      if (t >= hi && t > t0) enter(t);
+      F8 out;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float z = bias[i] + w[K - 1][i] * xt.v[i];
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) z += w[j][i] * win[j].v[i];
+        out.v[i] = z * sigmoidf(z);
+      }
+      if (t >= lo && t < hi) st8<TI>(y + t * a.y_rs, out);  // rows of no sequence stay as they were
+#pragma unroll
+      for (int j = 0; j + 1 < K - 1; ++j) win[j] = win[j + 1];
+      if constexpr (K > 1) win[K - 2] = xt;
+    }
+  }
+}
+
+// One token: grid (rows, channel blocks). The window is read, moved on by one row and written.
+template <typename TI, int K> __global__ __launch_bounds__(256) void k_conv_decode(ConvCarryArgs a) {
+  const int c0 = (int)(blockIdx.y * blockDim.x + threadIdx.x) * 8;
+  if (c0 >= a.ch) return;
+  const int n = blockIdx.x;
+  const int slot = a.idx ? a.idx[n] : n;
+  if (slot < 0 || (K > 1 && slot >= a.n_slots)) return;  // the row is skipped
+  const F8 xt = ld8<TI>((const TI*)a.x + (int64_t)n * a.x_rs + c0);
+  TI* st = (TI*)a.state + (int64_t)slot * (K - 1) * a.ch + c0;
+  F8 win[K > 1 ? K - 1 : 1];
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) win[j] = ld8<TI>(st + (int64_t)j * a.ch);
+  F8 out;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float z = a.bias ? a.bias[c0 + i] : 0.f;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) z += a.w[(int64_t)(c0 + i) * K + j] * win[j].v[i];
+    z += a.w[(int64_t)(c0 + i) * K + K - 1] * xt.v[i];
+    out.v[i] = z * sigmoidf(z);
+  }
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) st8<TI>(st + (int64_t)j * a.ch, j + 1 < K - 1 ? win[j + 1 < K - 1 ? j + 1 : j] : xt);
+  st8<TI>((TI*)a.y + (int64_t)n * a.y_rs + c0, out);
+}
+
+// Threads of a workgroup along the channels: whole waves, at most 256.
+static int conv_threads(int ch) {
+  const int t = (ch / 8 + 63) / 64 * 64;
+  return t < 256 ? t : 256;
+}
+
+template <typename TI, int K, int RUN, int PF> static void prompt_run(const ConvCarryArgs& a, hipStream_t s) {
+  const int nt = conv_threads(a.ch);
+  const int64_t blocks = (a.rows + RUN - 1) / RUN + (a.last && K > 1 ? a.N : 0);
+  if (blocks == 0) return;
+  const dim3 grid((unsigned)blocks, (unsigned)((a.ch / 8 + nt - 1) / nt));
+  traced("k_conv_prompt", s, [&] { k_conv_prompt<TI, K, RUN, PF><<<grid, nt, 0, s>>>(a); });
+}
+
+template <typename TI, int K> static hipError_t prompt_k(const ConvCarryArgs& a, hipStream_t s) {
+  prompt_run<TI, K, 32, 1>(a, s);
+  return hipGetLastError();
+}
+
+template <typename TI, int K> static hipError_t decode_k(const ConvCarryArgs& a, hipStream_t s) {
+  const int nt = conv_threads(a.ch);
+  const dim3 grid((unsigned)a.N, (unsigned)((a.ch / 8 + nt - 1) / nt));
+  traced("k_conv_decode", s, [&] { k_conv_decode<TI, K><<<grid, nt, 0, s>>>(a); });
+  return hipGetLastError();
+}
+
+template <typename TI> static hipError_t conv_t(const ConvCarryArgs& a, bool decode, hipStream_t s) {
+  switch (a.K) {
+    case 1: return decode ? decode_k<TI, 1>(a, s) : prompt_k<TI, 1>(a, s);
+    case 2: return decode ? decode_k<TI, 2>(a, s) : prompt_k<TI, 2>(a, s);
+    case 3: return decode ? decode_k<TI, 3>(a, s) : prompt_k<TI, 3>(a, s);
+    case 4: return decode ? decode_k<TI, 4>(a, s) : prompt_k<TI, 4>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_conv_prompt(const ConvCarryArgs& a, int dtype, hipStream_t s) {
+  return dtype == 0 ? conv_t<float>(a, false, s) : conv_t<__bf16>(a, false, s);
+}
+
+hipError_t launch_conv_decode(const ConvCarryArgs& a, int dtype, hipStream_t s) {
+  if (a.N == 0) return hipSuccess;
+  return dtype == 0 ? conv_t<float>(a, true, s) : conv_t<__bf16>(a, true, s);
+}
+
+}  // namespace gdn

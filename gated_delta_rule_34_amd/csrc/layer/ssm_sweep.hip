@@ -1,0 +1,338 @@
+// ssm_sweep.hip -- the selective state space scan's sweep over a sequence's chunks, on gfx950:
+// outputs y and the state going forward in time, or dx and the state's adjoint going backward
+// (the formulas stand in ssm_common.h).
+//
+// One workgroup per (sequence, segment, head, 64 columns of x): four waves, each with 16 columns of
+// the state in its accumulators; columns of the state never mix. Per chunk the products K Q^T, M X,
+// S^T Q and K^T (w X) run on the matrix cores; every product is formed transposed, so that a lane
+// holds four adjacent columns of one token. The next chunk's rows are in registers while a chunk is
+// computed.
+//
+// Few sequences and heads leave compute units idle over a long serial chain, so a sequence is then
+// cut into S segments: a first launch runs the state alone over all segments but the last, from
+// zero, and the second starts each segment from the earlier segments' states and decays.
+#include "ssm_common.h"
+
+namespace gdn {
+
+struct SweepArgs {
+  int N, Hk, Hv, r, Dv, nslab, S, T, xcd;
+  int64_t T_total;
+  const int* cu;
+  const void *k, *q, *x;  // the vectors that write and that read the state, the values
+  int64_t k_rs, q_rs, x_rs, o_rs;
+  void* o;
+  const float *dt, *a_log, *dt_bias, *d_skip;
+  const float* s0;  // [N][Hv][Dk][Dv] or nullptr
+  float* st;        // final state, or nullptr
+  float* sv;        // the state before each chunk [slot][Hv][Dk][Dv], or nullptr
+  float* loc;       // segments' states from zero, in the accumulators' order
+  float* dec;       // [N][S][Hv] decay over each segment
+};
+
+// Gate rows in LDS: gamma and its remainder, the weight of an input inside the chunk, the decays
+// with which a token reads and writes the state, the weight of an output.
+enum { G_HI, G_LO, G_IN, G_RD, G_WR, G_OUT, G_ROWS };
+
+template <typename TI, int DK, bool REV, bool OUT>
+__global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
+  constexpr int NDT = DK / 16, KSD = ks_of<TI, DK>(), NSD = DK / KSD, KSC = ks_of<TI, SC>(), NSC = SC / KSC;
+  constexpr int NS = ssm_split<TI>(), TRI = REV ? TRI_UP : TRI_LOW;
+  using LK = Swz<TI, DK, true>;
+  using LX = Swz<TI, SP, true>;
+  using LM = Swz<TI, SC, false>;
+  __shared__ __align__(16) TI sK[SC * DK];
+  __shared__ __align__(16) TI sQ[OUT ? SC * DK : 8];
+  __shared__ __align__(16) TI sX[SC * SP];
+  __shared__ __align__(16) TI sM[OUT ? SC * SC : 8];
+  __shared__ __align__(16) float sg[2][G_ROWS][SC];
+  __shared__ float sbn[2];
+
+  const int segs = OUT ? a.S : a.S - 1;
+  int grp, mem;
+  if (a.xcd) {
+    if (!xcd_group(blockIdx.x, a.N * segs * a.Hk, a.r * a.nslab, grp, mem)) return;
+  } else {
+    grp = blockIdx.x / (a.r * a.nslab);
+    mem = blockIdx.x % (a.r * a.nslab);
+  }
+  const int kh = grp % a.Hk, sgm = (grp / a.Hk) % segs, n = grp / a.Hk / segs;
+  const int h = kh * a.r + mem / a.nslab, slab = mem % a.nslab;
+  const int w = wave_id(), l = lane_id(), g = l >> 4, r = l & 15;
+  const int col0 = slab * SP + 16 * w;  // this wave's columns of the head
+  const bool cols = col0 < a.Dv;        // (a head of 16 or 32 leaves waves without columns)
+  const int ncols = a.Dv - slab * SP < SP ? a.Dv - slab * SP : SP;
+
+  int64_t lo, hi;
+  ssm_seq(a.cu, a.T, a.T_total, n, lo, hi);
+  const int nch = (int)((hi - lo + SC - 1) / SC), cps = (nch + a.S - 1) / a.S;
+  const int k0 = min(nch, sgm * cps), k1 = min(nch, k0 + cps);
+
+  const float neg_a = -expf(a.a_log[h]) * kLog2e, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  const float dsk = a.d_skip ? a.d_skip[h] : 0.f;
+  const TI* kp = (const TI*)a.k + kh * DK;
+  const TI* qp = (const TI*)a.q + kh * DK;
+  const TI* xp = (const TI*)a.x + (int64_t)h * a.Dv + slab * SP;
+
+  // the state: tile t holds rows 16 t + 4 g + e of column col0 + r
+  f32x4 S[NDT];
+#pragma unroll
+  for (int t = 0; t < NDT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int64_t nh = (int64_t)n * a.Hv + h;
+  if constexpr (OUT) {
+    if (a.s0 && cols) {
+      const float* s0 = a.s0 + nh * DK * a.Dv + col0 + r;
+#pragma unroll
+      for (int t = 0; t < NDT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[t][e] = s0[(int64_t)(16 * t + 4 * g + e) * a.Dv];
+    }
+    for (int j = 0; j < sgm; ++j) {
+      const int64_t nj = ((int64_t)n * a.S + j) * a.Hv + h;
+      const float d = a.dec[nj];
+      const f32x4* p = reinterpret_cast<const f32x4*>(a.loc) + ((nj * a.nslab + slab) * NDT) * 256 + threadIdx.x;
+#pragma unroll
+      for (int t = 0; t < NDT; ++t) S[t] = d * S[t] + p[t * 256];
+    }
+    for (int i = threadIdx.x; i < SC * SC; i += 256) sM[i] = (TI)0.f;  // the tiles past the diagonal stay zero
+  }
+  float dec = 1.f;
+
+  auto chunk = [&](int k) { return REV ? nch - 1 - k : k; };
+  auto clen = [&](int c) { const int64_t rest = hi - lo - (int64_t)c * SC; return (int)(rest < SC ? rest : SC); };
+  TileRegs<TI, DK, LK> rk, rq;
+  TileRegs<TI, SP, LX> rx;
+  float rdt = 0.f;  // the last wave: dt of the chunk after the loaded one
+  auto load = [&](int k) {
+    const int c = chunk(k), len = clen(c);
+    const int64_t t0 = lo + (int64_t)c * SC;
+    rk.template load<false>(kp + t0 * a.k_rs, a.k_rs, len, DK);
+    if constexpr (OUT) rq.template load<false>(qp + t0 * a.q_rs, a.q_rs, len, DK);
+    rx.template load<true>(xp + t0 * a.x_rs, a.x_rs, len, ncols);
+  };
+  auto load_dt = [&](int k) {
+    const int c = chunk(k);
+    rdt = l < clen(c) ? a.dt[(lo + (int64_t)c * SC + l) * a.Hv + h] : 0.f;
+  };
+  auto gates = [&](int k, int buf) {
+    const bool valid = l < clen(chunk(k));
+    const Gate q = chunk_gate(rdt, bias, neg_a, valid);
+    const float hi32 = (float)q.gam, eb = exp2f(hi32), ee = exp2f((float)(q.tot - q.gam));
+    sg[buf][G_HI][l] = hi32;
+    sg[buf][G_LO][l] = (float)(q.gam - (double)hi32);
+    sg[buf][G_IN][l] = REV ? (valid ? 1.f : 0.f) : q.step;
+    sg[buf][G_RD][l] = REV ? ee : eb;
+    sg[buf][G_WR][l] = REV ? (valid ? eb : 0.f) : ee * q.step;
+    sg[buf][G_OUT][l] = REV ? q.step : 1.f;
+    if (l == 63) sbn[buf] = exp2f((float)q.tot);
+  };
+
+  if (k0 < k1) {
+    load(k0);
+    if (w == 3) {
+      load_dt(k0);
+      gates(k0, k0 & 1);
+      if (k0 + 1 < k1) load_dt(k0 + 1);
+    }
+  }
+  for (int k = k0; k < k1; ++k) {
+    const int buf = k & 1, c = chunk(k), len = clen(c);
+    const int64_t t0 = lo + (int64_t)c * SC;
+    rk.store(sK);
+    if constexpr (OUT) rq.store(sQ);
+    rx.store(sX);
+    __syncthreads();  // the chunk's rows and gates are in LDS
+    if (k + 1 < k1) load(k + 1);
+    const float(*gt)[SC] = sg[buf];
+    const float bn = sbn[buf];
+    f32x4 o[4];
+    if constexpr (OUT) {
+      if (a.sv && cols) {
+        float* sv = a.sv + ((lo / SC + n + c) * a.Hv + h) * (int64_t)DK * a.Dv + col0 + r;
+#pragma unroll
+        for (int t = 0; t < NDT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sv[(int64_t)(16 * t + 4 * g + e) * a.Dv] = S[t][e];
+      }
+      // M = Gamma o (Q K^T) o inputs' weights: its ten tiles dealt over the waves
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        const int idx = w + 4 * u;
+        if (idx >= 10) continue;
+        const int big = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, small = idx - big * (big + 1) / 2;
+        const int it = REV ? small : big, jt = REV ? big : small;
+        f32x4 m = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < NSD; ++s)
+          m = Mf<TI, KSD>::run(ld_n<TI, KSD, STD, LK>(sK, 16 * jt, s), ld_n<TI, KSD, STD, LK>(sQ, 16 * it, s), m);
+        const int i = 16 * it + r, j0 = 16 * jt + 4 * g;
+        const float ih = gt[G_HI][i], il = gt[G_LO][i];
+        const f32x4 jh = ld4(&gt[G_HI][j0]), jl = ld4(&gt[G_LO][j0]), wi = ld4(&gt[G_IN][j0]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float d = REV ? (jh[e] - ih) + (jl[e] - il) : (ih - jh[e]) + (il - jl[e]);
+          const bool in = REV ? i <= j0 + e : i >= j0 + e;
+          m[e] = in ? m[e] * exp2f(d) * wi[e] : 0.f;
+        }
+        st4<TI>(sM + LM::at(i, j0), m);
+      }
+      // S^T Q, decayed
+#pragma unroll
+      for (int t = 0; t < 4; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (cols) {
+#pragma unroll
+        for (int s = 0; s < NSD; ++s) {
+          FragT<TI, KSD> sf[1];
+          acc_split<TI, KSD, 1>(S, s, sf);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) o[t] = Mf<TI, KSD>::run(sf[0], ld_n<TI, KSD, ACC, LK>(sQ, 16 * t, s), o[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) o[t] *= gt[G_RD][16 * t + r];
+      }
+    }
+    if (w == 3 && k + 1 < k1) {  // the next chunk's gates
+      gates(k + 1, buf ^ 1);
+      if (k + 2 < k1) load_dt(k + 2);
+    }
+    if constexpr (OUT) __syncthreads();  // M is complete
+    if (cols) {
+#pragma unroll
+      for (int t = 0; t < NDT; ++t) S[t] *= bn;
+#pragma unroll
+      for (int s = 0; s < NSC; ++s) {
+        const FragT<TI, KSC> xf = ld_t<TI, KSC, STD, LX>(sX, 16 * w, s);
+        if constexpr (OUT) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            if (!tri_skip<TRI, KSC>(s, t)) o[t] = Mf<TI, KSC>::run(xf, ld_n<TI, KSC, STD, LM>(sM, 16 * t, s), o[t]);
+        }
+        FragT<TI, KSC> u[NS];
+        scale_split<TI, KSC, NS>(xf, gt[G_WR], s, u);
+#pragma unroll
+        for (int t = 0; t < NDT; ++t) {
+          const FragT<TI, KSC> kf = ld_t<TI, KSC, STD, LK>(sK, 16 * t, s);
+#pragma unroll
+          for (int m = NS - 1; m >= 0; --m) S[t] = Mf<TI, KSC>::run(kf, u[m], S[t]);
+        }
+      }
+      if constexpr (OUT) {
+        TI* op = (TI*)a.o + t0 * a.o_rs + (int64_t)h * a.Dv + col0 + 4 * g;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int i = 16 * t + r;
+          if (i < len)
+            st4<TI>(op + (int64_t)i * a.o_rs, o[t] * gt[G_OUT][i] + dsk * ld4<TI>(sX + LX::at(i, 16 * w + 4 * g)));
+        }
+      }
+    }
+    dec *= bn;
+    __syncthreads();  // LDS is free for the next chunk
+  }
+  if constexpr (OUT) {
+    if (a.st && cols && sgm == a.S - 1) {
+      float* st = a.st + nh * DK * a.Dv + col0 + r;
+#pragma unroll
+      for (int t = 0; t < NDT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[(int64_t)(16 * t + 4 * g + e) * a.Dv] = S[t][e];
+    }
+  } else {
+    const int64_t nj = ((int64_t)n * a.S + sgm) * a.Hv + h;
+    f32x4* p = reinterpret_cast<f32x4*>(a.loc) + ((nj * a.nslab + slab) * NDT) * 256 + threadIdx.x;
+#pragma unroll
+    for (int t = 0; t < NDT; ++t) p[t * 256] = S[t];
+    if (slab == 0 && threadIdx.x == 0) a.dec[nj] = dec;
+  }
+}
+
+// Segments per sequence: enough workgroups for the chip, each with at least kMinChunks chunks on
+// average (a segment costs its states and a second read of its rows).
+constexpr int kWantGroups = 512, kMinChunks = 4, kMaxSegments = 32;
+static int ssm_segments(const SsmArgs& a) {
+  if (a.N == 0) return 1;
+  const int64_t groups = (int64_t)a.N * a.Hv * ((a.Dv + SP - 1) / SP);
+  int64_t s = kWantGroups / groups;
+  const int64_t most = a.T_total / SC / a.N / kMinChunks;
+  if (s > most) s = most;
+  if (s > kMaxSegments) s = kMaxSegments;
+  return s < 1 ? 1 : (int)s;
+}
+
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+static size_t seg_bytes(const SsmArgs& a) {
+  const int S = ssm_segments(a);
+  if (S == 1) return 0;
+  const size_t u = (size_t)a.N * S * a.Hv;
+  return up256(u * ((a.Dv + SP - 1) / SP) * a.Dk * SP * 4) + up256(u * 4);
+}
+size_t ssm_saved_bytes(const SsmArgs& a) { return (size_t)ssm_slots(a.T_total, a.N) * a.Hv * a.Dk * a.Dv * 4; }
+size_t ssm_fwd_ws_bytes(const SsmArgs& a) { return seg_bytes(a); }
+
+template <typename TI, int DK, bool REV> static hipError_t sweep_go(const SsmArgs& a, float* sv, float* seg, hipStream_t s) {
+  SweepArgs v{};
+  v.N = a.N; v.Hk = a.Hk; v.Hv = a.Hv; v.r = a.r; v.Dv = a.Dv; v.T = a.T; v.T_total = a.T_total; v.cu = a.cu;
+  v.nslab = (a.Dv + SP - 1) / SP;
+  v.S = ssm_segments(a);
+  v.k = REV ? a.c : a.b; v.k_rs = REV ? a.c_rs : a.b_rs;
+  v.q = REV ? a.b : a.c; v.q_rs = REV ? a.b_rs : a.c_rs;
+  v.x = REV ? a.dy : a.x; v.x_rs = REV ? a.dy_rs : a.x_rs;
+  v.o = REV ? a.dx : a.y; v.o_rs = REV ? a.dx_rs : a.y_rs;
+  v.dt = a.dt; v.a_log = a.a_log; v.dt_bias = a.dt_bias; v.d_skip = a.d_skip;
+  v.s0 = REV ? a.dST : a.S0;
+  v.st = REV ? a.dS0 : a.ST;
+  v.sv = sv;
+  v.loc = seg;
+  v.dec = seg + (v.S > 1 ? up256((size_t)a.N * v.S * a.Hv * v.nslab * DK * SP * 4) / 4 : 0);
+  // A group's heads share b and c: with many groups they go to one XCD (workgroups are dealt to
+  // the eight XCDs in turn) and share its L2; few groups would leave XCDs idle.
+  auto grid = [&](int segs) {
+    const int G = a.N * segs * a.Hk, m = a.r * v.nslab;
+    v.xcd = G >= 32;
+    return v.xcd ? xcd_grid(G, m) : G * m;
+  };
+  if (v.S > 1) {
+    const int b = grid(v.S - 1);
+    traced(REV ? "k_ssm_state_rev" : "k_ssm_state", s, [&] { k_ssm_sweep<TI, DK, REV, false><<<b, 256, 0, s>>>(v); });
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int b = grid(v.S);
+  traced(REV ? "k_ssm_sweep_rev" : "k_ssm_sweep", s, [&] { k_ssm_sweep<TI, DK, REV, true><<<b, 256, 0, s>>>(v); });
+  return hipGetLastError();
+}
+
+template <typename TI, bool REV> static hipError_t sweep_d(const SsmArgs& a, float* sv, float* seg, hipStream_t s) {
+  switch (a.Dk) {
+    case 16: return sweep_go<TI, 16, REV>(a, sv, seg, s);
+    case 32: return sweep_go<TI, 32, REV>(a, sv, seg, s);
+    case 64: return sweep_go<TI, 64, REV>(a, sv, seg, s);
+    case 128: return sweep_go<TI, 128, REV>(a, sv, seg, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_ssm_forward(const SsmArgs& a, int dtype, hipStream_t s) {
+  return dtype == 0 ? sweep_d<float, false>(a, a.sv, a.ws, s) : sweep_d<__bf16, false>(a, a.sv, a.ws, s);
+}
+
+// Backward workspace: the adjoints at the chunks' ends, the parameters' partials, the segments.
+size_t ssm_bwd_ws_bytes(const SsmArgs& a) {
+  return up256(ssm_saved_bytes(a)) + up256((size_t)ssm_slots(a.T_total, a.N) * 3 * a.Hv * 4) + seg_bytes(a);
+}
+
+hipError_t launch_ssm_backward(const SsmArgs& a, int dtype, hipStream_t s) {
+  float* ds = a.ws;
+  float* part = ds + up256(ssm_saved_bytes(a)) / 4;
+  float* seg = part + up256((size_t)ssm_slots(a.T_total, a.N) * 3 * a.Hv * 4) / 4;
+  hipError_t e = hipSuccess;
+  if (a.N > 0) {
+    e = dtype == 0 ? sweep_d<float, true>(a, ds, seg, s) : sweep_d<__bf16, true>(a, ds, seg, s);
+    if (e == hipSuccess && ssm_slots(a.T_total, a.N) > 0) e = launch_ssm_grad(a, dtype, ds, part, s);
+  }
+  if (e == hipSuccess && (a.da_log || a.ddt_bias || a.dd_skip))
+    e = launch_colsum(part, ssm_slots(a.T_total, a.N), a.Hv, ColsumOut{{a.da_log, a.ddt_bias, a.dd_skip}}, 3, s);
+  return e;
+}
+
+}  // namespace gdn

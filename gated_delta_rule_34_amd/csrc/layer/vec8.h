@@ -1,0 +1,76 @@
+// vec8.h -- eight adjacent values of a row (one 16-byte bf16 piece, two float32 ones) as float32.
+#pragma once
+#include "../gdn_frag.h"
+#include "../gdn_internal.h"
+#include "layer_internal.h"
+
+namespace gdn {
+
+struct F8 {
+  float v[8];
+};
+
+template <typename TI> struct Raw8 {
+  f32x4 a, b;
+};
+template <> struct Raw8<__bf16> {
+  i32x4 a;
+};
+
+// Eight values as stored (converted at their use, so that a load in flight is not waited for).
+// NT: non-temporal, for rows that are read once.
+template <bool NT, typename TI> __device__ __forceinline__ Raw8<TI> ldraw8(const TI* p) {
+  Raw8<TI> r;
+  if constexpr (sizeof(TI) == 2) {
+    const i32x4* q = reinterpret_cast<const i32x4*>(p);
+    r.a = NT ? __builtin_nontemporal_load(q) : *q;
+  } else {
+    const f32x4* q = reinterpret_cast<const f32x4*>(p);
+    r.a = NT ? __builtin_nontemporal_load(q) : q[0];
+    r.b = NT ? __builtin_nontemporal_load(q + 1) : q[1];
+  }
+  return r;
+}
+
+template <typename TI> __device__ __forceinline__ F8 cvt8(const Raw8<TI>& x) {
+  F8 r;
+  if constexpr (sizeof(TI) == 2) {
+    const bf16x8 b = __builtin_bit_cast(bf16x8, x.a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.v[i] = (float)b[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.v[i] = x.a[i];
+      r.v[4 + i] = x.b[i];
+    }
+  }
+  return r;
+}
+
+template <typename TI> __device__ __forceinline__ F8 ld8(const TI* p) { return cvt8<TI>(ldraw8<false, TI>(p)); }
+
+template <typename TI> __device__ __forceinline__ void st8(TI* p, const F8& x) {
+  if constexpr (sizeof(TI) == 2) {
+    bf16x8 y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = (__bf16)x.v[i];
+    *reinterpret_cast<bf16x8*>(p) = y;
+  } else {
+    *reinterpret_cast<f32x4*>(p) = f32x4{x.v[0], x.v[1], x.v[2], x.v[3]};
+    *reinterpret_cast<f32x4*>(p + 4) = f32x4{x.v[4], x.v[5], x.v[6], x.v[7]};
+  }
+}
+
+__device__ __forceinline__ F8 zero8() { return F8{{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}}; }
+
+// 1 / (1 + e^-z) with the hardware reciprocal and exponential (about 1 ulp each; 0 where e^-z
+// overflows, NaN for NaN).
+__device__ __forceinline__ float sigmoidf(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
+
+// The step of the scan: softplus(z), z itself past 20 (where they agree to float32).
+__device__ __forceinline__ float softplusf(float z) { return z > 20.f ? z : log1pf(expf(z)); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+}  // namespace gdn

@@ -1,0 +1,155 @@
+"""GPU: conv1d + SiLU with a carried window (prompts and single tokens) against the float64 oracle.
+
+Tolerance, per element: the result's rounding (half a step of the type) and some 16 float32 roundings
+of the window's products (SiLU's slope is below 1.1). The carried rows are copies: equal."""
+import numpy as np
+import pytest
+
+from layer_gpu import HALF, cu_of, dev, host, rounded, torch_dtype
+
+pytestmark = pytest.mark.gpu
+
+
+def make(lens, ch, K, dtype, seed, bias=True, first=True):
+    rng = np.random.default_rng(seed)
+    T, N = sum(lens), len(lens)
+    return dict(x=rounded(rng.standard_normal((T, ch)), dtype), w=rounded(rng.uniform(-1, 1, (ch, K)), "f32"),
+                bias=rounded(rng.standard_normal(ch), "f32") if bias else None,
+                first=rounded(rng.standard_normal((N, K - 1, ch)), dtype) if first else None)
+
+
+def size_of(a, cu):
+    """Sum of the window's |products| per output."""
+    from oracle import layer as L
+
+    ab = {k: None if v is None else np.abs(v) for k, v in a.items()}
+    K = a["w"].shape[1]
+    out = np.zeros(a["x"].shape)
+    for n in range(len(cu) - 1):
+        head = np.zeros((K - 1, out.shape[1])) if ab["first"] is None else ab["first"][n]
+        ext = np.concatenate([head, ab["x"][cu[n]:cu[n + 1]]])
+        for t in range(cu[n + 1] - cu[n]):
+            out[cu[n] + t] = (ab["w"].T * ext[t:t + K]).sum(0)
+    return out + (0.0 if ab["bias"] is None else ab["bias"])
+
+
+def check(y, want, size, dtype):
+    tol = HALF[dtype] * np.abs(want) + 16 * 2.0 ** -24 * (size + 1e-30) * 1.1
+    assert (np.abs(y - want) <= tol).all(), float(np.max(np.abs(y - want) / tol))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+@pytest.mark.parametrize("bias,first", [(True, True), (False, False)])
+def test_prompt(dtype, K, bias, first):
+    """Lengths below the window, one, none, around a thread's run of rows; 296 channels leave lanes idle;
+    x and y are views of wider rows."""
+    import torch
+    import gated_delta_rule_34_amd as G
+    from oracle import layer as L
+
+    lens = [1, 0, 2, 3, 33, 32, 64, 70, 1]
+    a, cu = make(lens, 296, K, dtype, 30 + K, bias, first), cu_of(lens)
+    want, last_want = L.conv_prompt(cu, *a.values())
+    wide = torch.full((sum(lens), 296 + 24), float("nan"), dtype=torch_dtype(dtype), device="cuda")
+    x, y = wide[:, 8:304], torch.full_like(wide, 7.0)[:, :296]
+    x.copy_(dev(a["x"], dtype))
+    p = G.make_conv_problem(len(lens), sum(lens), 296, K, cu_seqlens=(t := torch.tensor(cu, dtype=torch.int32, device="cuda")), dtype=dtype)
+    last = torch.empty(len(lens), K - 1, 296, dtype=torch_dtype(dtype), device="cuda")
+    G.gdn_conv1d_silu_prompt(p, x, dev(a["w"]), dev(a["bias"]), dev(a["first"], dtype), y, last)
+    check(host(y), want, size_of(a, cu), dtype)
+    assert np.array_equal(host(last), last_want)
+    again = torch.empty_like(y)
+    G.gdn_conv1d_silu_prompt(p, x, dev(a["w"]), dev(a["bias"]), dev(a["first"], dtype), again, None)
+    assert torch.equal(again, y) and t is not None
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ch", [8, 2056])
+def test_parts_and_tokens_are_the_whole(dtype, ch):
+    """A prompt in three parts (the second shorter than the window), then single tokens, is the whole
+    prompt, bit for bit; equal lengths without cu_seqlens."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    a = make([60, 60], ch, 4, dtype, 5)
+    x, w, bias, first = dev(a["x"], dtype), dev(a["w"]), dev(a["bias"]), dev(a["first"], dtype)
+    whole, end = torch.empty_like(x), torch.empty_like(first)
+    G.gdn_conv1d_silu_prompt(G.make_conv_problem(2, 120, ch, 4, T=60, dtype=dtype), x, w, bias, first, whole, end)
+    x2, w2 = x.view(2, 60, ch), whole.view(2, 60, ch)
+    at, win = 0, first
+    for n in (35, 2, 20):
+        part, y, nxt = x2[:, at:at + n].reshape(-1, ch), torch.empty(2 * n, ch, dtype=x.dtype, device="cuda"), torch.empty_like(win)
+        G.gdn_conv1d_silu_prompt(G.make_conv_problem(2, 2 * n, ch, 4, T=n, dtype=dtype), part, w, bias, win, y, nxt)
+        assert torch.equal(y.view(2, n, ch), w2[:, at:at + n])
+        at, win = at + n, nxt
+    pool = torch.full((5, 3, ch), 9.0, dtype=x.dtype, device="cuda")
+    slots = torch.tensor([4, 1], dtype=torch.int32, device="cuda")
+    pool[[4, 1]] = win
+    p = G.make_conv_problem(2, 2, ch, 4, T=1, dtype=dtype)
+    for t in range(at, 60):
+        y = torch.empty(2, ch, dtype=x.dtype, device="cuda")
+        G.gdn_conv1d_silu_decode(p, x2[:, t].contiguous(), w, bias, pool, slots, y)
+        check(host(y), host(w2[:, t]), 8.0, dtype)
+    assert torch.equal(pool[[4, 1]], end) and bool((pool[[0, 2, 3]] == 9.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+def test_token(dtype, K):
+    import torch
+    import gated_delta_rule_34_amd as G
+    from oracle import layer as L
+
+    N, ch, slots = 11, 520, 14
+    a = make([1] * N, ch, K, dtype, 60 + K)
+    rng = np.random.default_rng(2)
+    idx = rng.permutation(slots)[:N]
+    pool = rounded(rng.standard_normal((slots, K - 1, ch)), dtype)
+    a["first"] = pool[idx]
+    want, last = L.conv_prompt(cu_of([1] * N), *a.values())
+    use = idx.copy()
+    use[2] = -3
+    if K > 1:
+        use[7] = slots
+    state, y = dev(pool, dtype), torch.full((N, ch), 7.0, dtype=torch_dtype(dtype), device="cuda")
+    p = G.make_conv_problem(N, N, ch, K, T=1, dtype=dtype)
+    G.gdn_conv1d_silu_decode(p, dev(a["x"], dtype), dev(a["w"]), dev(a["bias"]), state, torch.from_numpy(use.astype(np.int32)).cuda(), y)
+    live = [i for i in range(N) if use[i] == idx[i]]
+    check(host(y)[live], want[live], size_of(a, cu_of([1] * N))[live], dtype)
+    dead = [i for i in range(N) if i not in live]
+    assert bool((y[dead] == 7.0).all())
+    got = host(state)
+    assert np.array_equal(got[idx[live]], last[live])
+    rest = [s for s in range(slots) if s not in set(idx[live])]
+    assert np.array_equal(got[rest], pool[rest])
+
+
+def test_rows_of_no_sequence_and_malformed_tables():
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    a = make([40, 30], 64, 4, "bf16", 3)
+    x, w, first = dev(a["x"], "bf16"), dev(a["w"]), dev(a["first"], "bf16")
+    x[50:] = float("nan")
+    cu = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    for table in (cu(0, 20, 50), cu(0, 500, 70), cu(60, 20, 70), cu(-5, 20, 50), cu(0, 70, 20), cu(70, 0, -70)):
+        y, last = torch.full_like(x, 7.0), torch.empty_like(first)
+        G.gdn_conv1d_silu_prompt(G.make_conv_problem(2, 70, 64, 4, cu_seqlens=table), x, w, None, first, y, last)
+        if table.tolist() == [0, 20, 50]:
+            assert bool(torch.isfinite(y[:50]).all()) and bool((y[50:] == 7.0).all()) and torch.equal(last[1], x[47:50])
+
+
+def test_offsets_past_32_bits():
+    """Rows 40000 apart over more than 2^31 elements: the last rows are those of a call on them alone."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    rows, wide = 55000, 40000
+    big = torch.zeros(rows, wide, dtype=torch.bfloat16, device="cuda")
+    big[-40:, :64] = torch.randn(40, 64, device="cuda")
+    w = torch.randn(64, 4, device="cuda")
+    G.gdn_conv1d_silu_prompt(G.make_conv_problem(1, rows, 64, 4, T=rows), big[:, :64], w, None, None, big[:, 64:128], None)
+    alone = torch.empty(40, 64, dtype=torch.bfloat16, device="cuda")
+    G.gdn_conv1d_silu_prompt(G.make_conv_problem(1, 40, 64, 4, T=40), big[-40:, :64].contiguous(), w, None, None, alone, None)
+    assert torch.equal(big[-40:, 64:128], alone) and bool((alone != 0).any())

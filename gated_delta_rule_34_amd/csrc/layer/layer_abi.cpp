@@ -93,13 +93,20 @@ gdn::SsmArgs ssm_args(const gdn_ssm_problem* p) {
   return a;
 }
 
+// A row view of the scan: its kernels address the 64 rows of a chunk with 31-bit byte offsets.
+gdn_status ssm_view(const void* v, int64_t rs, int64_t width, int dtype, int64_t rows) {
+  // 64 rows of 2^23 - 1 float32 values span less than 2^31 bytes
+  if (rows > 0 && rs * esize(dtype) >= (int64_t)1 << 25) return GDN_EINVAL;
+  return check_view(v, rs, width, dtype, rows);
+}
+
 // The views x, b, c and dt that every scan call reads.
 gdn_status ssm_inputs(const gdn_ssm_problem* p, const void* x, int64_t x_rs, const void* b, int64_t b_rs,
                       const void* c, int64_t c_rs, const float* dt, gdn::SsmArgs& a) {
   const int64_t xw = (int64_t)p->Hv * p->Dv, kw = (int64_t)p->Hk * p->Dk;
-  GDN_TRY(check_view(x, x_rs, xw, p->dtype, p->T_total));
-  GDN_TRY(check_view(b, b_rs, kw, p->dtype, p->T_total));
-  GDN_TRY(check_view(c, c_rs, kw, p->dtype, p->T_total));
+  GDN_TRY(ssm_view(x, x_rs, xw, p->dtype, p->T_total));
+  GDN_TRY(ssm_view(b, b_rs, kw, p->dtype, p->T_total));
+  GDN_TRY(ssm_view(c, c_rs, kw, p->dtype, p->T_total));
   GDN_TRY(check_arr(dt, p->T_total > 0));
   a.x = x; a.x_rs = x_rs; a.b = b; a.b_rs = b_rs; a.c = c; a.c_rs = c_rs; a.dt = dt;
   return GDN_OK;
@@ -195,7 +202,7 @@ gdn_status gdn_ssm_fwd(const gdn_ssm_problem* p, const void* x, int64_t x_rs, co
   GDN_TRY(check_ssm(p));
   gdn::SsmArgs a = ssm_args(p);
   GDN_TRY(ssm_inputs(p, x, x_rs, b, b_rs, c, c_rs, dt, a));
-  GDN_TRY(check_view(y, y_rs, (int64_t)p->Hv * p->Dv, p->dtype, p->T_total));
+  GDN_TRY(ssm_view(y, y_rs, (int64_t)p->Hv * p->Dv, p->dtype, p->T_total));
   GDN_TRY(check_arr(S0, false, 16));
   GDN_TRY(check_arr(S_T, false, 16));
   if (S0 && S0 == S_T) return GDN_EINVAL;  // they must not overlap
@@ -217,10 +224,10 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_problem* p, const void* x, int64_t x_rs, co
   gdn::SsmArgs a = ssm_args(p);
   GDN_TRY(ssm_inputs(p, x, x_rs, b, b_rs, c, c_rs, dt, a));
   const int64_t xw = (int64_t)p->Hv * p->Dv, kw = (int64_t)p->Hk * p->Dk;
-  GDN_TRY(check_view(dy, dy_rs, xw, p->dtype, p->T_total));
-  GDN_TRY(check_view(dx, dx_rs, xw, p->dtype, p->T_total));
-  GDN_TRY(check_view(db, db_rs, kw, p->dtype, p->T_total));
-  GDN_TRY(check_view(dc, dc_rs, kw, p->dtype, p->T_total));
+  GDN_TRY(ssm_view(dy, dy_rs, xw, p->dtype, p->T_total));
+  GDN_TRY(ssm_view(dx, dx_rs, xw, p->dtype, p->T_total));
+  GDN_TRY(ssm_view(db, db_rs, kw, p->dtype, p->T_total));
+  GDN_TRY(ssm_view(dc, dc_rs, kw, p->dtype, p->T_total));
   GDN_TRY(check_arr(ddt, p->T_total > 0));
   GDN_TRY(check_arr(da_log, false));
   GDN_TRY(check_arr(ddt_bias, false));

@@ -88,27 +88,50 @@ template <typename TI> __device__ __forceinline__ void st4(TI* p, f32x4 v) {
     *reinterpret_cast<f32x4*>(p) = v;
 }
 
+// Raw buffer resource over [base, base + bytes), base and bytes wave-uniform: loads at or past `bytes`
+// give zeros and stores there are dropped, without a branch.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32 |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
+}
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every resource (64 rows span less than 2^31 bytes)
+template <bool NT> __device__ __forceinline__ i32x4 buf_ld16(__amdgpu_buffer_rsrc_t rs, uint32_t voff) {
+  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)voff, 0, NT ? 2 : 0));
+}
+template <typename TI> __device__ __forceinline__ void buf_st4(__amdgpu_buffer_rsrc_t rs, uint32_t voff, f32x4 v) {
+  if constexpr (sizeof(TI) == 2) {
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64(
+        __builtin_bit_cast(u2, bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]}), rs, (int)voff, 0, 0);
+  } else {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), rs, (int)voff, 0, 0);
+  }
+}
+
 // A [64][CN] tile of rows on its way through registers into LDS, by 256 threads. Rows at or past
 // len and columns at or past ncols arrive as zeros; nothing outside the caller's rows is read.
 template <typename TI, int CN, class L> struct TileRegs {
-  static constexpr int CE = 16 / (int)sizeof(TI), PPR = CN / CE, TOT = SC * PPR, U = (TOT + 255) / 256;
+  static constexpr int CE = 16 / (int)sizeof(TI), PPR = CN / CE, TOT = SC * PPR, U = (TOT + 255) / 256, STEP = 256 / PPR;
   i32x4 v[U];
-  template <bool NT> __device__ __forceinline__ void load(const TI* src, int64_t rs, int len, int ncols) {
+  uint32_t rsb, voff;  // row stride in bytes, this thread's first piece
+  __device__ __forceinline__ void init(int64_t rs, int ncols) {
+    const int q = (int)threadIdx.x, c = (q % PPR) * CE;
+    rsb = (uint32_t)rs * (uint32_t)sizeof(TI);
+    voff = q < TOT && c < ncols ? (uint32_t)(q / PPR) * rsb + c * (int)sizeof(TI) : kNowhere;
+  }
+  template <bool NT> __device__ __forceinline__ void load(const TI* src, int len) {
+    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(src, (uint32_t)len * rsb);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int q = u * 256 + (int)threadIdx.x, row = q / PPR, c = (q % PPR) * CE;
-      v[u] = i32x4{0, 0, 0, 0};
-      if (q < TOT && row < len && c < ncols) {
-        const i32x4* p = reinterpret_cast<const i32x4*>(src + (int64_t)row * rs + c);
-        v[u] = NT ? __builtin_nontemporal_load(p) : *p;
-      }
-    }
+    for (int u = 0; u < U; ++u) v[u] = buf_ld16<NT>(rs, voff + (uint32_t)(u * STEP) * rsb);
   }
   __device__ __forceinline__ void store(TI* lds) const {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int q = u * 256 + (int)threadIdx.x;
-      if (q < TOT) *reinterpret_cast<i32x4*>(lds + L::at(q / PPR, (q % PPR) * CE)) = v[u];
+      if (TOT % 256 == 0 || q < TOT) *reinterpret_cast<i32x4*>(lds + L::at(q / PPR, (q % PPR) * CE)) = v[u];
     }
   }
 };
@@ -151,10 +174,10 @@ __device__ __forceinline__ Gate chunk_gate(float dt, float bias, float neg_a_log
   return q;
 }
 
-// Rows [lo, hi) of sequence n, clamped into [0, T_total].
+// Rows [lo, hi) of sequence n (wave-uniform), clamped into [0, T_total].
 __device__ __forceinline__ void ssm_seq(const int* cu, int T, int64_t T_total, int n, int64_t& lo, int64_t& hi) {
   if (cu) {
-    int64_t x = cu[n], y = cu[n + 1];
+    int64_t x = __builtin_amdgcn_readfirstlane(cu[n]), y = __builtin_amdgcn_readfirstlane(cu[n + 1]);
     x = x < 0 ? 0 : (x > T_total ? T_total : x);
     y = y < x ? x : (y > T_total ? T_total : y);
     lo = x;

@@ -67,14 +67,16 @@ __global__ __launch_bounds__(256, 2) void k_ssm_grad(GradArgs a) {
 
   {
     TileRegs<TI, DK, LK> rb, rc;
-    rb.template load<false>((const TI*)p.b + t0 * p.b_rs + kh * DK, p.b_rs, len, DK);
-    rc.template load<false>((const TI*)p.c + t0 * p.c_rs + kh * DK, p.c_rs, len, DK);
+    rb.init(p.b_rs, DK);
+    rc.init(p.c_rs, DK);
+    rb.template load<false>((const TI*)p.b + t0 * p.b_rs + kh * DK, len);
+    rc.template load<false>((const TI*)p.c + t0 * p.c_rs + kh * DK, len);
     for (int i = threadIdx.x; i < SC * SC; i += 256) sR[i] = (TI)0.f;
     for (int i = threadIdx.x; i < 4 * SC; i += 256) sE[i / SC][i % SC] = sF[i / SC][i % SC] = 0.f;
     rb.store(sB);
     rc.store(sC);
   }
-  __syncthreads();
+  lds_barrier();
   // this wave's tiles of the lower triangle: token tiles it >= jt; element e of a lane is (i, j) =
   // (16 it + r, 16 jt + 4 g + e)
   int it[3], jt[3];
@@ -109,9 +111,11 @@ __global__ __launch_bounds__(256, 2) void k_ssm_grad(GradArgs a) {
       const int ncols = p.Dv - slab * SP < SP ? p.Dv - slab * SP : SP;
       {
         TileRegs<TI, SP, LX> rx, ry;
-        rx.template load<true>((const TI*)p.x + t0 * p.x_rs + (int64_t)h * p.Dv + slab * SP, p.x_rs, len, ncols);
-        ry.template load<true>((const TI*)p.dy + t0 * p.dy_rs + (int64_t)h * p.Dv + slab * SP, p.dy_rs, len, ncols);
-        __syncthreads();  // the previous rows are used up
+        rx.init(p.x_rs, ncols);
+        ry.init(p.dy_rs, ncols);
+        rx.template load<true>((const TI*)p.x + t0 * p.x_rs + (int64_t)h * p.Dv + slab * SP, len);
+        ry.template load<true>((const TI*)p.dy + t0 * p.dy_rs + (int64_t)h * p.Dv + slab * SP, len);
+        lds_barrier();  // the previous rows are used up
         rx.store(sX);
         ry.store(sY);
       }
@@ -122,12 +126,12 @@ __global__ __launch_bounds__(256, 2) void k_ssm_grad(GradArgs a) {
         sh[buf][0][l] = h32;
         sh[buf][1][l] = (float)(q.gam - (double)h32);
         sh[buf][2][l] = q.step;
-        sh[buf][3][l] = exp2f(h32);
-        sh[buf][4][l] = exp2f((float)(q.tot - q.gam));
+        sh[buf][3][l] = __builtin_amdgcn_exp2f(h32);
+        sh[buf][4][l] = __builtin_amdgcn_exp2f((float)(q.tot - q.gam));
         sh[buf][5][l] = q.z;
-        if (l == 63) sbn[buf] = exp2f((float)q.tot);
+        if (l == 63) sbn[buf] = __builtin_amdgcn_exp2f((float)q.tot);
       }
-      __syncthreads();
+      lds_barrier();
 #pragma unroll
       for (int x = 0; x < DT; ++x) {
         // rows d = 16 dtile + r of both states, eight (or one) adjacent columns per step
@@ -193,7 +197,7 @@ __global__ __launch_bounds__(256, 2) void k_ssm_grad(GradArgs a) {
       float row = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float gm = i >= j0 + e ? exp2f((ih - jh[e]) + (il - jl[e])) : 0.f;
+        const float gm = i >= j0 + e ? __builtin_amdgcn_exp2f((ih - jh[e]) + (il - jl[e])) : 0.f;
         const float gq = i >= j0 + e ? gm * Q[u][e] : 0.f;
         R[u][e] += gq * st[e];
         float wv = gq * G[u][e];
@@ -242,7 +246,7 @@ __global__ __launch_bounds__(256, 2) void k_ssm_grad(GradArgs a) {
       sfr[w] = frob;
       sdd[w] = dd;
     }
-    __syncthreads();
+    lds_barrier();
     if (w == 0) {  // one token per lane
       const int ti = l >> 4;
       float row = 0.f, col = 0.f;
@@ -274,7 +278,7 @@ __global__ __launch_bounds__(256, 2) void k_ssm_grad(GradArgs a) {
 #pragma unroll
   for (int u = 0; u < 3; ++u)
     if (w + 4 * u < 10) st4<TI>(sR + LX::at(16 * it[u] + r, 16 * jt[u] + 4 * g), R[u]);
-  __syncthreads();
+  lds_barrier();
 #pragma unroll
   for (int s = 0; s < NSC; ++s) {
     FragT<TI, KSC> bf[DT], cf[DT];

@@ -102,13 +102,17 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
   auto clen = [&](int c) { const int64_t rest = hi - lo - (int64_t)c * SC; return (int)(rest < SC ? rest : SC); };
   TileRegs<TI, DK, LK> rk, rq;
   TileRegs<TI, SP, LX> rx;
+  rk.init(a.k_rs, DK);
+  if constexpr (OUT) rq.init(a.q_rs, DK);
+  rx.init(a.x_rs, ncols);
+  const uint32_t orow = (uint32_t)a.o_rs * (uint32_t)sizeof(TI);
   float rdt = 0.f;  // the last wave: dt of the chunk after the loaded one
   auto load = [&](int k) {
     const int c = chunk(k), len = clen(c);
     const int64_t t0 = lo + (int64_t)c * SC;
-    rk.template load<false>(kp + t0 * a.k_rs, a.k_rs, len, DK);
-    if constexpr (OUT) rq.template load<false>(qp + t0 * a.q_rs, a.q_rs, len, DK);
-    rx.template load<true>(xp + t0 * a.x_rs, a.x_rs, len, ncols);
+    rk.template load<false>(kp + t0 * a.k_rs, len);
+    if constexpr (OUT) rq.template load<false>(qp + t0 * a.q_rs, len);
+    rx.template load<true>(xp + t0 * a.x_rs, len);
   };
   auto load_dt = [&](int k) {
     const int c = chunk(k);
@@ -117,14 +121,14 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
   auto gates = [&](int k, int buf) {
     const bool valid = l < clen(chunk(k));
     const Gate q = chunk_gate(rdt, bias, neg_a, valid);
-    const float hi32 = (float)q.gam, eb = exp2f(hi32), ee = exp2f((float)(q.tot - q.gam));
+    const float hi32 = (float)q.gam, eb = __builtin_amdgcn_exp2f(hi32), ee = __builtin_amdgcn_exp2f((float)(q.tot - q.gam));
     sg[buf][G_HI][l] = hi32;
     sg[buf][G_LO][l] = (float)(q.gam - (double)hi32);
     sg[buf][G_IN][l] = REV ? (valid ? 1.f : 0.f) : q.step;
     sg[buf][G_RD][l] = REV ? ee : eb;
     sg[buf][G_WR][l] = REV ? (valid ? eb : 0.f) : ee * q.step;
     sg[buf][G_OUT][l] = REV ? q.step : 1.f;
-    if (l == 63) sbn[buf] = exp2f((float)q.tot);
+    if (l == 63) sbn[buf] = __builtin_amdgcn_exp2f((float)q.tot);
   };
 
   if (k0 < k1) {
@@ -141,18 +145,22 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
     rk.store(sK);
     if constexpr (OUT) rq.store(sQ);
     rx.store(sX);
-    __syncthreads();  // the chunk's rows and gates are in LDS
+    lds_barrier();  // the chunk's rows and gates are in LDS
     if (k + 1 < k1) load(k + 1);
     const float(*gt)[SC] = sg[buf];
     const float bn = sbn[buf];
     f32x4 o[4];
     if constexpr (OUT) {
       if (a.sv && cols) {
-        float* sv = a.sv + ((lo / SC + n + c) * a.Hv + h) * (int64_t)DK * a.Dv + col0 + r;
+        const __amdgpu_buffer_rsrc_t rs = rows_rsrc(a.sv + ((lo / SC + n + c) * a.Hv + h) * (int64_t)DK * a.Dv, DK * a.Dv * 4);
+        const uint32_t voff = (uint32_t)(4 * g * a.Dv + col0 + r) * 4u;
 #pragma unroll
         for (int t = 0; t < NDT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sv[(int64_t)(16 * t + 4 * g + e) * a.Dv] = S[t][e];
+          for (int e = 0; e < 4; ++e) {
+            const float v = S[t][e];
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs, (int)voff, (16 * t + e) * a.Dv * 4, 0);
+          }
       }
       // M = Gamma o (Q K^T) o inputs' weights: its ten tiles dealt over the waves
 #pragma unroll
@@ -172,7 +180,7 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
         for (int e = 0; e < 4; ++e) {
           const float d = REV ? (jh[e] - ih) + (jl[e] - il) : (ih - jh[e]) + (il - jl[e]);
           const bool in = REV ? i <= j0 + e : i >= j0 + e;
-          m[e] = in ? m[e] * exp2f(d) * wi[e] : 0.f;
+          m[e] = in ? m[e] * __builtin_amdgcn_exp2f(d) * wi[e] : 0.f;
         }
         st4<TI>(sM + LM::at(i, j0), m);
       }
@@ -195,7 +203,7 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
       gates(k + 1, buf ^ 1);
       if (k + 2 < k1) load_dt(k + 2);
     }
-    if constexpr (OUT) __syncthreads();  // M is complete
+    if constexpr (OUT) lds_barrier();  // M is complete
     if (cols) {
 #pragma unroll
       for (int t = 0; t < NDT; ++t) S[t] *= bn;
@@ -217,17 +225,17 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
         }
       }
       if constexpr (OUT) {
-        TI* op = (TI*)a.o + t0 * a.o_rs + (int64_t)h * a.Dv + col0 + 4 * g;
+        const __amdgpu_buffer_rsrc_t rs = rows_rsrc((TI*)a.o + t0 * a.o_rs + (int64_t)h * a.Dv, (uint32_t)len * orow);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int i = 16 * t + r;
-          if (i < len)
-            st4<TI>(op + (int64_t)i * a.o_rs, o[t] * gt[G_OUT][i] + dsk * ld4<TI>(sX + LX::at(i, 16 * w + 4 * g)));
+          const int i = 16 * t + r;  // (rows past the chunk's end are dropped)
+          buf_st4<TI>(rs, (uint32_t)i * orow + (uint32_t)(col0 + 4 * g) * (uint32_t)sizeof(TI),
+                      o[t] * gt[G_OUT][i] + dsk * ld4<TI>(sX + LX::at(i, 16 * w + 4 * g)));
         }
       }
     }
     dec *= bn;
-    __syncthreads();  // LDS is free for the next chunk
+    lds_barrier();  // LDS is free for the next chunk
   }
   if constexpr (OUT) {
     if (a.st && cols && sgm == a.S - 1) {

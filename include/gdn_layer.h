@@ -31,7 +31,7 @@ extern "C" {
  *   y_t = S_t^T c_t + d_skip[h] x_t
  *
  * starting from S0 (zero when NULL). x, y: [rows][Hv*Dv]; b, c: [rows][Hk*Dk]; dt: float32
- * [T_total][Hv]. Sums and states are float32; products of bfloat16 inputs run on the matrix
+ * [T_total][Hv]; a row stride is below 2^25 bytes. Sums and states are float32; products of bfloat16 inputs run on the matrix
  * cores with every float32 factor split over several bfloat16 operands where the result is
  * float32.
  */

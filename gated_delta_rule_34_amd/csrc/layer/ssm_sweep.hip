@@ -38,12 +38,12 @@ template <typename TI, int DK, bool REV, bool OUT>
 __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
   constexpr int NDT = DK / 16, KSD = ks_of<TI, DK>(), NSD = DK / KSD, KSC = ks_of<TI, SC>(), NSC = SC / KSC;
   constexpr int NS = ssm_split<TI>(), TRI = REV ? TRI_UP : TRI_LOW;
-  using LK = Swz<TI, DK, true>;
+  using LK = Swz<TI, DK, true, DK * sizeof(TI) >= 64>;
   using LX = Swz<TI, SP, true>;
   using LM = Swz<TI, SC, false>;
-  __shared__ __align__(16) TI sK[SC * DK];
-  __shared__ __align__(16) TI sQ[OUT ? SC * DK : 8];
-  __shared__ __align__(16) TI sX[SC * SP];
+  __shared__ __align__(16) TI sK[LK::size(SC)];
+  __shared__ __align__(16) TI sQ[OUT ? LK::size(SC) : 8];
+  __shared__ __align__(16) TI sX2[2][SC * SP];
   __shared__ __align__(16) TI sM[OUT ? SC * SC : 8];
   __shared__ __align__(16) float sg[2][G_ROWS][SC];
   __shared__ float sbn[2];
@@ -138,14 +138,15 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
       gates(k0, k0 & 1);
       if (k0 + 1 < k1) load_dt(k0 + 1);
     }
+    rk.store(sK);
+    if constexpr (OUT) rq.store(sQ);
+    rx.store(sX2[k0 & 1]);
   }
   for (int k = k0; k < k1; ++k) {
     const int buf = k & 1, c = chunk(k), len = clen(c);
     const int64_t t0 = lo + (int64_t)c * SC;
-    rk.store(sK);
-    if constexpr (OUT) rq.store(sQ);
-    rx.store(sX);
-    lds_barrier();  // the chunk's rows and gates are in LDS
+    const TI* sX = sX2[buf];
+    lds_barrier();  // the chunk's rows and gates are in LDS, M is free
     if (k + 1 < k1) load(k + 1);
     const float(*gt)[SC] = sg[buf];
     const float bn = sbn[buf];
@@ -199,24 +200,15 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
         for (int t = 0; t < 4; ++t) o[t] *= gt[G_RD][16 * t + r];
       }
     }
-    if (w == 3 && k + 1 < k1) {  // the next chunk's gates
-      gates(k + 1, buf ^ 1);
-      if (k + 2 < k1) load_dt(k + 2);
-    }
-    if constexpr (OUT) lds_barrier();  // M is complete
-    if (cols) {
+    FragT<TI, KSC> xf[NSC];
+    if (cols) {  // the state past this chunk
 #pragma unroll
       for (int t = 0; t < NDT; ++t) S[t] *= bn;
 #pragma unroll
       for (int s = 0; s < NSC; ++s) {
-        const FragT<TI, KSC> xf = ld_t<TI, KSC, STD, LX>(sX, 16 * w, s);
-        if constexpr (OUT) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            if (!tri_skip<TRI, KSC>(s, t)) o[t] = Mf<TI, KSC>::run(xf, ld_n<TI, KSC, STD, LM>(sM, 16 * t, s), o[t]);
-        }
+        xf[s] = ld_t<TI, KSC, STD, LX>(sX, 16 * w, s);
         FragT<TI, KSC> u[NS];
-        scale_split<TI, KSC, NS>(xf, gt[G_WR], s, u);
+        scale_split<TI, KSC, NS>(xf[s], gt[G_WR], s, u);
 #pragma unroll
         for (int t = 0; t < NDT; ++t) {
           const FragT<TI, KSC> kf = ld_t<TI, KSC, STD, LK>(sK, 16 * t, s);
@@ -224,7 +216,20 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
           for (int m = NS - 1; m >= 0; --m) S[t] = Mf<TI, KSC>::run(kf, u[m], S[t]);
         }
       }
-      if constexpr (OUT) {
+    }
+    dec *= bn;
+    if (w == 3 && k + 1 < k1) {  // the next chunk's gates
+      gates(k + 1, buf ^ 1);
+      if (k + 2 < k1) load_dt(k + 2);
+    }
+    lds_barrier();  // M is complete, K and Q are free
+    if constexpr (OUT) {
+      if (cols) {
+#pragma unroll
+        for (int s = 0; s < NSC; ++s)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            if (!tri_skip<TRI, KSC>(s, t)) o[t] = Mf<TI, KSC>::run(xf[s], ld_n<TI, KSC, STD, LM>(sM, 16 * t, s), o[t]);
         const __amdgpu_buffer_rsrc_t rs = rows_rsrc((TI*)a.o + t0 * a.o_rs + (int64_t)h * a.Dv, (uint32_t)len * orow);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -234,8 +239,11 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
         }
       }
     }
-    dec *= bn;
-    lds_barrier();  // LDS is free for the next chunk
+    if (k + 1 < k1) {
+      rk.store(sK);
+      if constexpr (OUT) rq.store(sQ);
+      rx.store(sX2[buf ^ 1]);
+    }
   }
   if constexpr (OUT) {
     if (a.st && cols && sgm == a.S - 1) {

@@ -114,30 +114,51 @@ __global__ __launch_bounds__(256) void k_conv_prompt(ConvCarryArgs a) {
   }
 }
 
-// One token: grid (rows, channel blocks). The window is read, moved on by one row and written.
-template <typename TI, int K> __global__ __launch_bounds__(256) void k_conv_decode(ConvCarryArgs a) {
+// One token: grid (rows / R, channel blocks). The window is read, moved on by one row and written.
+// A thread takes R rows of its channels: their loads are in flight together, and the weights, which
+// its lanes read 32 K bytes apart, are read once for all of them.
+template <typename TI, int K, int R> __global__ __launch_bounds__(256) void k_conv_decode(ConvCarryArgs a) {
   const int c0 = (int)(blockIdx.y * blockDim.x + threadIdx.x) * 8;
   if (c0 >= a.ch) return;
-  const int n = blockIdx.x;
-  const int slot = a.idx ? a.idx[n] : n;
-  if (slot < 0 || (K > 1 && slot >= a.n_slots)) return;  // the row is skipped
-  const F8 xt = ld8<TI>((const TI*)a.x + (int64_t)n * a.x_rs + c0);
-  TI* st = (TI*)a.state + (int64_t)slot * (K - 1) * a.ch + c0;
-  F8 win[K > 1 ? K - 1 : 1];
+  Raw8<TI> xr[R], sr[R][K > 1 ? K - 1 : 1];
+  int slot[R];
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) win[j] = ld8<TI>(st + (int64_t)j * a.ch);
-  F8 out;
+  for (int u = 0; u < R; ++u) {
+    const int n = (int)blockIdx.x * R + u;
+    slot[u] = n >= a.N ? -1 : a.idx ? a.idx[n] : n;
+    if (K > 1 && slot[u] >= a.n_slots) slot[u] = -1;
+    if (slot[u] < 0) continue;  // the row is skipped
+    xr[u] = ldraw8<false, TI>((const TI*)a.x + (int64_t)n * a.x_rs + c0);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) sr[u][j] = ldraw8<false, TI>((const TI*)a.state + ((int64_t)slot[u] * (K - 1) + j) * a.ch + c0);
+  }
+  float w[K][8], bias[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float z = a.bias ? a.bias[c0 + i] : 0.f;
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) z += a.w[(int64_t)(c0 + i) * K + j] * win[j].v[i];
-    z += a.w[(int64_t)(c0 + i) * K + K - 1] * xt.v[i];
-    out.v[i] = z * sigmoidf(z);
+    for (int j = 0; j < K; ++j) w[j][i] = a.w[(int64_t)(c0 + i) * K + j];
+    bias[i] = a.bias ? a.bias[c0 + i] : 0.f;
   }
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) st8<TI>(st + (int64_t)j * a.ch, j + 1 < K - 1 ? win[j + 1 < K - 1 ? j + 1 : j] : xt);
-  st8<TI>((TI*)a.y + (int64_t)n * a.y_rs + c0, out);
+  for (int u = 0; u < R; ++u) {
+    if (slot[u] < 0) continue;
+    const F8 xt = cvt8<TI>(xr[u]);
+    F8 out;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out.v[i] = bias[i] + w[K - 1][i] * xt.v[i];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      const F8 s = cvt8<TI>(sr[u][j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) out.v[i] += w[j][i] * s.v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out.v[i] *= sigmoidf(out.v[i]);
+    TI* st = (TI*)a.state + (int64_t)slot[u] * (K - 1) * a.ch + c0;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) straw8<TI>(st + (int64_t)j * a.ch, j + 1 < K - 1 ? sr[u][j + 1 < K - 1 ? j + 1 : j] : xr[u]);
+    st8<TI>((TI*)a.y + (int64_t)((int)blockIdx.x * R + u) * a.y_rs + c0, out);
+  }
 }
 
 // Threads of a workgroup along the channels: whole waves, at most 256.
@@ -159,10 +180,16 @@ template <typename TI, int K> static hipError_t prompt_k(const ConvCarryArgs& a,
   return hipGetLastError();
 }
 
+// Rows per thread of a decode step: four once that leaves every compute unit a workgroup.
 template <typename TI, int K> static hipError_t decode_k(const ConvCarryArgs& a, hipStream_t s) {
-  const int nt = conv_threads(a.ch);
-  const dim3 grid((unsigned)a.N, (unsigned)((a.ch / 8 + nt - 1) / nt));
-  traced("k_conv_decode", s, [&] { k_conv_decode<TI, K><<<grid, nt, 0, s>>>(a); });
+  const int nt = conv_threads(a.ch), yb = (a.ch / 8 + nt - 1) / nt;
+  if ((int64_t)a.N * yb >= 4 * 256) {
+    const dim3 grid((unsigned)((a.N + 3) / 4), (unsigned)yb);
+    traced("k_conv_decode", s, [&] { k_conv_decode<TI, K, 4><<<grid, nt, 0, s>>>(a); });
+  } else {
+    const dim3 grid((unsigned)a.N, (unsigned)yb);
+    traced("k_conv_decode", s, [&] { k_conv_decode<TI, K, 1><<<grid, nt, 0, s>>>(a); });
+  }
   return hipGetLastError();
 }
 

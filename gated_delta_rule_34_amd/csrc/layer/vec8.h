@@ -32,6 +32,15 @@ template <bool NT, typename TI> __device__ __forceinline__ Raw8<TI> ldraw8(const
   return r;
 }
 
+template <typename TI> __device__ __forceinline__ void straw8(TI* p, const Raw8<TI>& x) {
+  if constexpr (sizeof(TI) == 2) {
+    *reinterpret_cast<i32x4*>(p) = x.a;
+  } else {
+    *reinterpret_cast<f32x4*>(p) = x.a;
+    *reinterpret_cast<f32x4*>(p + 4) = x.b;
+  }
+}
+
 template <typename TI> __device__ __forceinline__ F8 cvt8(const Raw8<TI>& x) {
   F8 r;
   if constexpr (sizeof(TI) == 2) {

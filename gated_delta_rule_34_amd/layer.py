@@ -52,106 +52,112 @@ SIGNATURES = {
 LAYER_EXPORTED = tuple(SIGNATURES)
 
 
-@functools.lru_cache(maxsize=None)
+_bound = {}
+
+
 def _fn(name):
-    fn = getattr(_lib, name)
-    fn.argtypes, fn.restype = SIGNATURES[name]
+    fn = _bound.get(name)
+    if fn is None:
+        fn = getattr(_lib, name)
+        fn.argtypes, fn.restype = SIGNATURES[name]
+        _bound[name] = fn
     return fn
 
 
 def _call(name, p, *args):
-    st = _fn(name)(ctypes.byref(p), *args)
+    st = (_bound.get(name) or _fn(name))(p, *args)
     if st != GDN_OK:
         raise GdnError(st, name)
 
 
 # ------------------------------------------------------------------------------------ checks
+# A single token's kernels take a few microseconds, and so do careless checks of their ten tensors:
+# these look at each tensor once, with the cheapest calls that torch has.
+
+_torch = _types = _f32 = _i32 = _raw_stream = None
 
 
-def _dtype_of(p):
+def _use_torch():
+    """Looks torch's names up (the package itself loads without torch)."""
+    global _torch, _types, _f32, _i32, _raw_stream
     import torch
 
-    return torch.bfloat16 if p.dtype == GDN_BF16 else torch.float32
+    _f32, _i32 = torch.float32, torch.int32
+    _types = {GDN_F32: torch.float32, GDN_BF16: torch.bfloat16}
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _torch = torch
 
 
-class _Check:
-    """Checks the tensors of one call and gives their addresses: all on one device, the current one."""
+def _begin(p, t, name):
+    """The device of a call, that of its tensor `t`, which has to be the current one, and the type of its rows."""
+    if _torch is None:
+        _use_torch()
+    if t is None:
+        raise ValueError(f"{name}: missing")
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name}: expected a GPU tensor")
+    if device != _torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{device}: make that device current")
+    if getattr(p, "device", device) != device:
+        raise ValueError(f"{name} is on cuda:{device}, the problem's parameters on cuda:{p.device}")
+    return device, _types.get(p.dtype, _torch.bfloat16)
 
-    def __init__(self, p, stream):
-        import torch
 
-        self.torch, self.dtype, self.stream, self.device = torch, _dtype_of(p), stream, None
-
-    def _place(self, t, name):
-        if not t.is_cuda:
-            raise ValueError(f"{name}: expected a GPU tensor")
-        if self.device is None:
-            self.device = t.device
-            if t.device.index != self.torch.cuda.current_device():
-                raise ValueError(f"{name} is on {t.device}: make that device current")
-        elif t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, other tensors on {self.device}")
-
-    def rows(self, t, name, rows, width, optional=False):
-        """(address, row stride) of a [rows, width] view, or [rows, heads, D] with contiguous heads."""
-        if t is None:
-            if optional:
-                return None, 0
-            raise ValueError(f"{name}: missing")
-        self._place(t, name)
-        if t.dtype != self.dtype:
-            raise ValueError(f"{name}: expected {self.dtype}, got {t.dtype}")
-        if t.dim() not in (2, 3) or t.shape[0] != rows or _inner(t) != width:
-            raise ValueError(f"{name}: expected {rows} rows of {width}, got {tuple(t.shape)}")
-        if rows == 0:
-            return t.data_ptr(), width  # no row to address
-        if t.stride(-1) != 1 or (t.dim() == 3 and t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+def _rows(t, name, rows, width, device, dtype):
+    """(address, row stride) of a [rows, width] view, or [rows, heads, D] with contiguous heads."""
+    if t is None:
+        raise ValueError(f"{name}: missing")
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3:
+        flat = st[2] == 1 and (shape[1] == 1 or st[1] == shape[2])
+        inner = shape[1] * shape[2]
+    elif len(shape) == 2:
+        flat, inner = st[1] == 1, shape[1]
+    else:
+        flat = inner = None
+    if inner != width or shape[0] != rows or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name}: expected {rows} rows of {width} of {dtype} on cuda:{device}, got {tuple(shape)} of {t.dtype} on {t.device}")
+    if rows > 1:
+        if not flat:
             raise ValueError(f"{name}: rows must be contiguous")
-        return t.data_ptr(), (t.stride(0) if rows > 1 else width)
-
-    def array(self, t, name, shape, dtype=None, optional=False):
-        """Address of a contiguous tensor of `shape` (float32 unless given)."""
-        if t is None:
-            if optional:
-                return None
-            raise ValueError(f"{name}: missing")
-        self._place(t, name)
-        want = dtype or self.torch.float32
-        if t.dtype != want or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous {want} tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-        return t.data_ptr()
-
-    def scratch(self, t):
-        """(address, bytes) of a workspace, or of none."""
-        if t is None:
-            return None, 0
-        self._place(t, "workspace")
-        return t.data_ptr(), t.numel() * t.element_size()
-
-    def on(self):
-        return self.stream if self.stream is not None else self.torch.cuda.current_stream().cuda_stream
+        return t.data_ptr(), st[0]
+    if rows == 1 and not flat and width > 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.data_ptr(), width  # no second row to address
 
 
-def _inner(t):
-    return t.shape[1] if t.dim() == 2 else t.shape[1] * t.shape[2]
+def _array(t, name, shape, device, dtype):
+    """Address of a contiguous tensor of `shape`."""
+    if t is None:
+        raise ValueError(f"{name}: missing")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on cuda:{device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _scratch(t, device):
+    """(address, bytes) of a workspace, or of none."""
+    if t is None:
+        return None, 0
+    if t.get_device() != device:
+        raise ValueError(f"workspace: expected a tensor on cuda:{device}, got {t.device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _on(stream, device):
+    return stream if stream is not None else _raw_stream(device)
 
 
 def _dtype(dtype):
     return {"f32": GDN_F32, "bf16": GDN_BF16}[dtype] if isinstance(dtype, str) else int(dtype)
 
 
-def _params(p, count, **arrays):
-    """Puts the addresses of float32 parameter vectors of `count` values into the problem, which keeps them alive."""
-    import torch
-
-    for name, t in arrays.items():
-        if t is None:
-            setattr(p, name, None)
-            continue
-        if not t.is_cuda or t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != count or not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous float32 GPU vector of {count}")
-        setattr(p, name, t.data_ptr())
-    p._keep = arrays
+def _vector(t, name, count, device):
+    """Address of a float32 parameter vector, or None."""
+    return None if t is None else _array(t, name, (count,), device, _f32)
 
 
 # ------------------------------------------------------------------------------------ scan
@@ -160,49 +166,46 @@ def _params(p, count, **arrays):
 def make_ssm_problem(N, T_total, Hk, Hv, Dk, Dv, *, a_log, dt_bias=None, d_skip=None, T=None, cu_seqlens=None, dtype="bf16"):
     """Build a gdn_ssm_problem. ``a_log`` (and optionally ``dt_bias``, ``d_skip``): device float32
     [Hv]; ``cu_seqlens``: device int32 [N + 1] or None. The problem keeps these tensors alive."""
-    p = gdn_ssm_problem()
-    p.N, p.T_total = int(N), int(T_total)
-    p.T = int(T if T is not None else (T_total // N if (cu_seqlens is None and N) else 0))
-    p.Hk, p.Hv, p.Dk, p.Dv = int(Hk), int(Hv), int(Dk), int(Dv)
-    p.dtype = _dtype(dtype)
-    _params(p, p.Hv, a_log=a_log, dt_bias=dt_bias, d_skip=d_skip)
-    _seqs(p, cu_seqlens)
+    if _torch is None:
+        _use_torch()
+    device, cu = a_log.get_device(), None
+    if device < 0:
+        raise ValueError("a_log: expected a GPU tensor")
+    if cu_seqlens is not None:
+        cu = cu_seqlens.data_ptr()
+        if cu_seqlens.get_device() != device or cu_seqlens.dtype is not _i32 or cu_seqlens.shape != (N + 1,) or not cu_seqlens.is_contiguous():
+            raise ValueError(f"cu_seqlens: expected a contiguous int32 vector of {N + 1} on cuda:{device}")
+    if T is None:
+        T = T_total // N if (cu is None and N) else 0
+    p = gdn_ssm_problem(N, T, T_total, cu, Hk, Hv, Dk, Dv, _dtype(dtype), _vector(a_log, "a_log", Hv, device),
+                        _vector(dt_bias, "dt_bias", Hv, device), _vector(d_skip, "d_skip", Hv, device))
+    p.device, p._keep = device, (a_log, dt_bias, d_skip, cu_seqlens)
     return p
 
 
-def _seqs(p, cu):
-    import torch
-
-    if cu is not None:
-        if not cu.is_cuda or cu.dtype != torch.int32 or tuple(cu.shape) != (p.N + 1,) or not cu.is_contiguous():
-            raise ValueError(f"cu_seqlens: expected a contiguous int32 GPU vector of {p.N + 1}")
-        p._keep["cu_seqlens"] = cu
-        p.cu_seqlens = cu.data_ptr()
-
-
 def gdn_ssm_fwd_workspace_bytes(p) -> int:
-    return int(_fn("gdn_ssm_fwd_workspace_bytes")(ctypes.byref(p)))
+    return _fn("gdn_ssm_fwd_workspace_bytes")(p)
 
 
 def gdn_ssm_bwd_workspace_bytes(p) -> int:
-    return int(_fn("gdn_ssm_bwd_workspace_bytes")(ctypes.byref(p)))
+    return _fn("gdn_ssm_bwd_workspace_bytes")(p)
 
 
 def gdn_ssm_chunk_state_bytes(p) -> int:
-    return int(_fn("gdn_ssm_chunk_state_bytes")(ctypes.byref(p)))
+    return _fn("gdn_ssm_chunk_state_bytes")(p)
 
 
-def _ssm_ins(k, p, x, b, c, dt):
-    T = p.T_total
-    return (*k.rows(x, "x", T, p.Hv * p.Dv), *k.rows(b, "b", T, p.Hk * p.Dk), *k.rows(c, "c", T, p.Hk * p.Dk),
-            k.array(dt, "dt", (T, p.Hv)))
+def _ssm_ins(p, x, b, c, dt, device, dtype):
+    T, kw = p.T_total, p.Hk * p.Dk
+    return (*_rows(x, "x", T, p.Hv * p.Dv, device, dtype), *_rows(b, "b", T, kw, device, dtype),
+            *_rows(c, "c", T, kw, device, dtype), _array(dt, "dt", (T, p.Hv), device, _f32))
 
 
-def _saved(k, p, states):
+def _saved(p, states, device):
     """Address of the saved chunk states, large enough for the problem."""
     if states is None:
         return None
-    at, size = k.scratch(states)
+    at, size = _scratch(states, device)
     if size < gdn_ssm_chunk_state_bytes(p):
         raise ValueError(f"chunk_states: {gdn_ssm_chunk_state_bytes(p)} bytes needed, got {size}")
     return at
@@ -210,32 +213,42 @@ def _saved(k, p, states):
 
 def gdn_ssm_fwd(p, x, b, c, dt, S0, y, S_T, chunk_states, workspace, stream=None):
     """Call gdn_ssm_fwd: y and S_T of the scan over prompts. Raises GdnError on a non-OK status."""
-    k = _Check(p, stream)
+    device, dtype = _begin(p, x, "x")
     st = (p.N, p.Hv, p.Dk, p.Dv)
-    _call("gdn_ssm_fwd", p, *_ssm_ins(k, p, x, b, c, dt), k.array(S0, "S0", st, optional=True),
-          *k.rows(y, "y", p.T_total, p.Hv * p.Dv), k.array(S_T, "S_T", st, optional=True), _saved(k, p, chunk_states),
-          *k.scratch(workspace), k.on())
+    _call("gdn_ssm_fwd", p, *_ssm_ins(p, x, b, c, dt, device, dtype), None if S0 is None else _array(S0, "S0", st, device, _f32),
+          *_rows(y, "y", p.T_total, p.Hv * p.Dv, device, dtype), None if S_T is None else _array(S_T, "S_T", st, device, _f32),
+          _saved(p, chunk_states, device), *_scratch(workspace, device), _on(stream, device))
 
 
 def gdn_ssm_bwd(p, x, b, c, dt, chunk_states, dy, dS_T, dx, db, dc, ddt, da_log, ddt_bias, dd_skip, dS0, workspace,
                 stream=None):
     """Call gdn_ssm_bwd: the gradients of gdn_ssm_fwd's inputs (da_log, ddt_bias, dd_skip, dS0 may be None)."""
-    k = _Check(p, stream)
+    device, dtype = _begin(p, x, "x")
     T, xw, kw, st = p.T_total, p.Hv * p.Dv, p.Hk * p.Dk, (p.N, p.Hv, p.Dk, p.Dv)
-    _call("gdn_ssm_bwd", p, *_ssm_ins(k, p, x, b, c, dt), _saved(k, p, chunk_states), *k.rows(dy, "dy", T, xw),
-          k.array(dS_T, "dS_T", st, optional=True), *k.rows(dx, "dx", T, xw), *k.rows(db, "db", T, kw),
-          *k.rows(dc, "dc", T, kw), k.array(ddt, "ddt", (T, p.Hv)), k.array(da_log, "da_log", (p.Hv,), optional=True),
-          k.array(ddt_bias, "ddt_bias", (p.Hv,), optional=True), k.array(dd_skip, "dd_skip", (p.Hv,), optional=True),
-          k.array(dS0, "dS0", st, optional=True), *k.scratch(workspace), k.on())
+    _call("gdn_ssm_bwd", p, *_ssm_ins(p, x, b, c, dt, device, dtype), _saved(p, chunk_states, device),
+          *_rows(dy, "dy", T, xw, device, dtype), None if dS_T is None else _array(dS_T, "dS_T", st, device, _f32),
+          *_rows(dx, "dx", T, xw, device, dtype), *_rows(db, "db", T, kw, device, dtype), *_rows(dc, "dc", T, kw, device, dtype),
+          _array(ddt, "ddt", (T, p.Hv), device, _f32),
+          *(None if v is None else _array(v, n, (p.Hv,), device, _f32)
+            for v, n in ((da_log, "da_log"), (ddt_bias, "ddt_bias"), (dd_skip, "dd_skip"))),
+          None if dS0 is None else _array(dS0, "dS0", st, device, _f32), *_scratch(workspace, device), _on(stream, device))
+
+
+def _pool(state, slot_idx, N, device, shape, dtype):
+    """(address, slots, address of the slot map) of a pool of states [n_slots, *shape]."""
+    if state is None:
+        raise ValueError("state: missing")
+    n_slots = state.shape[0]
+    return (_array(state, "state", (n_slots, *shape), device, dtype), n_slots,
+            None if slot_idx is None else _array(slot_idx, "slot_idx", (N,), device, _i32))
 
 
 def gdn_ssm_decode(p, x, b, c, dt, state, slot_idx, y, stream=None):
     """Call gdn_ssm_decode: one token per row; ``state`` float32 [n_slots, Hv, Dk, Dv] updated in place,
     ``slot_idx`` int32 [N] or None (row n -> slot n)."""
-    k = _Check(p, stream)
-    n_slots = 0 if state is None else int(state.shape[0])
-    _call("gdn_ssm_decode", p, *_ssm_ins(k, p, x, b, c, dt), k.array(state, "state", (n_slots, p.Hv, p.Dk, p.Dv)), n_slots,
-          k.array(slot_idx, "slot_idx", (p.N,), k.torch.int32, optional=True), *k.rows(y, "y", p.N, p.Hv * p.Dv), k.on())
+    device, dtype = _begin(p, x, "x")
+    _call("gdn_ssm_decode", p, *_ssm_ins(p, x, b, c, dt, device, dtype), *_pool(state, slot_idx, p.N, device, (p.Hv, p.Dk, p.Dv), _f32),
+          *_rows(y, "y", p.N, p.Hv * p.Dv, device, dtype), _on(stream, device))
 
 
 def ssm_forward(p, x, b, c, dt, S0=None, y=None, want_final=True, workspace=None, stream=None, save=True):
@@ -277,26 +290,30 @@ def ssm_backward(p, x, b, c, dt, S0, states, dy, dS_T=None, grads=None, want_dS0
 # ------------------------------------------------------------------------------------ conv
 
 
+def _conv_ins(p, x, w, bias, device, dtype):
+    ch = p.channels
+    return (*_rows(x, "x", p.T_total, ch, device, dtype), _array(w, "w", (ch, p.kernel_size), device, _f32),
+            None if bias is None else _array(bias, "bias", (ch,), device, _f32))
+
+
 def gdn_conv1d_silu_prompt(p, x, w, bias, first, y, last, stream=None):
     """Call gdn_conv1d_silu_prompt: y = SiLU(bias + causal conv1d(x, w)) per sequence, continuing from
     ``first`` [N, K - 1, channels] (None: zeros); ``last`` (None: skip) gets the rows a continuation needs."""
-    k = _Check(p, stream)
+    device, dtype = _begin(p, x, "x")
     win = (p.N, p.kernel_size - 1, p.channels)
-    _call("gdn_conv1d_silu_prompt", p, *k.rows(x, "x", p.T_total, p.channels),
-          k.array(w, "w", (p.channels, p.kernel_size)), k.array(bias, "bias", (p.channels,), optional=True),
-          k.array(first, "first", win, k.dtype, optional=True), *k.rows(y, "y", p.T_total, p.channels),
-          k.array(last, "last", win, k.dtype, optional=True), k.on())
+    _call("gdn_conv1d_silu_prompt", p, *_conv_ins(p, x, w, bias, device, dtype),
+          None if first is None else _array(first, "first", win, device, dtype),
+          *_rows(y, "y", p.T_total, p.channels, device, dtype),
+          None if last is None else _array(last, "last", win, device, dtype), _on(stream, device))
 
 
 def gdn_conv1d_silu_decode(p, x, w, bias, state, slot_idx, y, stream=None):
     """Call gdn_conv1d_silu_decode: one token per row; ``state`` [n_slots, K - 1, channels] is moved on by a
     row in place, ``slot_idx`` int32 [N] or None (row n -> slot n)."""
-    k = _Check(p, stream)
-    n_slots = 0 if state is None else int(state.shape[0])
-    _call("gdn_conv1d_silu_decode", p, *k.rows(x, "x", p.N, p.channels), k.array(w, "w", (p.channels, p.kernel_size)),
-          k.array(bias, "bias", (p.channels,), optional=True),
-          k.array(state, "state", (n_slots, p.kernel_size - 1, p.channels), k.dtype), n_slots,
-          k.array(slot_idx, "slot_idx", (p.N,), k.torch.int32, optional=True), *k.rows(y, "y", p.N, p.channels), k.on())
+    device, dtype = _begin(p, x, "x")
+    _call("gdn_conv1d_silu_decode", p, *_conv_ins(p, x, w, bias, device, dtype),
+          *_pool(state, slot_idx, p.N, device, (p.kernel_size - 1, p.channels), dtype),
+          *_rows(y, "y", p.N, p.channels, device, dtype), _on(stream, device))
 
 
 # ------------------------------------------------------------------------------------ norms
@@ -304,24 +321,17 @@ def gdn_conv1d_silu_decode(p, x, w, bias, state, slot_idx, y, stream=None):
 
 def make_norm_problem(rows, width, *, groups=1, shared=False, eps=1e-6, gate_first=False, scale=1.0, dtype="bf16"):
     """Build a gdn_norm_problem: rows of ``groups`` groups of ``width`` values."""
-    p = gdn_norm_problem()
-    p.rows, p.groups, p.width = int(rows), int(groups), int(width)
-    p.shared, p.gate_first = 1 if shared else 0, 1 if gate_first else 0
-    p.eps, p.scale, p.dtype = float(eps), float(scale), _dtype(dtype)
-    return p
+    return gdn_norm_problem(rows, groups, width, 1 if shared else 0, 1 if gate_first else 0, eps, scale, _dtype(dtype))
 
 
-def _w_shape(p):
-    return p.width if p.shared else p.groups * p.width
-
-
-def _weight(k, p, t, name):
-    """A norm's weights, flat or [groups, width]."""
-    return k.array(None if t is None else t.view(-1) if t.is_contiguous() else t, name, (_w_shape(p),))
+def _weight(p, t, name, device):
+    """Address of a norm's weights, flat or [groups, width] (one group when shared)."""
+    groups = 1 if p.shared else p.groups
+    return _array(t, name, (groups, p.width) if t is not None and t.dim() == 2 else (groups * p.width,), device, _f32)
 
 
 def _ws_bytes(name, p):
-    return int(_fn(name)(ctypes.byref(p)))
+    return _fn(name)(p)
 
 
 def gdn_gated_norm_bwd_workspace_bytes(p) -> int:
@@ -334,17 +344,19 @@ def gdn_add_norm_bwd_workspace_bytes(p) -> int:
 
 def gdn_gated_norm_fwd(p, x, z, w, y, stream=None):
     """Call gdn_gated_norm_fwd: y = norm(x) silu(z), or norm(x silu(z)) with gate_first."""
-    k, full = _Check(p, stream), p.groups * p.width
-    _call("gdn_gated_norm_fwd", p, *k.rows(x, "x", p.rows, full), *k.rows(z, "z", p.rows, full), _weight(k, p, w, "w"),
-          *k.rows(y, "y", p.rows, full), k.on())
+    device, dtype = _begin(p, x, "x")
+    n, full = p.rows, p.groups * p.width
+    _call("gdn_gated_norm_fwd", p, *_rows(x, "x", n, full, device, dtype), *_rows(z, "z", n, full, device, dtype),
+          _weight(p, w, "w", device), *_rows(y, "y", n, full, device, dtype), _on(stream, device))
 
 
 def gdn_gated_norm_bwd(p, x, z, w, dy, dx, dz, dw, workspace, stream=None):
     """Call gdn_gated_norm_bwd (dw None: skipped, and then no workspace is needed)."""
-    k, full = _Check(p, stream), p.groups * p.width
-    _call("gdn_gated_norm_bwd", p, *k.rows(x, "x", p.rows, full), *k.rows(z, "z", p.rows, full), _weight(k, p, w, "w"),
-          *k.rows(dy, "dy", p.rows, full), *k.rows(dx, "dx", p.rows, full), *k.rows(dz, "dz", p.rows, full),
-          None if dw is None else _weight(k, p, dw, "dw"), *k.scratch(workspace), k.on())
+    device, dtype = _begin(p, x, "x")
+    v = (p.rows, p.groups * p.width, device, dtype)
+    _call("gdn_gated_norm_bwd", p, *_rows(x, "x", *v), *_rows(z, "z", *v), _weight(p, w, "w", device), *_rows(dy, "dy", *v),
+          *_rows(dx, "dx", *v), *_rows(dz, "dz", *v), None if dw is None else _weight(p, dw, "dw", device),
+          *_scratch(workspace, device), _on(stream, device))
 
 
 def gated_norm_forward(p, x, z, w, stream=None):
@@ -366,19 +378,21 @@ def gated_norm_backward(p, x, z, w, dy, workspace=None, stream=None):
 
 def gdn_add_norm_fwd(p, h, y, s, w, res, out, stream=None):
     """Call gdn_add_norm_fwd: res = h + scale s y (s None: ones), out = norm(res)."""
-    k, v = _Check(p, stream), (p.rows, p.width)
-    _call("gdn_add_norm_fwd", p, *k.rows(h, "h", *v), *k.rows(y, "y", *v), k.array(s, "s", (p.width,), optional=True),
-          k.array(w, "w", (p.width,)), *k.rows(res, "res", *v), *k.rows(out, "out", *v), k.on())
+    device, dtype = _begin(p, h, "h")
+    v, width = (p.rows, p.width, device, dtype), (p.width,)
+    _call("gdn_add_norm_fwd", p, *_rows(h, "h", *v), *_rows(y, "y", *v), None if s is None else _array(s, "s", width, device, _f32),
+          _array(w, "w", width, device, _f32), *_rows(res, "res", *v), *_rows(out, "out", *v), _on(stream, device))
 
 
 def gdn_add_norm_bwd(p, res, y, s, w, dout, dres, dh, dy, dw, ds, workspace, stream=None):
     """Call gdn_add_norm_bwd (dres, dy, dw, ds may be None; y only where ds is None)."""
-    k, v = _Check(p, stream), (p.rows, p.width)
-    _call("gdn_add_norm_bwd", p, *k.rows(res, "res", *v), *k.rows(y, "y", *v, optional=ds is None),
-          k.array(s, "s", (p.width,), optional=True), k.array(w, "w", (p.width,)), *k.rows(dout, "dout", *v),
-          *k.rows(dres, "dres", *v, optional=True), *k.rows(dh, "dh", *v), *k.rows(dy, "dy", *v, optional=True),
-          k.array(dw, "dw", (p.width,), optional=True), k.array(ds, "ds", (p.width,), optional=True), *k.scratch(workspace),
-          k.on())
+    device, dtype = _begin(p, res, "res")
+    v, width, none = (p.rows, p.width, device, dtype), (p.width,), (None, 0)
+    _call("gdn_add_norm_bwd", p, *_rows(res, "res", *v), *(none if y is None and ds is None else _rows(y, "y", *v)),
+          None if s is None else _array(s, "s", width, device, _f32), _array(w, "w", width, device, _f32),
+          *_rows(dout, "dout", *v), *(none if dres is None else _rows(dres, "dres", *v)), *_rows(dh, "dh", *v),
+          *(none if dy is None else _rows(dy, "dy", *v)), None if dw is None else _array(dw, "dw", width, device, _f32),
+          None if ds is None else _array(ds, "ds", width, device, _f32), *_scratch(workspace, device), _on(stream, device))
 
 
 def add_norm_forward(p, h, y, s, w, stream=None):

@@ -24,17 +24,20 @@ __device__ __forceinline__ void carry_clamp(const ConvCarryArgs& a, int l, int64
   hi = y;
 }
 
-// The sequence of row t and its rows [lo, hi). A row of no sequence (behind the last one, or in
-// front of cu[0] in a malformed table) gets one that does not hold it.
+// The sequence of row t and its rows [lo, hi), by a whole wave: every step probes 64 offsets at
+// once (one step up to 64 sequences, two up to 4096). A row of no sequence (behind the last one, or
+// in front of cu[0] in a malformed table) gets one that does not hold it.
 __device__ __forceinline__ int carry_seq(const ConvCarryArgs& a, int64_t t, int64_t& lo, int64_t& hi) {
   int l = 0;
   if (!a.cu) {
     l = (int)(t / a.T);
   } else {
-    int r = a.N;  // largest n with cu[n] <= t
-    while (r - l > 1) {
-      const int m = (l + r) >> 1;
-      if (a.cu[m] <= t) l = m; else r = m;
+    for (int n = a.N; n > 1;) {  // the largest of the n sequences from l on with cu[.] <= t
+      const int stride = (n + 63) / 64, i = lane_id() * stride;
+      const uint64_t m = __ballot(i < n && a.cu[l + i] <= t);
+      const int at = (m ? 63 - __builtin_clzll(m) : 0) * stride;
+      l += at;
+      n = n - at < stride ? n - at : stride;
     }
   }
   carry_clamp(a, l, lo, hi);
@@ -44,9 +47,12 @@ __device__ __forceinline__ int carry_seq(const ConvCarryArgs& a, int64_t t, int6
 // Each thread owns 8 adjacent channels and RUN consecutive rows, the next PF of them in flight.
 // Blocks past the runs copy one sequence's last rows each.
 template <typename TI, int K, int RUN, int PF>
-__global__ __launch_bounds__(256) void k_conv_prompt(ConvCarryArgs a) {
-  const int c0 = (int)(blockIdx.y * blockDim.x + threadIdx.x) * 8;
-  if (c0 >= a.ch) return;
+__global__ __launch_bounds__(64) void k_conv_prompt(ConvCarryArgs a) {
+  // channel blocks run fastest, so that workgroups in flight read whole neighbouring rows
+  const int yb = (a.ch / 8 + (int)blockDim.x - 1) / (int)blockDim.x, bx = (int)blockIdx.x / yb;
+  int c0 = (((int)blockIdx.x - bx * yb) * (int)blockDim.x + (int)threadIdx.x) * 8;
+  const bool on = c0 < a.ch;  // (idle lanes stay for the search of the sequence)
+  c0 = on ? c0 : 0;
   const TI* x = (const TI*)a.x + c0;
   const TI* first = a.first ? (const TI*)a.first + c0 : nullptr;
   const int64_t runs = (a.rows + RUN - 1) / RUN;
@@ -55,24 +61,29 @@ __global__ __launch_bounds__(256) void k_conv_prompt(ConvCarryArgs a) {
   auto carried = [&](int n, int64_t s) -> F8 {
     return first ? ld8<TI>(first + ((int64_t)n * (K - 1) + (K - 1) + s) * a.ch) : zero8();
   };
-  if ((int64_t)blockIdx.x >= runs) {
-    const int n = (int)(blockIdx.x - runs);
+  if (bx >= runs) {
+    const int n = (int)(bx - runs);
     carry_clamp(a, n, lo, hi);
     TI* last = (TI*)a.last + c0;
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
       const int64_t s = hi - lo - (K - 1) + j;
-      st8<TI>(last + ((int64_t)n * (K - 1) + j) * a.ch, s >= 0 ? ld8<TI>(x + (lo + s) * a.x_rs) : carried(n, s));
+      const F8 v = s >= 0 ? ld8<TI>(x + (lo + s) * a.x_rs) : carried(n, s);
+      if (on) st8<TI>(last + ((int64_t)n * (K - 1) + j) * a.ch, v);
     }
     return;
   }
-  const int64_t t0 = (int64_t)blockIdx.x * RUN;
+  const int64_t t0 = (int64_t)bx * RUN;
   const int64_t t1 = t0 + RUN < a.rows ? t0 + RUN : a.rows;
   TI* y = (TI*)a.y + c0;
   Raw8<TI> buf[PF];
 #pragma unroll
   for (int u = 0; u < PF; ++u)
     if (t0 + u < t1) buf[u] = ldraw8<true, TI>(x + (t0 + u) * a.x_rs);
+  // the rows in front of the run, used if they belong to its sequence
+  F8 win[K > 1 ? K - 1 : 1];
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) win[j] = t0 - (K - 1) + j >= 0 ? ld8<TI>(x + (t0 - (K - 1) + j) * a.x_rs) : zero8();
   float w[K][8], bias[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -80,13 +91,13 @@ __global__ __launch_bounds__(256) void k_conv_prompt(ConvCarryArgs a) {
     for (int j = 0; j < K; ++j) w[j][i] = a.w[(int64_t)(c0 + i) * K + j];
     bias[i] = a.bias ? a.bias[c0 + i] : 0.f;
   }
-  F8 win[K > 1 ? K - 1 : 1];
-  auto enter = [&](int64_t t) {  // the window in front of row t
+  auto enter = [&](int64_t t) {  // places of row t's window in front of its sequence: carried rows, or none
     const int n = carry_seq(a, t, lo, hi);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
       const int64_t s = t - lo - (K - 1) + j;
-      win[j] = t < lo || t >= hi ? zero8() : s >= 0 ? ld8<TI>(x + (lo + s) * a.x_rs) : carried(n, s);
+      if (t < lo || t >= hi) win[j] = zero8();
+      else if (s < 0) win[j] = carried(n, s);
     }
   };
   enter(t0);
@@ -106,7 +117,7 @@ __global__ __launch_bounds__(256) void k_conv_prompt(ConvCarryArgs a) {
         for (int j = 0; j < K - 1; ++j) z += w[j][i] * win[j].v[i];
         out.v[i] = z * sigmoidf(z);
       }
-      if (t >= lo && t < hi) st8<TI>(y + t * a.y_rs, out);  // rows of no sequence stay as they were
+      if (on && t >= lo && t < hi) st8nt<TI>(y + t * a.y_rs, out);  // rows of no sequence stay as they were
 #pragma unroll
       for (int j = 0; j + 1 < K - 1; ++j) win[j] = win[j + 1];
       if constexpr (K > 1) win[K - 2] = xt;
@@ -117,7 +128,7 @@ __global__ __launch_bounds__(256) void k_conv_prompt(ConvCarryArgs a) {
 // One token: grid (rows / R, channel blocks). The window is read, moved on by one row and written.
 // A thread takes R rows of its channels: their loads are in flight together, and the weights, which
 // its lanes read 32 K bytes apart, are read once for all of them.
-template <typename TI, int K, int R> __global__ __launch_bounds__(256) void k_conv_decode(ConvCarryArgs a) {
+template <typename TI, int K, int R> __global__ __launch_bounds__(64) void k_conv_decode(ConvCarryArgs a) {
   const int c0 = (int)(blockIdx.y * blockDim.x + threadIdx.x) * 8;
   if (c0 >= a.ch) return;
   Raw8<TI> xr[R], sr[R][K > 1 ? K - 1 : 1];
@@ -161,34 +172,38 @@ template <typename TI, int K, int R> __global__ __launch_bounds__(256) void k_co
   }
 }
 
-// Threads of a workgroup along the channels: whole waves, at most 256.
-static int conv_threads(int ch) {
-  const int t = (ch / 8 + 63) / 64 * 64;
-  return t < 256 ? t : 256;
-}
+// One-wave workgroups (512 channels): a token step of 256 rows x 10240 channels spreads over 1280 of
+// them and takes 17.5 us, over 320 of four waves 20.
+constexpr int kConvWave = 64;
+static int conv_blocks(int ch) { return (ch / 8 + kConvWave - 1) / kConvWave; }
 
 template <typename TI, int K, int RUN, int PF> static void prompt_run(const ConvCarryArgs& a, hipStream_t s) {
-  const int nt = conv_threads(a.ch);
   const int64_t blocks = (a.rows + RUN - 1) / RUN + (a.last && K > 1 ? a.N : 0);
   if (blocks == 0) return;
-  const dim3 grid((unsigned)blocks, (unsigned)((a.ch / 8 + nt - 1) / nt));
-  traced("k_conv_prompt", s, [&] { k_conv_prompt<TI, K, RUN, PF><<<grid, nt, 0, s>>>(a); });
+  const unsigned grid = (unsigned)(blocks * conv_blocks(a.ch));
+  traced("k_conv_prompt", s, [&] { k_conv_prompt<TI, K, RUN, PF><<<grid, kConvWave, 0, s>>>(a); });
 }
 
+// Long runs amortise a run's weights, window and search; short ones leave no compute unit idle.
+// Measured (bf16, K = 4): 21488 x 10240 in 64-row runs 197 us, in 16-row ones 243; 2048 x 10240 45
+// and 28 us; 512 x 2048 38 and 14, in 8-row ones 11 us.
 template <typename TI, int K> static hipError_t prompt_k(const ConvCarryArgs& a, hipStream_t s) {
-  prompt_run<TI, K, 32, 1>(a, s);
+  const int64_t long_runs = (a.rows + 63) / 64 * conv_blocks(a.ch);
+  if (long_runs >= 2048) prompt_run<TI, K, 64, 2>(a, s);
+  else if (long_runs >= 256) prompt_run<TI, K, 16, 4>(a, s);
+  else prompt_run<TI, K, 8, 8>(a, s);
   return hipGetLastError();
 }
 
 // Rows per thread of a decode step: four once that leaves every compute unit a workgroup.
 template <typename TI, int K> static hipError_t decode_k(const ConvCarryArgs& a, hipStream_t s) {
-  const int nt = conv_threads(a.ch), yb = (a.ch / 8 + nt - 1) / nt;
+  const int yb = conv_blocks(a.ch);
   if ((int64_t)a.N * yb >= 4 * 256) {
     const dim3 grid((unsigned)((a.N + 3) / 4), (unsigned)yb);
-    traced("k_conv_decode", s, [&] { k_conv_decode<TI, K, 4><<<grid, nt, 0, s>>>(a); });
+    traced("k_conv_decode", s, [&] { k_conv_decode<TI, K, 4><<<grid, kConvWave, 0, s>>>(a); });
   } else {
     const dim3 grid((unsigned)a.N, (unsigned)yb);
-    traced("k_conv_decode", s, [&] { k_conv_decode<TI, K, 1><<<grid, nt, 0, s>>>(a); });
+    traced("k_conv_decode", s, [&] { k_conv_decode<TI, K, 1><<<grid, kConvWave, 0, s>>>(a); });
   }
   return hipGetLastError();
 }

@@ -123,9 +123,11 @@ gdn_status check_conv(const gdn_conv_problem* p) {
   if (!p || p->channels <= 0 || p->channels % 8) return GDN_EINVAL;
   if (p->kernel_size < 1 || p->kernel_size > 4) return GDN_EUNSUPPORTED;
   if (p->dtype != GDN_F32 && p->dtype != GDN_BF16) return GDN_EUNSUPPORTED;
-  if (p->channels / 8 > 65535LL * 256) return GDN_EINVAL;  // grid limits
-  if (p->N > kMaxBlocks / 2) return GDN_EINVAL;
-  return check_seqs(p->N, p->T, p->T_total, p->cu_seqlens);
+  if (p->channels / 8 > 65535LL * 64 || p->N > kMaxBlocks / 2) return GDN_EINVAL;  // grid limits
+  GDN_TRY(check_seqs(p->N, p->T, p->T_total, p->cu_seqlens));
+  // one wave per 512 channels of 64 rows and of each sequence's last rows
+  const int64_t waves = (p->T_total / 64 + 64 + p->N) * ((p->channels + 511) / 512);
+  return waves < (1LL << 32) / 64 ? GDN_OK : GDN_EINVAL;
 }
 
 gdn::ConvCarryArgs conv_args(const gdn_conv_problem* p, const void* x, int64_t x_rs, const float* w,

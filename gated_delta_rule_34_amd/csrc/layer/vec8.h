@@ -71,6 +71,19 @@ template <typename TI> __device__ __forceinline__ void st8(TI* p, const F8& x) {
   }
 }
 
+// st8 past the caches' normal allocation, for results that nothing reads soon.
+template <typename TI> __device__ __forceinline__ void st8nt(TI* p, const F8& x) {
+  if constexpr (sizeof(TI) == 2) {
+    bf16x8 y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = (__bf16)x.v[i];
+    store_nt(reinterpret_cast<bf16x8*>(p), y);
+  } else {
+    store_nt(reinterpret_cast<f32x4*>(p), f32x4{x.v[0], x.v[1], x.v[2], x.v[3]});
+    store_nt(reinterpret_cast<f32x4*>(p + 4), f32x4{x.v[4], x.v[5], x.v[6], x.v[7]});
+  }
+}
+
 __device__ __forceinline__ F8 zero8() { return F8{{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}}; }
 
 // 1 / (1 + e^-z) with the hardware reciprocal and exponential (about 1 ulp each; 0 where e^-z

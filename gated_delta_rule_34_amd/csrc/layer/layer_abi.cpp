@@ -69,8 +69,9 @@ gdn_status check_ssm(const gdn_ssm_problem* p) {
   if (!size_ok(p->Dk) || !size_ok(p->Dv)) return GDN_EUNSUPPORTED;
   GDN_TRY(check_seqs(p->N, p->T, p->T_total, p->cu_seqlens));
   // one workgroup per (sequence, head, 64 columns), per (row, head) and per (chunk, group)
+  constexpr int64_t most = kMaxBlocks / 2;  // (of up to 512 threads)
   const int64_t slabs = p->Dv > 64 ? 2 : 1, slots = p->T_total / 64 + p->N;
-  if ((int64_t)(p->N + 8) * p->Hv > kMaxBlocks / slabs || slots > kMaxBlocks / p->Hv) return GDN_EINVAL;
+  if ((int64_t)(p->N + 8) * p->Hv > most / slabs || slots > most / p->Hv) return GDN_EINVAL;
   GDN_TRY(check_arr(p->a_log, true));
   GDN_TRY(check_arr(p->dt_bias, false));
   return check_arr(p->d_skip, false);

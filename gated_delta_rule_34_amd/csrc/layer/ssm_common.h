@@ -111,10 +111,10 @@ template <typename TI> __device__ __forceinline__ void buf_st4(__amdgpu_buffer_r
   }
 }
 
-// A [64][CN] tile of rows on its way through registers into LDS, by 256 threads. Rows at or past
+// A [64][CN] tile of rows on its way through registers into LDS, by NT threads. Rows at or past
 // len and columns at or past ncols arrive as zeros; nothing outside the caller's rows is read.
-template <typename TI, int CN, class L> struct TileRegs {
-  static constexpr int CE = 16 / (int)sizeof(TI), PPR = CN / CE, TOT = SC * PPR, U = (TOT + 255) / 256, STEP = 256 / PPR;
+template <typename TI, int CN, class L, int NT> struct TileRegs {
+  static constexpr int CE = 16 / (int)sizeof(TI), PPR = CN / CE, TOT = SC * PPR, U = (TOT + NT - 1) / NT, STEP = NT / PPR;
   i32x4 v[U];
   uint32_t rsb, voff;  // row stride in bytes, this thread's first piece
   __device__ __forceinline__ void init(int64_t rs, int ncols) {
@@ -122,16 +122,16 @@ template <typename TI, int CN, class L> struct TileRegs {
     rsb = (uint32_t)rs * (uint32_t)sizeof(TI);
     voff = q < TOT && c < ncols ? (uint32_t)(q / PPR) * rsb + c * (int)sizeof(TI) : kNowhere;
   }
-  template <bool NT> __device__ __forceinline__ void load(const TI* src, int len) {
+  template <bool ONCE> __device__ __forceinline__ void load(const TI* src, int len) {
     const __amdgpu_buffer_rsrc_t rs = rows_rsrc(src, (uint32_t)len * rsb);
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = buf_ld16<NT>(rs, voff + (uint32_t)(u * STEP) * rsb);
+    for (int u = 0; u < U; ++u) v[u] = buf_ld16<ONCE>(rs, voff + (uint32_t)(u * STEP) * rsb);
   }
   __device__ __forceinline__ void store(TI* lds) const {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int q = u * 256 + (int)threadIdx.x;
-      if (TOT % 256 == 0 || q < TOT) *reinterpret_cast<i32x4*>(lds + L::at(q / PPR, (q % PPR) * CE)) = v[u];
+      const int q = u * NT + (int)threadIdx.x;
+      if (TOT % NT == 0 || q < TOT) *reinterpret_cast<i32x4*>(lds + L::at(q / PPR, (q % PPR) * CE)) = v[u];
     }
   }
 };
@@ -160,6 +160,13 @@ __device__ __forceinline__ double lane_value_f64(double x, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+// log1p(x) for x >= 0: log(u) x / (u - 1) with u = 1 + x as rounded, which takes the rounding back
+// out (Kahan); a few ulp, a third of the library function's operations.
+__device__ __forceinline__ float log1p_pos(float x) {
+  const float u = 1.f + x, d = u - 1.f;
+  return d == 0.f ? x : __logf(u) * (x * __builtin_amdgcn_rcpf(d));
+}
+
 // Gates of one chunk, one token per lane: the step, gamma (log2), its sum over the chunk.
 struct Gate {
   float z, step;
@@ -168,7 +175,7 @@ struct Gate {
 __device__ __forceinline__ Gate chunk_gate(float dt, float bias, float neg_a_log2, bool valid) {
   Gate q;
   q.z = dt + bias;
-  q.step = valid ? softplusf(q.z) : 0.f;
+  q.step = !valid ? 0.f : q.z > 20.f ? q.z : log1p_pos(expf(q.z));
   q.gam = wave_scan_incl_f64(valid ? (double)(neg_a_log2 * q.step) : 0.0);
   q.tot = lane_value_f64(q.gam, 63);
   return q;

@@ -66,7 +66,7 @@ __global__ __launch_bounds__(256, 2) void k_ssm_grad(GradArgs a) {
   const int len = (int)(hi - t0 < SC ? hi - t0 : SC);
 
   {
-    TileRegs<TI, DK, LK> rb, rc;
+    TileRegs<TI, DK, LK, 256> rb, rc;
     rb.init(p.b_rs, DK);
     rc.init(p.c_rs, DK);
     rb.template load<false>((const TI*)p.b + t0 * p.b_rs + kh * DK, len);
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256, 2) void k_ssm_grad(GradArgs a) {
     for (int slab = 0; slab < a.nslab; ++slab) {
       const int ncols = p.Dv - slab * SP < SP ? p.Dv - slab * SP : SP;
       {
-        TileRegs<TI, SP, LX> rx, ry;
+        TileRegs<TI, SP, LX, 256> rx, ry;
         rx.init(p.x_rs, ncols);
         ry.init(p.dy_rs, ncols);
         rx.template load<true>((const TI*)p.x + t0 * p.x_rs + (int64_t)h * p.Dv + slab * SP, len);

@@ -2,11 +2,13 @@
 // outputs y and the state going forward in time, or dx and the state's adjoint going backward
 // (the formulas stand in ssm_common.h).
 //
-// One workgroup per (sequence, segment, head, 64 columns of x): four waves, each with 16 columns of
-// the state in its accumulators; columns of the state never mix. Per chunk the products K Q^T, M X,
-// S^T Q and K^T (w X) run on the matrix cores; every product is formed transposed, so that a lane
-// holds four adjacent columns of one token. The next chunk's rows are in registers while a chunk is
-// computed.
+// One workgroup per (sequence, segment, head, 64 columns of x): eight waves, wave w with 16 columns
+// (w mod 4) and half of the state's rows (w / 4) in its accumulators; columns of the state never mix,
+// and the two halves' shares of S^T Q meet in LDS. Per chunk the products K Q^T, S^T Q, K^T (w X) and
+// M X run on the matrix cores; every product is formed transposed, so that a lane holds four adjacent
+// columns of one token. The next chunk's rows are in registers while a chunk is computed. A chunk is
+// a chain of short dependent products, bound by their latency: eight waves of 128 registers, so that
+// two workgroups (four waves per SIMD) share a compute unit, hide what four waves of 230 did not.
 //
 // Few sequences and heads leave compute units idle over a long serial chain, so a sequence is then
 // cut into S segments: a first launch runs the state alone over all segments but the last, from
@@ -30,13 +32,17 @@ struct SweepArgs {
   float* dec;       // [N][S][Hv] decay over each segment
 };
 
-// Gate rows in LDS: gamma and its remainder, the weight of an input inside the chunk, the decays
-// with which a token reads and writes the state, the weight of an output.
-enum { G_HI, G_LO, G_IN, G_RD, G_WR, G_OUT, G_ROWS };
+// Gate rows in LDS: gamma and its remainder, the step (the weight of an input, in reverse of an
+// output), the decays with which a token reads and writes the state.
+enum { G_HI, G_LO, G_IN, G_RD, G_WR, G_ROWS };
+
+template <typename TI, int DK> constexpr int sweep_waves() { return 2; }  // per SIMD
 
 template <typename TI, int DK, bool REV, bool OUT>
-__global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
-  constexpr int NDT = DK / 16, KSD = ks_of<TI, DK>(), NSD = DK / KSD, KSC = ks_of<TI, SC>(), NSC = SC / KSC;
+__global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(SweepArgs a) {
+  constexpr int NT = 512, DH = DK >= 32 ? DK / 2 : 16, ND = DH / 16;  // this wave's rows of the state
+  constexpr int KSD = ks_of<TI, DK>(), NSD = DK / KSD, KSC = ks_of<TI, SC>(), NSC = SC / KSC;
+  constexpr int KSH = ks_of<TI, DH>(), NSH = DH / KSH;
   constexpr int NS = ssm_split<TI>(), TRI = REV ? TRI_UP : TRI_LOW;
   using LK = Swz<TI, DK, true, DK * sizeof(TI) >= 64>;
   using LX = Swz<TI, SP, true>;
@@ -45,8 +51,9 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
   __shared__ __align__(16) TI sQ[OUT ? LK::size(SC) : 8];
   __shared__ __align__(16) TI sX2[2][SC * SP];
   __shared__ __align__(16) TI sM[OUT ? SC * SC : 8];
-  __shared__ __align__(16) float sg[2][G_ROWS][SC];
-  __shared__ float sbn[2];
+  __shared__ __align__(16) f32x4 sP[OUT ? 8 * 2 * 64 : 1];  // shares of S^T Q for the other half
+  __shared__ __align__(16) float sg[16][G_ROWS][SC];
+  __shared__ float sbn[16];
 
   const int segs = OUT ? a.S : a.S - 1;
   int grp, mem;
@@ -59,8 +66,11 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
   const int kh = grp % a.Hk, sgm = (grp / a.Hk) % segs, n = grp / a.Hk / segs;
   const int h = kh * a.r + mem / a.nslab, slab = mem % a.nslab;
   const int w = wave_id(), l = lane_id(), g = l >> 4, r = l & 15;
-  const int col0 = slab * SP + 16 * w;  // this wave's columns of the head
-  const bool cols = col0 < a.Dv;        // (a head of 16 or 32 leaves waves without columns)
+  const int cw = w & 3, hf = w >> 2;            // this wave's columns and half
+  const int col0 = slab * SP + 16 * cw;         // its first column of the head
+  const bool cols = col0 < a.Dv;                // (a head of 16 or 32 leaves waves without columns)
+  const bool has = cols && hf * DH < DK;        // whether it holds a part of the state
+  const int d0 = hf * DH + 4 * g;               // its first row there, this lane's
   const int ncols = a.Dv - slab * SP < SP ? a.Dv - slab * SP : SP;
 
   int64_t lo, hi;
@@ -74,39 +84,17 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
   const TI* qp = (const TI*)a.q + kh * DK;
   const TI* xp = (const TI*)a.x + (int64_t)h * a.Dv + slab * SP;
 
-  // the state: tile t holds rows 16 t + 4 g + e of column col0 + r
-  f32x4 S[NDT];
-#pragma unroll
-  for (int t = 0; t < NDT; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int64_t nh = (int64_t)n * a.Hv + h;
-  if constexpr (OUT) {
-    if (a.s0 && cols) {
-      const float* s0 = a.s0 + nh * DK * a.Dv + col0 + r;
-#pragma unroll
-      for (int t = 0; t < NDT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[t][e] = s0[(int64_t)(16 * t + 4 * g + e) * a.Dv];
-    }
-    for (int j = 0; j < sgm; ++j) {
-      const int64_t nj = ((int64_t)n * a.S + j) * a.Hv + h;
-      const float d = a.dec[nj];
-      const f32x4* p = reinterpret_cast<const f32x4*>(a.loc) + ((nj * a.nslab + slab) * NDT) * 256 + threadIdx.x;
-#pragma unroll
-      for (int t = 0; t < NDT; ++t) S[t] = d * S[t] + p[t * 256];
-    }
-    for (int i = threadIdx.x; i < SC * SC; i += 256) sM[i] = (TI)0.f;  // the tiles past the diagonal stay zero
-  }
-  float dec = 1.f;
-
   auto chunk = [&](int k) { return REV ? nch - 1 - k : k; };
   auto clen = [&](int c) { const int64_t rest = hi - lo - (int64_t)c * SC; return (int)(rest < SC ? rest : SC); };
-  TileRegs<TI, DK, LK> rk, rq;
-  TileRegs<TI, SP, LX> rx;
+  TileRegs<TI, DK, LK, NT> rk, rq;
+  TileRegs<TI, SP, LX, NT> rx;
   rk.init(a.k_rs, DK);
   if constexpr (OUT) rq.init(a.q_rs, DK);
   rx.init(a.x_rs, ncols);
   const uint32_t orow = (uint32_t)a.o_rs * (uint32_t)sizeof(TI);
-  float rdt = 0.f;  // the last wave: dt of the chunk after the loaded one
+  // Gates come eight chunks at a time, one for each wave (a chunk's are a long chain of dependent
+  // operations: by one wave, chunk by chunk, they took a fifth of the step).
+  float rdt = 0.f;  // dt of this wave's chunk of the next eight
   auto load = [&](int k) {
     const int c = chunk(k), len = clen(c);
     const int64_t t0 = lo + (int64_t)c * SC;
@@ -116,28 +104,64 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
   };
   auto load_dt = [&](int k) {
     const int c = chunk(k);
-    rdt = l < clen(c) ? a.dt[(lo + (int64_t)c * SC + l) * a.Hv + h] : 0.f;
+    rdt = k < k1 && l < clen(c) ? a.dt[(lo + (int64_t)c * SC + l) * a.Hv + h] : 0.f;
   };
-  auto gates = [&](int k, int buf) {
-    const bool valid = l < clen(chunk(k));
+  auto gates = [&](int k) {
+    const bool valid = k < k1 && l < clen(chunk(k));
     const Gate q = chunk_gate(rdt, bias, neg_a, valid);
     const float hi32 = (float)q.gam, eb = __builtin_amdgcn_exp2f(hi32), ee = __builtin_amdgcn_exp2f((float)(q.tot - q.gam));
-    sg[buf][G_HI][l] = hi32;
-    sg[buf][G_LO][l] = (float)(q.gam - (double)hi32);
-    sg[buf][G_IN][l] = REV ? (valid ? 1.f : 0.f) : q.step;
-    sg[buf][G_RD][l] = REV ? ee : eb;
-    sg[buf][G_WR][l] = REV ? (valid ? eb : 0.f) : ee * q.step;
-    sg[buf][G_OUT][l] = REV ? q.step : 1.f;
-    if (l == 63) sbn[buf] = __builtin_amdgcn_exp2f((float)q.tot);
+    float(*gt)[SC] = sg[(k - k0) & 15];
+    gt[G_HI][l] = hi32;
+    gt[G_LO][l] = (float)(q.gam - (double)hi32);
+    gt[G_IN][l] = q.step;
+    gt[G_RD][l] = REV ? ee : eb;
+    gt[G_WR][l] = REV ? (valid ? eb : 0.f) : ee * q.step;
+    if (l == 63) sbn[(k - k0) & 15] = __builtin_amdgcn_exp2f((float)q.tot);
+  };
+  if (k0 < k1) {
+    load_dt(k0 + w);
+    load(k0);
+  }
+
+  // the state: tile t holds rows d0 + 16 t + e of column col0 + r
+  f32x4 S[ND];
+#pragma unroll
+  for (int t = 0; t < ND; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int64_t nh = (int64_t)n * a.Hv + h;
+  if constexpr (OUT) {
+    if (a.s0 && has) {
+      const float* s0 = a.s0 + nh * DK * a.Dv + col0 + r;
+#pragma unroll
+      for (int t = 0; t < ND; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[t][e] = s0[(int64_t)(d0 + 16 * t + e) * a.Dv];
+    }
+    for (int j = 0; j < sgm; ++j) {
+      const int64_t nj = ((int64_t)n * a.S + j) * a.Hv + h;
+      const float d = a.dec[nj];
+      const f32x4* p = reinterpret_cast<const f32x4*>(a.loc) + ((nj * a.nslab + slab) * ND) * NT + threadIdx.x;
+#pragma unroll
+      for (int t = 0; t < ND; ++t) S[t] = d * S[t] + p[t * NT];
+    }
+    for (int i = threadIdx.x; i < SC * SC; i += NT) sM[i] = (TI)0.f;  // the tiles past the diagonal stay zero
+  }
+  float dec = 1.f;
+  auto save = [&](int k) {  // the state before chunk k
+    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(a.sv + ((lo / SC + n + chunk(k)) * a.Hv + h) * (int64_t)DK * a.Dv, DK * a.Dv * 4);
+    const uint32_t voff = (uint32_t)(d0 * a.Dv + col0 + r) * 4u;
+#pragma unroll
+    for (int t = 0; t < ND; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = S[t][e];
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs, (int)voff, (16 * t + e) * a.Dv * 4, 0);
+      }
   };
 
   if (k0 < k1) {
-    load(k0);
-    if (w == 3) {
-      load_dt(k0);
-      gates(k0, k0 & 1);
-      if (k0 + 1 < k1) load_dt(k0 + 1);
-    }
+    if (OUT && a.sv && has) save(k0);
+    gates(k0 + w);
+    load_dt(k0 + 8 + w);
     rk.store(sK);
     if constexpr (OUT) rq.store(sQ);
     rx.store(sX2[k0 & 1]);
@@ -146,27 +170,16 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
     const int buf = k & 1, c = chunk(k), len = clen(c);
     const int64_t t0 = lo + (int64_t)c * SC;
     const TI* sX = sX2[buf];
-    lds_barrier();  // the chunk's rows and gates are in LDS, M is free
+    lds_barrier();  // the chunk's rows and gates are in LDS, M and the shares are free
     if (k + 1 < k1) load(k + 1);
-    const float(*gt)[SC] = sg[buf];
-    const float bn = sbn[buf];
+    const float(*gt)[SC] = sg[(k - k0) & 15];
+    const float bn = sbn[(k - k0) & 15];
     f32x4 o[4];
     if constexpr (OUT) {
-      if (a.sv && cols) {
-        const __amdgpu_buffer_rsrc_t rs = rows_rsrc(a.sv + ((lo / SC + n + c) * a.Hv + h) * (int64_t)DK * a.Dv, DK * a.Dv * 4);
-        const uint32_t voff = (uint32_t)(4 * g * a.Dv + col0 + r) * 4u;
-#pragma unroll
-        for (int t = 0; t < NDT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float v = S[t][e];
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs, (int)voff, (16 * t + e) * a.Dv * 4, 0);
-          }
-      }
       // M = Gamma o (Q K^T) o inputs' weights: its ten tiles dealt over the waves
 #pragma unroll
-      for (int u = 0; u < 3; ++u) {
-        const int idx = w + 4 * u;
+      for (int u = 0; u < 2; ++u) {
+        const int idx = w + 8 * u;
         if (idx >= 10) continue;
         const int big = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0, small = idx - big * (big + 1) / 2;
         const int it = REV ? small : big, jt = REV ? big : small;
@@ -181,90 +194,110 @@ __global__ __launch_bounds__(256, 2) void k_ssm_sweep(SweepArgs a) {
         for (int e = 0; e < 4; ++e) {
           const float d = REV ? (jh[e] - ih) + (jl[e] - il) : (ih - jh[e]) + (il - jl[e]);
           const bool in = REV ? i <= j0 + e : i >= j0 + e;
-          m[e] = in ? m[e] * __builtin_amdgcn_exp2f(d) * wi[e] : 0.f;
+          m[e] *= __builtin_amdgcn_exp2f(d);
+          if constexpr (!REV) m[e] *= wi[e];
+          m[e] = in ? m[e] : 0.f;
         }
         st4<TI>(sM + LM::at(i, j0), m);
       }
-      // S^T Q, decayed
+      // this half's share of S^T Q, decayed; two token tiles of it go to the other half
 #pragma unroll
       for (int t = 0; t < 4; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (cols) {
+      if (has) {
 #pragma unroll
-        for (int s = 0; s < NSD; ++s) {
-          FragT<TI, KSD> sf[1];
-          acc_split<TI, KSD, 1>(S, s, sf);
+        for (int s = 0; s < NSH; ++s) {
+          FragT<TI, KSH> sf[1];
+          acc_split<TI, KSH, 1>(S, s, sf);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) o[t] = Mf<TI, KSD>::run(sf[0], ld_n<TI, KSD, ACC, LK>(sQ, 16 * t, s), o[t]);
+          for (int t = 0; t < 4; ++t)
+            o[t] = Mf<TI, KSH>::run(sf[0], ld_n<TI, KSH, ACC, LK>(sQ, 16 * t, hf * NSH + s), o[t]);
         }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) o[t] *= gt[G_RD][16 * t + r];
+      }
+      if (hf == 0) {
+        sP[(w * 2 + 0) * 64 + l] = o[2];
+        sP[(w * 2 + 1) * 64 + l] = o[3];
+      } else {
+        sP[(w * 2 + 0) * 64 + l] = o[0];
+        sP[(w * 2 + 1) * 64 + l] = o[1];
+        o[0] = o[2];
+        o[1] = o[3];
       }
     }
     FragT<TI, KSC> xf[NSC];
-    if (cols) {  // the state past this chunk
+    if (cols) {
 #pragma unroll
-      for (int t = 0; t < NDT; ++t) S[t] *= bn;
+      for (int s = 0; s < NSC; ++s) xf[s] = ld_t<TI, KSC, STD, LX>(sX, 16 * cw, s);
+    }
+    if (has) {  // the state past this chunk
+#pragma unroll
+      for (int t = 0; t < ND; ++t) S[t] *= bn;
 #pragma unroll
       for (int s = 0; s < NSC; ++s) {
-        xf[s] = ld_t<TI, KSC, STD, LX>(sX, 16 * w, s);
         FragT<TI, KSC> u[NS];
         scale_split<TI, KSC, NS>(xf[s], gt[G_WR], s, u);
 #pragma unroll
-        for (int t = 0; t < NDT; ++t) {
-          const FragT<TI, KSC> kf = ld_t<TI, KSC, STD, LK>(sK, 16 * t, s);
+        for (int t = 0; t < ND; ++t) {
+          const FragT<TI, KSC> kf = ld_t<TI, KSC, STD, LK>(sK, hf * DH + 16 * t, s);
 #pragma unroll
           for (int m = NS - 1; m >= 0; --m) S[t] = Mf<TI, KSC>::run(kf, u[m], S[t]);
         }
       }
     }
     dec *= bn;
-    if (w == 3 && k + 1 < k1) {  // the next chunk's gates
-      gates(k + 1, buf ^ 1);
-      if (k + 2 < k1) load_dt(k + 2);
-    }
-    lds_barrier();  // M is complete, K and Q are free
+    lds_barrier();  // M and the shares are complete, K and Q are free
     if constexpr (OUT) {
-      if (cols) {
+      if (a.sv && has && k + 1 < k1) save(k + 1);
+      if (cols) {  // this wave's token tiles 2 hf and 2 hf + 1
+        const __amdgpu_buffer_rsrc_t rs = rows_rsrc((TI*)a.o + t0 * a.o_rs + (int64_t)h * a.Dv, (uint32_t)len * orow);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) o[t] = (o[t] + sP[((w ^ 4) * 2 + t) * 64 + l]) * gt[G_RD][32 * hf + 16 * t + r];
+        // steps of M X whose tiles are all zero are left out (wave-uniform)
 #pragma unroll
         for (int s = 0; s < NSC; ++s)
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
-            if (!tri_skip<TRI, KSC>(s, t)) o[t] = Mf<TI, KSC>::run(xf[s], ld_n<TI, KSC, STD, LM>(sM, 16 * t, s), o[t]);
-        const __amdgpu_buffer_rsrc_t rs = rows_rsrc((TI*)a.o + t0 * a.o_rs + (int64_t)h * a.Dv, (uint32_t)len * orow);
+          for (int t = 0; t < 2; ++t)
+            if (hf == 0 ? !tri_skip<TRI, KSC>(s, t) : !tri_skip<TRI, KSC>(s, 2 + t))
+              o[t] = Mf<TI, KSC>::run(xf[s], ld_n<TI, KSC, STD, LM>(sM, 32 * hf + 16 * t, s), o[t]);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int i = 16 * t + r;  // (rows past the chunk's end are dropped)
+        for (int t = 0; t < 2; ++t) {
+          const int i = 32 * hf + 16 * t + r;  // (rows past the chunk's end are dropped)
+          f32x4 v = o[t];
+          if constexpr (REV) v *= gt[G_IN][i];
           buf_st4<TI>(rs, (uint32_t)i * orow + (uint32_t)(col0 + 4 * g) * (uint32_t)sizeof(TI),
-                      o[t] * gt[G_OUT][i] + dsk * ld4<TI>(sX + LX::at(i, 16 * w + 4 * g)));
+                      v + dsk * ld4<TI>(sX + LX::at(i, 16 * cw + 4 * g)));
         }
       }
     }
     if (k + 1 < k1) {
+      if (((k + 1 - k0) & 7) == 0) {  // the next eight chunks' gates
+        gates(k + 1 + w);
+        load_dt(k + 9 + w);
+      }
       rk.store(sK);
       if constexpr (OUT) rq.store(sQ);
       rx.store(sX2[buf ^ 1]);
     }
   }
   if constexpr (OUT) {
-    if (a.st && cols && sgm == a.S - 1) {
+    if (a.st && has && sgm == a.S - 1) {
       float* st = a.st + nh * DK * a.Dv + col0 + r;
 #pragma unroll
-      for (int t = 0; t < NDT; ++t)
+      for (int t = 0; t < ND; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) st[(int64_t)(16 * t + 4 * g + e) * a.Dv] = S[t][e];
+        for (int e = 0; e < 4; ++e) st[(int64_t)(d0 + 16 * t + e) * a.Dv] = S[t][e];
     }
   } else {
     const int64_t nj = ((int64_t)n * a.S + sgm) * a.Hv + h;
-    f32x4* p = reinterpret_cast<f32x4*>(a.loc) + ((nj * a.nslab + slab) * NDT) * 256 + threadIdx.x;
+    f32x4* p = reinterpret_cast<f32x4*>(a.loc) + ((nj * a.nslab + slab) * ND) * NT + threadIdx.x;
 #pragma unroll
-    for (int t = 0; t < NDT; ++t) p[t * 256] = S[t];
+    for (int t = 0; t < ND; ++t) p[t * NT] = S[t];
     if (slab == 0 && threadIdx.x == 0) a.dec[nj] = dec;
   }
 }
 
 // Segments per sequence: enough workgroups for the chip, each with at least kMinChunks chunks on
 // average (a segment costs its states and a second read of its rows).
-constexpr int kWantGroups = 512, kMinChunks = 4, kMaxSegments = 32;
+constexpr int kWantGroups = 256, kMinChunks = 4, kMaxSegments = 32;
 static int ssm_segments(const SsmArgs& a) {
   if (a.N == 0) return 1;
   const int64_t groups = (int64_t)a.N * a.Hv * ((a.Dv + SP - 1) / SP);
@@ -280,7 +313,7 @@ static size_t seg_bytes(const SsmArgs& a) {
   const int S = ssm_segments(a);
   if (S == 1) return 0;
   const size_t u = (size_t)a.N * S * a.Hv;
-  return up256(u * ((a.Dv + SP - 1) / SP) * a.Dk * SP * 4) + up256(u * 4);
+  return up256(u * ((a.Dv + SP - 1) / SP) * (a.Dk < 32 ? 32 : a.Dk) * SP * 4) + up256(u * 4);
 }
 size_t ssm_saved_bytes(const SsmArgs& a) { return (size_t)ssm_slots(a.T_total, a.N) * a.Hv * a.Dk * a.Dv * 4; }
 size_t ssm_fwd_ws_bytes(const SsmArgs& a) { return seg_bytes(a); }
@@ -299,7 +332,7 @@ template <typename TI, int DK, bool REV> static hipError_t sweep_go(const SsmArg
   v.st = REV ? a.dS0 : a.ST;
   v.sv = sv;
   v.loc = seg;
-  v.dec = seg + (v.S > 1 ? up256((size_t)a.N * v.S * a.Hv * v.nslab * DK * SP * 4) / 4 : 0);
+  v.dec = seg + (v.S > 1 ? up256((size_t)a.N * v.S * a.Hv * v.nslab * (DK < 32 ? 32 : DK) * SP * 4) / 4 : 0);
   // A group's heads share b and c: with many groups they go to one XCD (workgroups are dealt to
   // the eight XCDs in turn) and share its L2; few groups would leave XCDs idle.
   auto grid = [&](int segs) {
@@ -309,12 +342,12 @@ template <typename TI, int DK, bool REV> static hipError_t sweep_go(const SsmArg
   };
   if (v.S > 1) {
     const int b = grid(v.S - 1);
-    traced(REV ? "k_ssm_state_rev" : "k_ssm_state", s, [&] { k_ssm_sweep<TI, DK, REV, false><<<b, 256, 0, s>>>(v); });
+    traced(REV ? "k_ssm_state_rev" : "k_ssm_state", s, [&] { k_ssm_sweep<TI, DK, REV, false><<<b, 512, 0, s>>>(v); });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const int b = grid(v.S);
-  traced(REV ? "k_ssm_sweep_rev" : "k_ssm_sweep", s, [&] { k_ssm_sweep<TI, DK, REV, true><<<b, 256, 0, s>>>(v); });
+  traced(REV ? "k_ssm_sweep_rev" : "k_ssm_sweep", s, [&] { k_ssm_sweep<TI, DK, REV, true><<<b, 512, 0, s>>>(v); });
   return hipGetLastError();
 }
 

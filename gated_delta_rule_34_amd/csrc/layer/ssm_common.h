@@ -28,16 +28,15 @@ template <typename TI, int KS, int NS> __device__ __forceinline__ void split_fra
   if constexpr (KS == 4) {
     o[0] = v[0];
   } else {
-    float rest[Mf<TI, KS>::KE];
+    typedef float fv __attribute__((ext_vector_type(Mf<TI, KS>::KE)));
+    fv rest;
 #pragma unroll
     for (int j = 0; j < Mf<TI, KS>::KE; ++j) rest[j] = v[j];
 #pragma unroll
-    for (int k = 0; k < NS; ++k)
-#pragma unroll
-      for (int j = 0; j < Mf<TI, KS>::KE; ++j) {
-        o[k][j] = (__bf16)rest[j];
-        rest[j] -= (float)o[k][j];
-      }
+    for (int k = 0; k < NS; ++k) {
+      o[k] = __builtin_convertvector(rest, FragT<TI, KS>);
+      if (k + 1 < NS) rest -= __builtin_convertvector(o[k], fv);
+    }
   }
 }
 

@@ -14,6 +14,12 @@
 // it, so they run once per group on the sum over its heads. b, c, x, dy are exact as bfloat16
 // operands; the states are split over three (24 bits), so that the float32 results keep float32
 // accuracy. Bound by HBM: the two states of a chunk and head are 8 Dk Dv bytes.
+//
+// Eight waves: wave w holds 16 rows of Dk (all tokens; with a smaller state some tokens) and one or two
+// tiles of the tokens' triangle. The next head's rows and states are on their way while a head is
+// computed (a state's registers are refilled as soon as its fragments are split off). What is left of a
+// head after its products is one value per token: its sums over lanes and waves, and the scans that give
+// q, are done for HB heads at once, one head to a wave, and so are the gates.
 #include "ssm_common.h"
 
 namespace gdn {
@@ -27,22 +33,22 @@ struct GradArgs {
 };
 
 template <typename TI, int DK>
-__global__ __launch_bounds__(256, 2) void k_ssm_grad(GradArgs a) {
+__global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
   const SsmArgs& p = a.p;
-  constexpr int NDT = DK / 16, KSD = ks_of<TI, DK>(), NSD = DK / KSD, KSC = ks_of<TI, SC>(), NSC = SC / KSC;
+  constexpr int NT = 512, NDT = DK / 16, KSD = ks_of<TI, DK>(), NSD = DK / KSD, KSC = ks_of<TI, SC>(), NSC = SC / KSC;
   constexpr int NS = ssm_split<TI>(), KE = Mf<TI, KSC>::KE;
-  // tiles of a [Dk][64 tokens] product: DT tiles along Dk, TT along the tokens for each wave
-  constexpr int DT = NDT >= 4 ? NDT / 4 : 1, TT = NDT >= 4 ? 4 : NDT;
+  constexpr int TT = NDT == 8 ? 4 : NDT == 4 ? 2 : 1;   // token tiles of a wave's [16 of Dk][64 tokens] products
+  constexpr int HB = sizeof(TI) == 4 ? 2 : 8;           // heads whose scans are done together
+  constexpr int XB = sizeof(TI) == 4 ? 1 : 2;           // buffers of x and dy
   using LK = Swz<TI, DK, true>;
   using LX = Swz<TI, SP, true>;
   __shared__ __align__(16) TI sB[SC * DK];
   __shared__ __align__(16) TI sC[SC * DK];
-  __shared__ __align__(16) TI sX[SC * SP];
-  __shared__ __align__(16) TI sY[SC * SP];
+  __shared__ __align__(16) TI sXY[XB][2][SC * SP];
   __shared__ __align__(16) TI sR[SC * SC];
-  __shared__ __align__(16) float sh[2][6][SC];  // gamma, its remainder, step, 2^gamma, e, dt + bias
-  __shared__ float sbn[2];
-  __shared__ float srow[10][16], scol[10][16], sdiag[SC], sE[4][SC], sF[4][SC], sfr[4], sdd[4];
+  __shared__ __align__(16) float sh[2][HB][6][SC];  // gamma, its remainder, step, 2^gamma, e, dt + bias
+  __shared__ float sbn[2][HB];
+  __shared__ float srow[HB][10][16], scol[HB][10][16], sdiag[HB][SC], sE[HB][8][SC], sF[HB][8][SC], sfr[HB][8], sdd[HB][8];
 
   const int kh = (int)(blockIdx.x % p.Hk);
   const int64_t slot = blockIdx.x / p.Hk;
@@ -58,32 +64,98 @@ __global__ __launch_bounds__(256, 2) void k_ssm_grad(GradArgs a) {
   ssm_seq(p.cu, p.T, p.T_total, n, lo, hi);
   const int64_t k = slot - (lo / SC + n);
   if (k < 0 || k >= (hi - lo + SC - 1) / SC) {  // a slot of no chunk
-    for (int i = threadIdx.x; i < 3 * p.r; i += 256)
+    for (int i = threadIdx.x; i < 3 * p.r; i += NT)
       a.part[((int64_t)(i / p.r) * a.slots + slot) * p.Hv + kh * p.r + i % p.r] = 0.f;
     return;
   }
   const int64_t t0 = lo + k * SC;
   const int len = (int)(hi - t0 < SC ? hi - t0 : SC);
 
+  const int dtile = w % NDT, ttile0 = (w / NDT) * TT;       // this wave's tiles of the [Dk][tokens] products
+  const bool mine = NDT > 1 || w < 4;                       // (a state of 16 rows leaves four waves without)
+  const int pairs = p.r * a.nslab;                          // (head, slab) steps
+
+  // rows and states of step q on their way
+  TileRegs<TI, SP, LX, NT> rx, ry;
+  float rs[NSC][KE], rd[NSC][KE];  // this lane's row of S and dS: 64 columns, KE per step
+  auto load_rows = [&](int q) {
+    const int h = kh * p.r + q / a.nslab, slab = q % a.nslab;
+    const int ncols = p.Dv - slab * SP < SP ? p.Dv - slab * SP : SP;
+    rx.init(p.x_rs, ncols);
+    ry.init(p.dy_rs, ncols);
+    rx.template load<true>((const TI*)p.x + t0 * p.x_rs + (int64_t)h * p.Dv + slab * SP, len);
+    ry.template load<true>((const TI*)p.dy + t0 * p.dy_rs + (int64_t)h * p.Dv + slab * SP, len);
+  };
+  auto load_state = [&](int q, int s) {
+    const int h = kh * p.r + q / a.nslab, slab = q % a.nslab;
+    const int64_t base = (slot * p.Hv + h) * (int64_t)DK * p.Dv;
+    const uint32_t bytes = (uint32_t)(DK * p.Dv) * 4u;
+    const __amdgpu_buffer_rsrc_t bs = rows_rsrc(a.sv + base, bytes), bd = rows_rsrc(a.ds + base, bytes);
+    const int c = slab * SP + kidx<KSC, STD>(s, g, 0);
+    const uint32_t voff = mine && c < p.Dv ? (uint32_t)((16 * dtile + r) * p.Dv + c) * 4u : kNowhere;
+    if constexpr (KE == 1) {
+      rs[s][0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bs, (int)voff, 0, 2));
+      rd[s][0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bd, (int)voff, 0, 2));
+    } else {
+#pragma unroll
+      for (int j = 0; j < KE; j += 4) {
+        const f32x4 vs = __builtin_bit_cast(f32x4, buf_ld16<true>(bs, voff + 4u * j));
+        const f32x4 vd = __builtin_bit_cast(f32x4, buf_ld16<true>(bd, voff + 4u * j));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          rs[s][j + e] = vs[e];
+          rd[s][j + e] = vd[e];
+        }
+      }
+    }
+  };
+  // the gates of head hh + w (one head of a batch to a wave)
+  float rdt = 0.f;
+  auto load_dt = [&](int hh) {
+    rdt = w < HB && hh + w < p.r && l < len ? p.dt[(t0 + l) * p.Hv + kh * p.r + hh + w] : 0.f;
+  };
+  auto gates = [&](int hh) {
+    if (w >= HB || hh + w >= p.r) return;
+    const int h = kh * p.r + hh + w, b = (hh / HB) & 1;
+    const Gate q = chunk_gate(rdt, p.dt_bias ? p.dt_bias[h] : 0.f, -expf(p.a_log[h]) * kLog2e, l < len);
+    const float h32 = (float)q.gam;
+    float(*gt)[SC] = sh[b][w];
+    gt[0][l] = h32;
+    gt[1][l] = (float)(q.gam - (double)h32);
+    gt[2][l] = q.step;
+    gt[3][l] = __builtin_amdgcn_exp2f(h32);
+    gt[4][l] = __builtin_amdgcn_exp2f((float)(q.tot - q.gam));
+    gt[5][l] = q.z;
+    if (l == 63) sbn[b][w] = __builtin_amdgcn_exp2f((float)q.tot);
+  };
+
   {
-    TileRegs<TI, DK, LK, 256> rb, rc;
+    TileRegs<TI, DK, LK, NT> rb, rc;
     rb.init(p.b_rs, DK);
     rc.init(p.c_rs, DK);
     rb.template load<false>((const TI*)p.b + t0 * p.b_rs + kh * DK, len);
     rc.template load<false>((const TI*)p.c + t0 * p.c_rs + kh * DK, len);
-    for (int i = threadIdx.x; i < SC * SC; i += 256) sR[i] = (TI)0.f;
-    for (int i = threadIdx.x; i < 4 * SC; i += 256) sE[i / SC][i % SC] = sF[i / SC][i % SC] = 0.f;
+    load_dt(0);
+    load_rows(0);
+#pragma unroll
+    for (int s = 0; s < NSC; ++s) load_state(0, s);
+    for (int i = threadIdx.x; i < SC * SC; i += NT) sR[i] = (TI)0.f;
+    for (int i = threadIdx.x; i < HB * 8 * SC; i += NT) (&sE[0][0][0])[i] = (&sF[0][0][0])[i] = 0.f;
     rb.store(sB);
     rc.store(sC);
+    gates(0);
+    load_dt(HB);
+    rx.store(sXY[0][0]);
+    ry.store(sXY[0][1]);
   }
   lds_barrier();
   // this wave's tiles of the lower triangle: token tiles it >= jt; element e of a lane is (i, j) =
   // (16 it + r, 16 jt + 4 g + e)
-  int it[3], jt[3];
-  f32x4 G[3], R[3];
+  int it[2], jt[2];
+  f32x4 G[2], R[2], Q[2];
 #pragma unroll
-  for (int u = 0; u < 3; ++u) {
-    const int idx = w + 4 * u;
+  for (int u = 0; u < 2; ++u) {
+    const int idx = w + 8 * u;
     it[u] = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
     jt[u] = idx - it[u] * (it[u] + 1) / 2;
     G[u] = R[u] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -92,232 +164,187 @@ __global__ __launch_bounds__(256, 2) void k_ssm_grad(GradArgs a) {
     for (int s = 0; s < NSD; ++s)
       G[u] = Mf<TI, KSD>::run(ld_n<TI, KSD, STD, LK>(sB, 16 * jt[u], s), ld_n<TI, KSD, STD, LK>(sC, 16 * it[u], s), G[u]);
   }
-  auto dtile = [&](int x) { return NDT >= 4 ? w * DT + x : w % NDT; };
-  auto ttile = [&](int y) { return NDT >= 4 ? y : (w / NDT) * TT + y; };
-  f32x4 dC[DT][TT], dB[DT][TT];
-  zero(dC);
-  zero(dB);
+  f32x4 dC[TT], dB[TT], E[TT], F[TT];
+#pragma unroll
+  for (int y = 0; y < TT; ++y) dC[y] = dB[y] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float frob = 0.f;
 
-  for (int hh = 0; hh < p.r; ++hh) {
-    const int h = kh * p.r + hh, buf = hh & 1;
-    f32x4 E[DT][TT], F[DT][TT], Q[3];
-    zero(E);
-    zero(F);
+  for (int q = 0; q < pairs; ++q) {
+    const int hh = q / a.nslab, slab = q % a.nslab, xb = XB == 2 ? q & 1 : 0, hb = hh % HB;
+    const TI *sX = sXY[xb][0], *sY = sXY[xb][1];
+    if (slab == 0) {
+      frob = 0.f;
 #pragma unroll
-    for (int u = 0; u < 3; ++u) Q[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float frob = 0.f;
-    const int64_t base = (slot * p.Hv + h) * (int64_t)DK * p.Dv;
-    for (int slab = 0; slab < a.nslab; ++slab) {
-      const int ncols = p.Dv - slab * SP < SP ? p.Dv - slab * SP : SP;
-      {
-        TileRegs<TI, SP, LX, 256> rx, ry;
-        rx.init(p.x_rs, ncols);
-        ry.init(p.dy_rs, ncols);
-        rx.template load<true>((const TI*)p.x + t0 * p.x_rs + (int64_t)h * p.Dv + slab * SP, len);
-        ry.template load<true>((const TI*)p.dy + t0 * p.dy_rs + (int64_t)h * p.Dv + slab * SP, len);
-        lds_barrier();  // the previous rows are used up
-        rx.store(sX);
-        ry.store(sY);
-      }
-      if (w == 3 && slab == 0) {
-        const float dt = l < len ? p.dt[(t0 + l) * p.Hv + h] : 0.f;
-        const Gate q = chunk_gate(dt, p.dt_bias ? p.dt_bias[h] : 0.f, -expf(p.a_log[h]) * kLog2e, l < len);
-        const float h32 = (float)q.gam;
-        sh[buf][0][l] = h32;
-        sh[buf][1][l] = (float)(q.gam - (double)h32);
-        sh[buf][2][l] = q.step;
-        sh[buf][3][l] = __builtin_amdgcn_exp2f(h32);
-        sh[buf][4][l] = __builtin_amdgcn_exp2f((float)(q.tot - q.gam));
-        sh[buf][5][l] = q.z;
-        if (l == 63) sbn[buf] = __builtin_amdgcn_exp2f((float)q.tot);
-      }
-      lds_barrier();
+      for (int y = 0; y < TT; ++y) E[y] = F[y] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int x = 0; x < DT; ++x) {
-        // rows d = 16 dtile + r of both states, eight (or one) adjacent columns per step
-        const int64_t off = base + (int64_t)(16 * dtile(x) + r) * p.Dv + slab * SP;
+      for (int u = 0; u < 2; ++u) Q[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (q + 1 < pairs) load_rows(q + 1);
 #pragma unroll
-        for (int s = 0; s < NSC; ++s) {
-          const int c = kidx<KSC, STD>(s, g, 0);
-          float vs[KE], vd[KE];
+    for (int s = 0; s < NSC; ++s) {
+      FragT<TI, KSC> fs[NS], fd[NS];
 #pragma unroll
-          for (int j = 0; j < KE; ++j) vs[j] = vd[j] = 0.f;
-          if (c < ncols) {
-            if constexpr (KE == 1) {
-              vs[0] = a.sv[off + c];
-              vd[0] = a.ds[off + c];
-            } else {
+      for (int j = 0; j < KE; ++j) frob += rs[s][j] * rd[s][j];
+      split_frag<TI, KSC, NS>(rs[s], fs);
+      split_frag<TI, KSC, NS>(rd[s], fd);
+      if (q + 1 < pairs) load_state(q + 1, s);
+      if (!mine) continue;
 #pragma unroll
-              for (int j = 0; j < KE; j += 4) {
-                const f32x4 p4 = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(a.sv + off + c + j));
-                const f32x4 q4 = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(a.ds + off + c + j));
+      for (int y = 0; y < TT; ++y) {
+        const FragT<TI, KSC> yf = ld_n<TI, KSC, STD, LX>(sY, 16 * (ttile0 + y), s);
+        const FragT<TI, KSC> xf = ld_n<TI, KSC, STD, LX>(sX, 16 * (ttile0 + y), s);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  vs[j + e] = p4[e];
-                  vd[j + e] = q4[e];
-                }
-              }
-            }
-          }
-          if (NDT >= 4 || w < NDT) {
-#pragma unroll
-            for (int j = 0; j < KE; ++j) frob += vs[j] * vd[j];
-          }
-          FragT<TI, KSC> fs[NS], fd[NS];
-          split_frag<TI, KSC, NS>(vs, fs);
-          split_frag<TI, KSC, NS>(vd, fd);
-#pragma unroll
-          for (int y = 0; y < TT; ++y) {
-            const FragT<TI, KSC> yf = ld_n<TI, KSC, STD, LX>(sY, 16 * ttile(y), s);
-            const FragT<TI, KSC> xf = ld_n<TI, KSC, STD, LX>(sX, 16 * ttile(y), s);
-#pragma unroll
-            for (int m = NS - 1; m >= 0; --m) {
-              E[x][y] = Mf<TI, KSC>::run(fs[m], yf, E[x][y]);
-              F[x][y] = Mf<TI, KSC>::run(fd[m], xf, F[x][y]);
-            }
-          }
+        for (int m = NS - 1; m >= 0; --m) {
+          E[y] = Mf<TI, KSC>::run(fs[m], yf, E[y]);
+          F[y] = Mf<TI, KSC>::run(fd[m], xf, F[y]);
         }
       }
-#pragma unroll
-      for (int u = 0; u < 3; ++u) {
-        if (w + 4 * u >= 10) continue;
-#pragma unroll
-        for (int s = 0; s < NSC; ++s)
-          Q[u] = Mf<TI, KSC>::run(ld_n<TI, KSC, STD, LX>(sX, 16 * jt[u], s), ld_n<TI, KSC, STD, LX>(sY, 16 * it[u], s), Q[u]);
-      }
-    }
-    const float(*gt)[SC] = sh[buf];
-    float dd = 0.f;
-#pragma unroll
-    for (int u = 0; u < 3; ++u) {
-      if (w + 4 * u >= 10) continue;
-      const int i = 16 * it[u] + r, j0 = 16 * jt[u] + 4 * g;
-      const float ih = gt[0][i], il = gt[1][i];
-      const f32x4 jh = ld4(&gt[0][j0]), jl = ld4(&gt[1][j0]), st = ld4(&gt[2][j0]);
-      float row = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float gm = i >= j0 + e ? __builtin_amdgcn_exp2f((ih - jh[e]) + (il - jl[e])) : 0.f;
-        const float gq = i >= j0 + e ? gm * Q[u][e] : 0.f;
-        R[u][e] += gq * st[e];
-        float wv = gq * G[u][e];
-        if (i == j0 + e) {
-          dd += Q[u][e];
-          sdiag[i] = wv;
-          wv = 0.f;
-        }
-        row += wv * st[e];
-        const float cs = row16_sum(wv);
-        if (r == 0) scol[w + 4 * u][4 * g + e] = cs;
-      }
-      row += __shfl_xor(row, 16);
-      row += __shfl_xor(row, 32);
-      if (g == 0) srow[w + 4 * u][r] = row;
     }
 #pragma unroll
-    for (int y = 0; y < TT; ++y) {
-      const int t = 16 * ttile(y) + r;
-      const float eb = gt[3][t], ed = gt[4][t] * gt[2][t];
-      float ce = 0.f, bf = 0.f;
+    for (int u = 0; u < 2; ++u) {
+      if (w + 8 * u >= 10) continue;
 #pragma unroll
-      for (int x = 0; x < DT; ++x) {
-        const int d0 = 16 * dtile(x) + 4 * g;
-        const f32x4 cv = ld4<TI>(sC + LK::at(t, d0)), bv = ld4<TI>(sB + LK::at(t, d0));
+      for (int s = 0; s < NSC; ++s)
+        Q[u] = Mf<TI, KSC>::run(ld_n<TI, KSC, STD, LX>(sX, 16 * jt[u], s), ld_n<TI, KSC, STD, LX>(sY, 16 * it[u], s), Q[u]);
+    }
+    if (slab == a.nslab - 1) {
+      const float(*gt)[SC] = sh[(hh / HB) & 1][hb];
+      float dd = 0.f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (w + 8 * u >= 10) continue;
+        const int i = 16 * it[u] + r, j0 = 16 * jt[u] + 4 * g;
+        const float ih = gt[0][i], il = gt[1][i];
+        const f32x4 jh = ld4(&gt[0][j0]), jl = ld4(&gt[1][j0]), st = ld4(&gt[2][j0]);
+        float row = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          ce += cv[e] * E[x][y][e];
-          bf += bv[e] * F[x][y][e];
+          const float gm = __builtin_amdgcn_exp2f((ih - jh[e]) + (il - jl[e]));
+          const float gq = i >= j0 + e ? gm * Q[u][e] : 0.f;
+          R[u][e] += gq * st[e];
+          float wv = gq * G[u][e];
+          if (i == j0 + e) {
+            dd += Q[u][e];
+            sdiag[hb][i] = wv;
+            wv = 0.f;
+          }
+          row += wv * st[e];
+          const float cs = row16_sum(wv);
+          if (r == 0) scol[hb][w + 8 * u][4 * g + e] = cs;
         }
-        dC[x][y] += eb * E[x][y];
-        dB[x][y] += ed * F[x][y];
+        row += __shfl_xor(row, 16);
+        row += __shfl_xor(row, 32);
+        if (g == 0) srow[hb][w + 8 * u][r] = row;
       }
-      ce += __shfl_xor(ce, 16);
-      ce += __shfl_xor(ce, 32);
-      bf += __shfl_xor(bf, 16);
-      bf += __shfl_xor(bf, 32);
-      if (g == 0) {
-        sE[w][t] = ce;
-        sF[w][t] = bf;
-      }
-    }
-    frob = wave_sum(frob);
-    dd = wave_sum(dd);
-    if (l == 0) {
-      sfr[w] = frob;
-      sdd[w] = dd;
-    }
-    lds_barrier();
-    if (w == 0) {  // one token per lane
-      const int ti = l >> 4;
-      float row = 0.f, col = 0.f;
+      if (mine) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (x <= ti) row += srow[ti * (ti + 1) / 2 + x][r];
-        if (x >= ti) col += scol[x * (x + 1) / 2 + ti][r];
+        for (int y = 0; y < TT; ++y) {
+          const int t = 16 * (ttile0 + y) + r, d0 = 16 * dtile + 4 * g;
+          const float eb = gt[3][t], ed = gt[4][t] * gt[2][t];
+          const f32x4 cv = ld4<TI>(sC + LK::at(t, d0)), bv = ld4<TI>(sB + LK::at(t, d0));
+          float ce = 0.f, bf = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ce += cv[e] * E[y][e];
+            bf += bv[e] * F[y][e];
+          }
+          dC[y] += eb * E[y];
+          dB[y] += ed * F[y];
+          ce += __shfl_xor(ce, 16);
+          ce += __shfl_xor(ce, 32);
+          bf += __shfl_xor(bf, 16);
+          bf += __shfl_xor(bf, 32);
+          if (g == 0) {
+            sE[hb][w][t] = ce;
+            sF[hb][w][t] = bf;
+          }
+        }
       }
-      const float step = gt[2][l], z = gt[5][l];
-      const float ce = gt[3][l] * (sE[0][l] + sE[1][l] + sE[2][l] + sE[3][l]);
-      const float bf = gt[4][l] * (sF[0][l] + sF[1][l] + sF[2][l] + sF[3][l]);
-      const float before = __shfl_up(wave_scan_incl(step * bf), 1);  // (the last token's own term carries no decay)
-      const float q = wave_rscan_incl(row - step * col + ce) + (l > 0 ? before : 0.f) +
-                      sbn[buf] * (sfr[0] + sfr[1] + sfr[2] + sfr[3]);
-      const float na = -expf(p.a_log[h]);
-      const bool live = l < len;
-      const float ddt = live ? (sdiag[l] + col + bf + na * q) / (1.f + expf(-z)) : 0.f;
-      if (live) p.ddt[(t0 + l) * p.Hv + h] = ddt;
-      const float da = wave_sum(live ? q * step * na : 0.f), db = wave_sum(ddt);
+      const float fsum = wave_sum(frob), dsum = wave_sum(dd);
       if (l == 0) {
-        const int64_t at = slot * p.Hv + h, plane = a.slots * p.Hv;
-        a.part[at] = da;
-        a.part[plane + at] = db;
-        a.part[2 * plane + at] = sdd[0] + sdd[1] + sdd[2] + sdd[3];
+        sfr[hb][w] = mine && ttile0 == 0 ? fsum : 0.f;  // (each row of the states once)
+        sdd[hb][w] = dsum;
       }
+      if (hb == HB - 1 || hh == p.r - 1) {
+        lds_barrier();  // the batch's sums are complete
+        const int h0 = hh - hb;
+        if (w <= hb) {  // one head, one token per lane
+          const int h = kh * p.r + h0 + w, ti = l >> 4, b = (h0 / HB) & 1;
+          const float(*gw)[SC] = sh[b][w];
+          float row = 0.f, col = 0.f, ce = 0.f, bf = 0.f, fr = 0.f, dsum8 = 0.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (x <= ti) row += srow[w][ti * (ti + 1) / 2 + x][r];
+            if (x >= ti) col += scol[w][x * (x + 1) / 2 + ti][r];
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            ce += sE[w][x][l];
+            bf += sF[w][x][l];
+            fr += sfr[w][x];
+            dsum8 += sdd[w][x];
+          }
+          const float step = gw[2][l], z = gw[5][l];
+          ce *= gw[3][l];
+          bf *= gw[4][l];
+          const float before = __shfl_up(wave_scan_incl(step * bf), 1);  // (the last token's own term carries no decay)
+          const float qt = wave_rscan_incl(row - step * col + ce) + (l > 0 ? before : 0.f) + sbn[b][w] * fr;
+          const float na = -expf(p.a_log[h]);
+          const bool live = l < len;
+          const float ddt = live ? (sdiag[w][l] + col + bf + na * qt) / (1.f + expf(-z)) : 0.f;
+          if (live) p.ddt[(t0 + l) * p.Hv + h] = ddt;
+          const float da = wave_sum(live ? qt * step * na : 0.f), db = wave_sum(ddt);
+          if (l == 0) {
+            const int64_t at = slot * p.Hv + h, plane = a.slots * p.Hv;
+            a.part[at] = da;
+            a.part[plane + at] = db;
+            a.part[2 * plane + at] = dsum8;
+          }
+        }
+        if (hh + 1 < p.r) {
+          gates(hh + 1);
+          load_dt(hh + 1 + HB);
+        }
+      }
+    }
+    if (q + 1 < pairs) {
+      if constexpr (XB == 1) lds_barrier();  // x and dy are used up
+      rx.store(sXY[XB == 2 ? xb ^ 1 : 0][0]);
+      ry.store(sXY[XB == 2 ? xb ^ 1 : 0][1]);
+      lds_barrier();  // the next step's rows (and gates) are in LDS, the sums of this batch are free
     }
   }
   // the heads' sum of Gamma D Q, and its products with b and c
 #pragma unroll
-  for (int u = 0; u < 3; ++u)
-    if (w + 4 * u < 10) st4<TI>(sR + LX::at(16 * it[u] + r, 16 * jt[u] + 4 * g), R[u]);
+  for (int u = 0; u < 2; ++u)
+    if (w + 8 * u < 10) st4<TI>(sR + LX::at(16 * it[u] + r, 16 * jt[u] + 4 * g), R[u]);
   lds_barrier();
+  if (!mine) return;
 #pragma unroll
   for (int s = 0; s < NSC; ++s) {
-    FragT<TI, KSC> bf[DT], cf[DT];
-#pragma unroll
-    for (int x = 0; x < DT; ++x) {
-      bf[x] = ld_t<TI, KSC, STD, LK>(sB, 16 * dtile(x), s);
-      cf[x] = ld_t<TI, KSC, STD, LK>(sC, 16 * dtile(x), s);
-    }
+    const FragT<TI, KSC> bf = ld_t<TI, KSC, STD, LK>(sB, 16 * dtile, s), cf = ld_t<TI, KSC, STD, LK>(sC, 16 * dtile, s);
 #pragma unroll
     for (int y = 0; y < TT; ++y) {
-      const FragT<TI, KSC> rn = ld_n<TI, KSC, STD, LX>(sR, 16 * ttile(y), s);
-      const FragT<TI, KSC> rt = ld_t<TI, KSC, STD, LX>(sR, 16 * ttile(y), s);
-#pragma unroll
-      for (int x = 0; x < DT; ++x) {
-        dC[x][y] = Mf<TI, KSC>::run(bf[x], rn, dC[x][y]);
-        dB[x][y] = Mf<TI, KSC>::run(cf[x], rt, dB[x][y]);
-      }
+      dC[y] = Mf<TI, KSC>::run(bf, ld_n<TI, KSC, STD, LX>(sR, 16 * (ttile0 + y), s), dC[y]);
+      dB[y] = Mf<TI, KSC>::run(cf, ld_t<TI, KSC, STD, LX>(sR, 16 * (ttile0 + y), s), dB[y]);
     }
   }
 #pragma unroll
   for (int y = 0; y < TT; ++y) {
-    const int t = 16 * ttile(y) + r;
+    const int t = 16 * (ttile0 + y) + r, d0 = kh * DK + 16 * dtile + 4 * g;
     if (t >= len) continue;
-#pragma unroll
-    for (int x = 0; x < DT; ++x) {
-      const int d0 = kh * DK + 16 * dtile(x) + 4 * g;
-      st4<TI>((TI*)p.dc + (t0 + t) * p.dc_rs + d0, dC[x][y]);
-      st4<TI>((TI*)p.db + (t0 + t) * p.db_rs + d0, dB[x][y]);
-    }
+    st4<TI>((TI*)p.dc + (t0 + t) * p.dc_rs + d0, dC[y]);
+    st4<TI>((TI*)p.db + (t0 + t) * p.db_rs + d0, dB[y]);
   }
 }
 
 template <typename TI> static hipError_t grad_d(const GradArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)(a.slots * a.p.Hk);
   switch (a.p.Dk) {
-    case 16: traced("k_ssm_grad", s, [&] { k_ssm_grad<TI, 16><<<grid, 256, 0, s>>>(a); }); break;
-    case 32: traced("k_ssm_grad", s, [&] { k_ssm_grad<TI, 32><<<grid, 256, 0, s>>>(a); }); break;
-    case 64: traced("k_ssm_grad", s, [&] { k_ssm_grad<TI, 64><<<grid, 256, 0, s>>>(a); }); break;
-    case 128: traced("k_ssm_grad", s, [&] { k_ssm_grad<TI, 128><<<grid, 256, 0, s>>>(a); }); break;
+    case 16: traced("k_ssm_grad", s, [&] { k_ssm_grad<TI, 16><<<grid, 512, 0, s>>>(a); }); break;
+    case 32: traced("k_ssm_grad", s, [&] { k_ssm_grad<TI, 32><<<grid, 512, 0, s>>>(a); }); break;
+    case 64: traced("k_ssm_grad", s, [&] { k_ssm_grad<TI, 64><<<grid, 512, 0, s>>>(a); }); break;
+    case 128: traced("k_ssm_grad", s, [&] { k_ssm_grad<TI, 128><<<grid, 512, 0, s>>>(a); }); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();

@@ -71,6 +71,15 @@ __device__ __forceinline__ void acc_split(const f32x4* t, int s, FragT<TI, KS> (
   split_frag<TI, KS, NS>(v, o);
 }
 
+// Sum over the four lanes that share l % 16, in each of them: the halves of the wave exchanged, then
+// the halves of each half.
+__device__ __forceinline__ float group4_sum(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 // Four adjacent values of a row as float32, and back.
 template <typename TI> __device__ __forceinline__ f32x4 ld4(const TI* p) {
   if constexpr (sizeof(TI) == 2) {

@@ -48,18 +48,29 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
   __shared__ __align__(16) TI sR[SC * SC];
   __shared__ __align__(16) float sh[2][HB][6][SC];  // gamma, its remainder, step, 2^gamma, e, dt + bias
   __shared__ float sbn[2][HB];
-  __shared__ float srow[HB][10][16], scol[HB][10][16], sdiag[HB][SC], sE[HB][8][SC], sF[HB][8][SC], sfr[HB][8], sdd[HB][8];
+  __shared__ __align__(16) float srow[HB][10][16], scol[HB][10][16];
+  __shared__ float sdiag[HB][SC], sE[HB][8][SC], sF[HB][8][SC], sfr[HB][8], sdd[HB][8];
 
   const int kh = (int)(blockIdx.x % p.Hk);
   const int64_t slot = blockIdx.x / p.Hk;
   const int w = wave_id(), l = lane_id(), g = l >> 4, r = l & 15;
-  // the slot's sequence: the largest n whose first slot is not behind it
+  // the slot's sequence: the largest n whose first slot is not behind it, 64 probes at a time
   int n = 0;
   int64_t lo, hi;
-  for (int top = p.N; top - n > 1;) {
-    const int m = (n + top) >> 1;
-    ssm_seq(p.cu, p.T, p.T_total, m, lo, hi);
-    if (lo / SC + m <= slot) n = m; else top = m;
+  if (p.cu || p.N > 1) {
+    for (int m = p.N; m > 1;) {
+      const int stride = (m + 63) / 64, i = l * stride;
+      bool in = false;
+      if (i < m) {
+        int64_t x = p.cu ? (int64_t)p.cu[n + i] : (int64_t)(n + i) * p.T;
+        x = x < 0 ? 0 : (x > p.T_total ? p.T_total : x);
+        in = x / SC + n + i <= slot;
+      }
+      const uint64_t hit = __ballot(in);
+      const int at = (hit ? 63 - __builtin_clzll(hit) : 0) * stride;
+      n += at;
+      m = m - at < stride ? m - at : stride;
+    }
   }
   ssm_seq(p.cu, p.T, p.T_total, n, lo, hi);
   const int64_t k = slot - (lo / SC + n);
@@ -216,24 +227,34 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
         const int i = 16 * it[u] + r, j0 = 16 * jt[u] + 4 * g;
         const float ih = gt[0][i], il = gt[1][i];
         const f32x4 jh = ld4(&gt[0][j0]), jl = ld4(&gt[1][j0]), st = ld4(&gt[2][j0]);
-        float row = 0.f;
+        const bool diag = it[u] == jt[u];  // (wave-uniform; below it every pair is in)
+        f32x4 wv;
+        float row = 0.f, dg = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float gm = __builtin_amdgcn_exp2f((ih - jh[e]) + (il - jl[e]));
-          const float gq = i >= j0 + e ? gm * Q[u][e] : 0.f;
+          float gq = __builtin_amdgcn_exp2f((ih - jh[e]) + (il - jl[e])) * Q[u][e];
+          if (diag) gq = i >= j0 + e ? gq : 0.f;
           R[u][e] += gq * st[e];
-          float wv = gq * G[u][e];
-          if (i == j0 + e) {
-            dd += Q[u][e];
-            sdiag[hb][i] = wv;
-            wv = 0.f;
+          wv[e] = gq * G[u][e];
+          if (diag) {
+            dd += i == j0 + e ? Q[u][e] : 0.f;
+            dg = i == j0 + e ? wv[e] : dg;
+            wv[e] = i == j0 + e ? 0.f : wv[e];
           }
-          row += wv * st[e];
-          const float cs = row16_sum(wv);
-          if (r == 0) scol[hb][w + 8 * u][4 * g + e] = cs;
+          row += wv[e] * st[e];
         }
-        row += __shfl_xor(row, 16);
-        row += __shfl_xor(row, 32);
+        if (diag && (r >> 2) == g) sdiag[hb][i] = dg;
+        row = group4_sum(row);
+        // column sums over the tile's 16 lanes, four columns side by side
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wv[e] += dpp<0xB1>(wv[e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wv[e] += dpp<0x4E>(wv[e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wv[e] += dpp<0x141>(wv[e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wv[e] += dpp<0x140>(wv[e]);
+        if (r == 0) *reinterpret_cast<f32x4*>(&scol[hb][w + 8 * u][4 * g]) = wv;
         if (g == 0) srow[hb][w + 8 * u][r] = row;
       }
       if (mine) {
@@ -242,18 +263,16 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
           const int t = 16 * (ttile0 + y) + r, d0 = 16 * dtile + 4 * g;
           const float eb = gt[3][t], ed = gt[4][t] * gt[2][t];
           const f32x4 cv = ld4<TI>(sC + LK::at(t, d0)), bv = ld4<TI>(sB + LK::at(t, d0));
-          float ce = 0.f, bf = 0.f;
+          float ce = cv[0] * E[y][0], bf = bv[0] * F[y][0];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 1; e < 4; ++e) {
             ce += cv[e] * E[y][e];
             bf += bv[e] * F[y][e];
           }
           dC[y] += eb * E[y];
           dB[y] += ed * F[y];
-          ce += __shfl_xor(ce, 16);
-          ce += __shfl_xor(ce, 32);
-          bf += __shfl_xor(bf, 16);
-          bf += __shfl_xor(bf, 32);
+          ce = group4_sum(ce);
+          bf = group4_sum(bf);
           if (g == 0) {
             sE[hb][w][t] = ce;
             sF[hb][w][t] = bf;

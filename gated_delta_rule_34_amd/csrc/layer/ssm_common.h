@@ -17,6 +17,15 @@ namespace gdn {
 constexpr int SC = 64;  // tokens per chunk
 constexpr int SP = 64;  // columns of x per workgroup (a head's slab)
 
+// Rows of Cn elements in LDS, 16 bytes apart from one another: reads of 16 rows at one column and the
+// transposed reads of 4 rows fall in different banks, and the addresses of a lane's reads differ by
+// constants (the permuted layouts of gdn_frag.h took some 25 registers more for them).
+template <typename T, int Cn> struct PadRow {
+  static constexpr int LD = Cn + 16 / (int)sizeof(T);
+  static constexpr int size(int R) { return R * LD; }
+  __device__ __forceinline__ static int at(int r, int c) { return r * LD + c; }
+};
+
 // bfloat16 terms that a float32 factor is split into as a matrix operand: three (24 bits) where
 // the result is float32, one where it is rounded to bfloat16 anyway.
 template <typename TI> constexpr int ssm_split() { return sizeof(TI) == 2 ? 3 : 1; }

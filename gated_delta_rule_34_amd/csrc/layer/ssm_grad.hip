@@ -40,10 +40,10 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
   constexpr int TT = NDT == 8 ? 4 : NDT == 4 ? 2 : 1;   // token tiles of a wave's [16 of Dk][64 tokens] products
   constexpr int HB = sizeof(TI) == 4 ? 2 : 8;           // heads whose scans are done together
   constexpr int XB = sizeof(TI) == 4 ? 1 : 2;           // buffers of x and dy
-  using LK = Swz<TI, DK, true>;
+  using LK = PadRow<TI, DK>;
   using LX = Swz<TI, SP, true>;
-  __shared__ __align__(16) TI sB[SC * DK];
-  __shared__ __align__(16) TI sC[SC * DK];
+  __shared__ __align__(16) TI sB[LK::size(SC)];
+  __shared__ __align__(16) TI sC[LK::size(SC)];
   __shared__ __align__(16) TI sXY[XB][2][SC * SP];
   __shared__ __align__(16) TI sR[SC * SC];
   __shared__ __align__(16) float sh[2][HB][6][SC];  // gamma, its remainder, step, 2^gamma, e, dt + bias

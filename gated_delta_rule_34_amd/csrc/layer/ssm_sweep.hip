@@ -7,8 +7,9 @@
 // and the two halves' shares of S^T Q meet in LDS. Per chunk the products K Q^T, S^T Q, K^T (w X) and
 // M X run on the matrix cores; every product is formed transposed, so that a lane holds four adjacent
 // columns of one token. The next chunk's rows are in registers while a chunk is computed. A chunk is
-// a chain of short dependent products, bound by their latency: eight waves of 128 registers, so that
-// two workgroups (four waves per SIMD) share a compute unit, hide what four waves of 230 did not.
+// a chain of short dependent products, bound by their latency and the LDS: eight waves of 128 registers,
+// so that two workgroups (four waves per SIMD) share a compute unit, hide what four waves of 230 (or one
+// workgroup of eight with 165) did not.
 //
 // Few sequences and heads leave compute units idle over a long serial chain, so a sequence is then
 // cut into S segments: a first launch runs the state alone over all segments but the last, from
@@ -36,15 +37,15 @@ struct SweepArgs {
 // output), the decays with which a token reads and writes the state.
 enum { G_HI, G_LO, G_IN, G_RD, G_WR, G_ROWS };
 
-template <typename TI, int DK> constexpr int sweep_waves() { return 2; }  // per SIMD
+template <typename TI, int DK> constexpr int sweep_waves() { return sizeof(TI) == 4 ? 2 : 4; }  // per SIMD
 
 template <typename TI, int DK, bool REV, bool OUT>
 __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(SweepArgs a) {
   constexpr int NT = 512, DH = DK >= 32 ? DK / 2 : 16, ND = DH / 16;  // this wave's rows of the state
   constexpr int KSD = ks_of<TI, DK>(), NSD = DK / KSD, KSC = ks_of<TI, SC>(), NSC = SC / KSC;
   constexpr int KSH = ks_of<TI, DH>(), NSH = DH / KSH;
-  constexpr int NS = ssm_split<TI>(), TRI = REV ? TRI_UP : TRI_LOW;
-  using LK = Swz<TI, DK, true, DK * sizeof(TI) >= 64>;
+  constexpr int NS = ssm_split<TI>(), TRI = REV ? TRI_UP : TRI_LOW, GB = 2;
+  using LK = PadRow<TI, DK>;
   using LX = Swz<TI, SP, true>;
   using LM = Swz<TI, SC, false>;
   __shared__ __align__(16) TI sK[LK::size(SC)];
@@ -52,8 +53,8 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   __shared__ __align__(16) TI sX2[2][SC * SP];
   __shared__ __align__(16) TI sM[OUT ? SC * SC : 8];
   __shared__ __align__(16) f32x4 sP[OUT ? 8 * 2 * 64 : 1];  // shares of S^T Q for the other half
-  __shared__ __align__(16) float sg[16][G_ROWS][SC];
-  __shared__ float sbn[16];
+  __shared__ __align__(16) float sg[2 * GB][G_ROWS][SC];
+  __shared__ float sbn[2 * GB];
 
   const int segs = OUT ? a.S : a.S - 1;
   int grp, mem;
@@ -92,9 +93,9 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   if constexpr (OUT) rq.init(a.q_rs, DK);
   rx.init(a.x_rs, ncols);
   const uint32_t orow = (uint32_t)a.o_rs * (uint32_t)sizeof(TI);
-  // Gates come eight chunks at a time, one for each wave (a chunk's are a long chain of dependent
-  // operations: by one wave, chunk by chunk, they took a fifth of the step).
-  float rdt = 0.f;  // dt of this wave's chunk of the next eight
+  // Gates come GB chunks at a time, one for each of GB waves: a chunk's are a long chain of dependent
+  // operations that by one wave in every chunk took a fifth of the step.
+  float rdt = 0.f;  // dt of this wave's chunk of the next ones
   auto load = [&](int k) {
     const int c = chunk(k), len = clen(c);
     const int64_t t0 = lo + (int64_t)c * SC;
@@ -104,19 +105,20 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   };
   auto load_dt = [&](int k) {
     const int c = chunk(k);
-    rdt = k < k1 && l < clen(c) ? a.dt[(lo + (int64_t)c * SC + l) * a.Hv + h] : 0.f;
+    rdt = w < GB && k < k1 && l < clen(c) ? a.dt[(lo + (int64_t)c * SC + l) * a.Hv + h] : 0.f;
   };
   auto gates = [&](int k) {
+    if (w >= GB) return;
     const bool valid = k < k1 && l < clen(chunk(k));
     const Gate q = chunk_gate(rdt, bias, neg_a, valid);
     const float hi32 = (float)q.gam, eb = __builtin_amdgcn_exp2f(hi32), ee = __builtin_amdgcn_exp2f((float)(q.tot - q.gam));
-    float(*gt)[SC] = sg[(k - k0) & 15];
+    float(*gt)[SC] = sg[(k - k0) & (2 * GB - 1)];
     gt[G_HI][l] = hi32;
     gt[G_LO][l] = (float)(q.gam - (double)hi32);
     gt[G_IN][l] = q.step;
     gt[G_RD][l] = REV ? ee : eb;
     gt[G_WR][l] = REV ? (valid ? eb : 0.f) : ee * q.step;
-    if (l == 63) sbn[(k - k0) & 15] = __builtin_amdgcn_exp2f((float)q.tot);
+    if (l == 63) sbn[(k - k0) & (2 * GB - 1)] = __builtin_amdgcn_exp2f((float)q.tot);
   };
   if (k0 < k1) {
     load_dt(k0 + w);
@@ -161,7 +163,7 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   if (k0 < k1) {
     if (OUT && a.sv && has) save(k0);
     gates(k0 + w);
-    load_dt(k0 + 8 + w);
+    load_dt(k0 + GB + w);
     rk.store(sK);
     if constexpr (OUT) rq.store(sQ);
     rx.store(sX2[k0 & 1]);
@@ -172,8 +174,8 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
     const TI* sX = sX2[buf];
     lds_barrier();  // the chunk's rows and gates are in LDS, M and the shares are free
     if (k + 1 < k1) load(k + 1);
-    const float(*gt)[SC] = sg[(k - k0) & 15];
-    const float bn = sbn[(k - k0) & 15];
+    const float(*gt)[SC] = sg[(k - k0) & (2 * GB - 1)];
+    const float bn = sbn[(k - k0) & (2 * GB - 1)];
     f32x4 o[4];
     if constexpr (OUT) {
       // M = Gamma o (Q K^T) o inputs' weights: its ten tiles dealt over the waves
@@ -269,9 +271,9 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
       }
     }
     if (k + 1 < k1) {
-      if (((k + 1 - k0) & 7) == 0) {  // the next eight chunks' gates
+      if (((k + 1 - k0) & (GB - 1)) == 0) {  // the next chunks' gates
         gates(k + 1 + w);
-        load_dt(k + 9 + w);
+        load_dt(k + 1 + GB + w);
       }
       rk.store(sK);
       if constexpr (OUT) rq.store(sQ);
@@ -295,9 +297,11 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   }
 }
 
-// Segments per sequence: enough workgroups for the chip, each with at least kMinChunks chunks on
-// average (a segment costs its states and a second read of its rows).
-constexpr int kWantGroups = 256, kMinChunks = 4, kMaxSegments = 32;
+// Segments per sequence: two workgroups to a compute unit, each with at least kMinChunks chunks on
+// average. A segment costs its states and a second read of its rows, so two gain nothing (4 x 4096
+// tokens, 64 heads: one segment 243 us, two 247), more do (16384 tokens, 32 heads: 8 of them 180 us,
+// 16 of them 150; without any some 900).
+constexpr int kWantGroups = 512, kMinChunks = 4, kMaxSegments = 32;
 static int ssm_segments(const SsmArgs& a) {
   if (a.N == 0) return 1;
   const int64_t groups = (int64_t)a.N * a.Hv * ((a.Dv + SP - 1) / SP);
@@ -305,7 +309,7 @@ static int ssm_segments(const SsmArgs& a) {
   const int64_t most = a.T_total / SC / a.N / kMinChunks;
   if (s > most) s = most;
   if (s > kMaxSegments) s = kMaxSegments;
-  return s < 1 ? 1 : (int)s;
+  return s <= 2 ? 1 : (int)s;
 }
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }

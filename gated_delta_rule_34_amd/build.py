@@ -1,10 +1,12 @@
-"""Build libgdn.so (HIP kernels for gfx950 + the C ABI) in-tree with hipcc."""
+"""Build libgdn.so (HIP kernels for gfx950 + the C ABI) in-tree with hipcc, and the binding's module
+_marshal.so with the host compiler."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -37,8 +39,20 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _marshal() -> None:
+    """The binding's C module (no GPU code)."""
+    out = os.path.join(PKG, "_marshal.so")
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", f"-I{sysconfig.get_paths()['include']}",
+           os.path.join(CSRC, "layer", "marshal.c"), "-o", out + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for marshal.c:\n{r.stderr}")
+    os.replace(out + ".tmp", out)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
+    _marshal()
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB + ".tmp"

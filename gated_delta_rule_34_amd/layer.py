@@ -15,6 +15,12 @@ import functools
 
 from . import GDN_BF16, GDN_F32, GDN_OK, GdnError, _empty_bytes, _lib, gdn_conv_problem
 
+try:
+    from . import _marshal
+except ImportError as e:
+    raise ImportError("gated_delta_rule_34_amd/_marshal.so is missing: build the package first "
+                      "(python gated_delta_rule_34_amd/build.py, or __graft_entry__.build())") from e
+
 P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
 
@@ -64,15 +70,21 @@ def _fn(name):
     return fn
 
 
+_address = {}
+
+
 def _call(name, p, *args):
-    st = (_bound.get(name) or _fn(name))(p, *args)
+    at = _address.get(name)
+    if at is None:
+        at = _address[name] = ctypes.cast(_fn(name), ctypes.c_void_p).value
+    st = _marshal.call(at, p, *args)
     if st != GDN_OK:
         raise GdnError(st, name)
 
 
 # ------------------------------------------------------------------------------------ checks
-# A single token's kernels take a few microseconds, and so do careless checks of their ten tensors:
-# these look at each tensor once, with the cheapest calls that torch has.
+# A single token's kernels take a few microseconds, and so would checks of their ten tensors in Python:
+# _marshal looks at each tensor, and what it does not accept is explained here.
 
 _torch = _types = _f32 = _i32 = _raw_stream = None
 
@@ -109,33 +121,22 @@ def _rows(t, name, rows, width, device, dtype):
     """(address, row stride) of a [rows, width] view, or [rows, heads, D] with contiguous heads."""
     if t is None:
         raise ValueError(f"{name}: missing")
-    shape, st = t.shape, t.stride()
-    if len(shape) == 3:
-        flat = st[2] == 1 and (shape[1] == 1 or st[1] == shape[2])
-        inner = shape[1] * shape[2]
-    elif len(shape) == 2:
-        flat, inner = st[1] == 1, shape[1]
-    else:
-        flat = inner = None
-    if inner != width or shape[0] != rows or t.dtype is not dtype or t.get_device() != device:
-        raise ValueError(f"{name}: expected {rows} rows of {width} of {dtype} on cuda:{device}, got {tuple(shape)} of {t.dtype} on {t.device}")
-    if rows > 1:
-        if not flat:
-            raise ValueError(f"{name}: rows must be contiguous")
-        return t.data_ptr(), st[0]
-    if rows == 1 and not flat and width > 1:
-        raise ValueError(f"{name}: rows must be contiguous")
-    return t.data_ptr(), width  # no second row to address
+    at = _marshal.rows(t, rows, width, device, dtype)
+    if at is None:
+        raise ValueError(f"{name}: expected {rows} rows of {width} contiguous values of {dtype} on cuda:{device}, "
+                         f"got {tuple(t.shape)} with strides {t.stride()} of {t.dtype} on {t.device}")
+    return at
 
 
 def _array(t, name, shape, device, dtype):
     """Address of a contiguous tensor of `shape`."""
     if t is None:
         raise ValueError(f"{name}: missing")
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+    at = _marshal.array(t, shape, device, dtype)
+    if at is None:
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on cuda:{device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return at
 
 
 def _scratch(t, device):

@@ -236,8 +236,8 @@ __global__ __launch_bounds__(NT) void k_norm_bwd(NormArgs a, int L, int gpb) {
           o.v[i] = a.gate_first ? dv * gt : dv;
           o2.v[i] = (a.gate_first ? dv * xx.v[i] : dy[j].v[i] * n * w[j].v[i]) * gd;
         }
-        st8<TI>((TI*)a.o + row * a.o_rs + gc + c, o);
-        st8<TI>((TI*)a.o2 + row * a.o2_rs + gc + c, o2);
+        st8nt<TI>((TI*)a.o + row * a.o_rs + gc + c, o);
+        st8nt<TI>((TI*)a.o2 + row * a.o2_rs + gc + c, o2);
       } else {
         F8 yy, up = zero8();
         if (a.ds) yy = cvt8<TI>(rz[j]);
@@ -250,8 +250,8 @@ __global__ __launch_bounds__(NT) void k_norm_bwd(NormArgs a, int L, int gpb) {
           if (a.ds) ds[j].v[i] += o.v[i] * yy.v[i];
           o2.v[i] = sv[j].v[i] * o.v[i];
         }
-        st8<TI>((TI*)a.o + row * a.o_rs + c, o);
-        if (a.o2) st8<TI>((TI*)a.o2 + row * a.o2_rs + c, o2);
+        st8nt<TI>((TI*)a.o + row * a.o_rs + c, o);
+        if (a.o2) st8nt<TI>((TI*)a.o2 + row * a.o2_rs + c, o2);
       }
     }
   }
@@ -301,9 +301,10 @@ __global__ __launch_bounds__(NT) void k_norm_bwd(NormArgs a, int L, int gpb) {
 }
 
 // Column sums of the planes [R][W] behind one another (grid y: the plane; its output may be
-// nullptr): a workgroup takes 16 columns, 16 threads each walk down every 16th row.
-__global__ __launch_bounds__(256) void k_colsum(const float* in, int64_t R, int W, ColsumOut o) {
-  __shared__ float part[16][17];
+// nullptr): a workgroup takes 16 columns, 64 threads each walk down every 64th row (a few hundred rows
+// of dependent loads are a matter of latency: 16 threads took 9.8 us for 2048 x 128, 64 take 5).
+__global__ __launch_bounds__(1024) void k_colsum(const float* in, int64_t R, int W, ColsumOut o) {
+  __shared__ float part[64][17];
   const int c = (int)(threadIdx.x & 15), k = (int)(threadIdx.x >> 4), col = (int)blockIdx.x * 16 + c;
   float* out = o.p[blockIdx.y];
   if (!out) return;
@@ -311,25 +312,30 @@ __global__ __launch_bounds__(256) void k_colsum(const float* in, int64_t R, int 
   float q = 0.f;
   if (col < W) {
 #pragma unroll 8
-    for (int64_t r = k; r < R; r += 16) q += in[r * W + col];
+    for (int64_t r = k; r < R; r += 64) q += in[r * W + col];
   }
   part[k][c] = q;
   __syncthreads();
-  if (k == 0 && col < W) {
+  if (k < 4) {  // one wave: 16 rows each, then the four of them
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += part[i][c];
-    out[col] = s;
+    for (int i = 0; i < 16; ++i) s += part[k * 16 + i][c];
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (k == 0 && col < W) out[col] = s;
   }
 }
 
 hipError_t launch_colsum(const float* in, int64_t R, int W, const ColsumOut& o, int planes, hipStream_t s) {
-  traced("k_colsum", s, [&] { k_colsum<<<dim3((unsigned)((W + 15) / 16), (unsigned)planes), 256, 0, s>>>(in, R, W, o); });
+  traced("k_colsum", s, [&] { k_colsum<<<dim3((unsigned)((W + 15) / 16), (unsigned)planes), 1024, 0, s>>>(in, R, W, o); });
   return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ launches
-// Backward grid: about two workgroups per compute unit and no more row splits than passes.
+// Backward grid. A workgroup-wide group holds some 200 registers a thread and two rows in flight per
+// compute unit's SIMD fill it (two workgroups each; more only cost partials: 16384 x 5120 takes 213 us,
+// with four 230); groups inside a wave are small, and eight workgroups keep enough loads in flight
+// (16384 x 48 x 128: 216 us, with two 273). No more row splits than passes.
 struct BwdGrid {
   int gpb, splits, blocks;
 };
@@ -339,7 +345,7 @@ static BwdGrid bwd_grid(const NormArgs& a, const NormPlan& p) {
   g.gpb = a.groups < slots ? a.groups : slots;
   g.blocks = (a.groups + g.gpb - 1) / g.gpb;
   const int64_t passes = (a.rows + slots / g.gpb - 1) / (slots / g.gpb);
-  int64_t want = (512 + g.blocks - 1) / g.blocks;
+  int64_t want = ((p.blk ? 512 : 2048) + g.blocks - 1) / g.blocks;
   if (want > passes) want = passes;
   g.splits = (int)(want < 1 ? 1 : want);
   return g;

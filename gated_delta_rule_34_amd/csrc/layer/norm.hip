@@ -62,6 +62,15 @@ template <bool BLK, int NT> __device__ __forceinline__ float group_sum(float x, 
   }
 }
 
+// The residual before its rounding: product and sum rounded one after the other, as the elementary
+// operations are (a fused one would round a few of 10^5 bfloat16 residuals to the other neighbour, which
+// every later value then shows).
+__device__ __forceinline__ float residual(float h, float f, float y) {
+#pragma clang fp contract(off)
+  const float p = f * y;
+  return h + p;
+}
+
 __device__ __forceinline__ float silu_grad(float z, float sg) { return sg * (1.f + z * (1.f - sg)); }
 
 // ------------------------------------------------------------------ forward
@@ -105,7 +114,7 @@ __global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a, int L) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float f = a.s ? a.scale * sv.v[i] : a.scale;
-          v[j].v[i] = (float)(TI)(xx.v[i] + f * zz.v[i]);  // as the residual is stored
+          v[j].v[i] = (float)(TI)residual(xx.v[i], f, zz.v[i]);  // as the residual is stored
         }
         st8<TI>((TI*)a.o + (int64_t)row * a.o_rs + c, v[j]);
       } else {
@@ -302,27 +311,28 @@ __global__ __launch_bounds__(NT) void k_norm_bwd(NormArgs a, int L, int gpb) {
 
 // Column sums of the planes [R][W] behind one another (grid y: the plane; its output may be
 // nullptr): a workgroup takes 16 columns, 64 threads each walk down every 64th row (a few hundred rows
-// of dependent loads are a matter of latency: 16 threads took 9.8 us for 2048 x 128, 64 take 5).
+// of dependent loads are a matter of latency: 16 threads took 9.8 us for 2048 x 128, 64 take 6). Sums
+// over tokens cancel: the partials are float32, their sum runs in 64 bits.
 __global__ __launch_bounds__(1024) void k_colsum(const float* in, int64_t R, int W, ColsumOut o) {
-  __shared__ float part[64][17];
+  __shared__ double part[64][17];
   const int c = (int)(threadIdx.x & 15), k = (int)(threadIdx.x >> 4), col = (int)blockIdx.x * 16 + c;
   float* out = o.p[blockIdx.y];
   if (!out) return;
   in += (int64_t)blockIdx.y * R * W;
-  float q = 0.f;
+  double q = 0.0;
   if (col < W) {
 #pragma unroll 8
-    for (int64_t r = k; r < R; r += 64) q += in[r * W + col];
+    for (int64_t r = k; r < R; r += 64) q += (double)in[r * W + col];
   }
   part[k][c] = q;
   __syncthreads();
   if (k < 4) {  // one wave: 16 rows each, then the four of them
-    float s = 0.f;
+    double s = 0.0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s += part[k * 16 + i][c];
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (k == 0 && col < W) out[col] = s;
+    if (k == 0 && col < W) out[col] = (float)s;
   }
 }
 

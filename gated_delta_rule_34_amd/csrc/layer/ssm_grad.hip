@@ -13,7 +13,7 @@
 // strong decays it would drown q). The two products with Gamma D Q are linear in
 // it, so they run once per group on the sum over its heads. b, c, x, dy are exact as bfloat16
 // operands; the states are split over three (24 bits), so that the float32 results keep float32
-// accuracy. Bound by HBM: the two states of a chunk and head are 8 Dk Dv bytes.
+// accuracy, and Gamma D Q over two, so that db and dc carry no rounding but their own. Bound by HBM: the two states of a chunk and head are 8 Dk Dv bytes.
 //
 // Eight waves: wave w holds 16 rows of Dk (all tokens; with a smaller state some tokens) and one or two
 // tiles of the tokens' triangle. The next head's rows and states are on their way while a head is
@@ -45,7 +45,8 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
   __shared__ __align__(16) TI sB[LK::size(SC)];
   __shared__ __align__(16) TI sC[LK::size(SC)];
   __shared__ __align__(16) TI sXY[XB][2][SC * SP];
-  __shared__ __align__(16) TI sR[SC * SC];
+  constexpr int NR = sizeof(TI) == 4 ? 1 : 2;           // terms of Gamma D Q as an operand
+  __shared__ __align__(16) TI sR[NR][SC * SC];
   __shared__ __align__(16) float sh[2][HB][6][SC];  // gamma, its remainder, step, 2^gamma, e, dt + bias
   __shared__ float sbn[2][HB];
   __shared__ __align__(16) float srow[HB][10][16], scol[HB][10][16];
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
     load_rows(0);
 #pragma unroll
     for (int s = 0; s < NSC; ++s) load_state(0, s);
-    for (int i = threadIdx.x; i < SC * SC; i += NT) sR[i] = (TI)0.f;
+    for (int i = threadIdx.x; i < NR * SC * SC; i += NT) sR[0][i] = (TI)0.f;
     for (int i = threadIdx.x; i < HB * 8 * SC; i += NT) (&sE[0][0][0])[i] = (&sF[0][0][0])[i] = 0.f;
     rb.store(sB);
     rc.store(sC);
@@ -336,7 +337,16 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
   // the heads' sum of Gamma D Q, and its products with b and c
 #pragma unroll
   for (int u = 0; u < 2; ++u)
-    if (w + 8 * u < 10) st4<TI>(sR + LX::at(16 * it[u] + r, 16 * jt[u] + 4 * g), R[u]);
+    if (w + 8 * u < 10) {
+      f32x4 rest = R[u];
+#pragma unroll
+      for (int m = 0; m < NR; ++m) {
+        TI* at = sR[m] + LX::at(16 * it[u] + r, 16 * jt[u] + 4 * g);
+        st4<TI>(at, rest);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rest[e] -= (float)(TI)rest[e];
+      }
+    }
   lds_barrier();
   if (!mine) return;
 #pragma unroll
@@ -344,8 +354,11 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
     const FragT<TI, KSC> bf = ld_t<TI, KSC, STD, LK>(sB, 16 * dtile, s), cf = ld_t<TI, KSC, STD, LK>(sC, 16 * dtile, s);
 #pragma unroll
     for (int y = 0; y < TT; ++y) {
-      dC[y] = Mf<TI, KSC>::run(bf, ld_n<TI, KSC, STD, LX>(sR, 16 * (ttile0 + y), s), dC[y]);
-      dB[y] = Mf<TI, KSC>::run(cf, ld_t<TI, KSC, STD, LX>(sR, 16 * (ttile0 + y), s), dB[y]);
+#pragma unroll
+      for (int m = NR - 1; m >= 0; --m) {
+        dC[y] = Mf<TI, KSC>::run(bf, ld_n<TI, KSC, STD, LX>(sR[m], 16 * (ttile0 + y), s), dC[y]);
+        dB[y] = Mf<TI, KSC>::run(cf, ld_t<TI, KSC, STD, LX>(sR[m], 16 * (ttile0 + y), s), dB[y]);
+      }
     }
   }
 #pragma unroll

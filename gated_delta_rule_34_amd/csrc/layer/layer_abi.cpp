@@ -71,7 +71,7 @@ gdn_status check_ssm(const gdn_ssm_problem* p) {
   // one workgroup per (sequence, head, 64 columns), per (row, head) and per (chunk, group)
   constexpr int64_t most = kMaxBlocks / 2;  // (of up to 512 threads)
   const int64_t slabs = p->Dv > 64 ? 2 : 1, slots = p->T_total / 64 + p->N;
-  if ((int64_t)(p->N + 8) * p->Hv > most / slabs || slots > most / p->Hv) return GDN_EINVAL;
+  if (((int64_t)p->N + 8) * p->Hv > most / slabs || slots > most / p->Hv) return GDN_EINVAL;
   GDN_TRY(check_arr(p->a_log, true));
   GDN_TRY(check_arr(p->dt_bias, false));
   return check_arr(p->d_skip, false);
@@ -206,9 +206,10 @@ gdn_status gdn_ssm_fwd(const gdn_ssm_problem* p, const void* x, int64_t x_rs, co
   gdn::SsmArgs a = ssm_args(p);
   GDN_TRY(ssm_inputs(p, x, x_rs, b, b_rs, c, c_rs, dt, a));
   GDN_TRY(ssm_view(y, y_rs, (int64_t)p->Hv * p->Dv, p->dtype, p->T_total));
+  if (p->T_total > 0 && (y == x || y == b || y == c)) return GDN_EINVAL;  // outputs must not overlap inputs
   GDN_TRY(check_arr(S0, false, 16));
   GDN_TRY(check_arr(S_T, false, 16));
-  if (S0 && S0 == S_T) return GDN_EINVAL;  // they must not overlap
+  if (S0 && S0 == S_T) return GDN_EINVAL;
   GDN_TRY(check_arr(chunk_states, false, 16));
   GDN_TRY(check_ws(workspace, workspace_bytes, gdn::ssm_fwd_ws_bytes(a)));
   if (p->N == 0) return GDN_OK;
@@ -231,6 +232,8 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_problem* p, const void* x, int64_t x_rs, co
   GDN_TRY(ssm_view(dx, dx_rs, xw, p->dtype, p->T_total));
   GDN_TRY(ssm_view(db, db_rs, kw, p->dtype, p->T_total));
   GDN_TRY(ssm_view(dc, dc_rs, kw, p->dtype, p->T_total));
+  // dx is written before x and dy are read for the last time
+  if (p->T_total > 0 && (dx == x || dx == dy || db == b || dc == c || ddt == dt)) return GDN_EINVAL;
   GDN_TRY(check_arr(ddt, p->T_total > 0));
   GDN_TRY(check_arr(da_log, false));
   GDN_TRY(check_arr(ddt_bias, false));
@@ -274,6 +277,7 @@ gdn_status gdn_conv1d_silu_prompt(const gdn_conv_problem* p, const void* x, int6
   GDN_TRY(check_arr(first, false, 16));
   GDN_TRY(check_arr(last, false, 16));
   if (first && first == last && p->N > 0 && p->kernel_size > 1) return GDN_EINVAL;  // they must not overlap
+  if (p->T_total > 0 && y == x) return GDN_EINVAL;
   gdn::ConvCarryArgs a = conv_args(p, x, x_rs, w, bias, y, y_rs);
   a.first = first;
   a.last = last;

@@ -6,7 +6,8 @@ residual addition with its norm (``gdn_gated_norm_*``, ``gdn_add_norm_*``). As i
 itself the functions keep the C names and only marshal tensors; ``ssm_forward`` and the like
 allocate outputs and workspaces with torch. Shapes, types, devices and inner strides are checked
 here (ValueError), the rest in the library (GdnError). Everything runs on the current stream of the
-tensors' device, which has to be the current device.
+tensors' device, which has to be the current device; the calls that allocate nothing also take a raw
+``stream`` (the caller then keeps the tensors alive until that stream is done with them).
 """
 from __future__ import annotations
 
@@ -238,6 +239,8 @@ def gdn_ssm_bwd(p, x, b, c, dt, chunk_states, dy, dS_T, dx, db, dc, ddt, da_log,
 def _pool(state, slot_idx, N, device, shape, dtype):
     """(address, slots, address of the slot map) of a pool of states [n_slots, *shape]."""
     if state is None:
+        if shape[0] == 0:  # a window of no rows
+            return None, N, None if slot_idx is None else _array(slot_idx, "slot_idx", (N,), device, _i32)
         raise ValueError("state: missing")
     n_slots = state.shape[0]
     return (_array(state, "state", (n_slots, *shape), device, dtype), n_slots,
@@ -252,7 +255,7 @@ def gdn_ssm_decode(p, x, b, c, dt, state, slot_idx, y, stream=None):
           *_rows(y, "y", p.N, p.Hv * p.Dv, device, dtype), _on(stream, device))
 
 
-def ssm_forward(p, x, b, c, dt, S0=None, y=None, want_final=True, workspace=None, stream=None, save=True):
+def ssm_forward(p, x, b, c, dt, S0=None, y=None, want_final=True, workspace=None, save=True):
     """Allocate y, S_T and (``save``) the chunk states for a backward, run gdn_ssm_fwd; returns
     (y, S_T, states), states None with ``save=False``."""
     import torch
@@ -263,11 +266,11 @@ def ssm_forward(p, x, b, c, dt, S0=None, y=None, want_final=True, workspace=None
     states = _empty_bytes(gdn_ssm_chunk_state_bytes(p), x.device) if save else None
     if workspace is None and (need := gdn_ssm_fwd_workspace_bytes(p)):
         workspace = _empty_bytes(need, x.device)
-    gdn_ssm_fwd(p, x, b, c, dt, S0, y, S_T, states, workspace, stream)
+    gdn_ssm_fwd(p, x, b, c, dt, S0, y, S_T, states, workspace)
     return y, S_T, states
 
 
-def ssm_backward(p, x, b, c, dt, S0, states, dy, dS_T=None, grads=None, want_dS0=True, workspace=None, stream=None):
+def ssm_backward(p, x, b, c, dt, S0, states, dy, dS_T=None, grads=None, want_dS0=True, workspace=None):
     """Allocate gradients, run gdn_ssm_bwd; returns dict dx, db, dc, ddt, da_log, ddt_bias, dd_skip,
     dS0 (None where the problem has no dt_bias or d_skip, or with ``want_dS0=False``). S0 itself is not
     read (the saved states hold what follows from it)."""
@@ -284,7 +287,7 @@ def ssm_backward(p, x, b, c, dt, S0, states, dy, dS_T=None, grads=None, want_dS0
     if workspace is None:
         workspace = _empty_bytes(gdn_ssm_bwd_workspace_bytes(p), x.device)
     gdn_ssm_bwd(p, x, b, c, dt, states, dy, dS_T, *(grads.get(n) for n in (
-        "dx", "db", "dc", "ddt", "da_log", "ddt_bias", "dd_skip", "dS0")), workspace, stream)
+        "dx", "db", "dc", "ddt", "da_log", "ddt_bias", "dd_skip", "dS0")), workspace)
     return grads
 
 
@@ -360,20 +363,20 @@ def gdn_gated_norm_bwd(p, x, z, w, dy, dx, dz, dw, workspace, stream=None):
           *_scratch(workspace, device), _on(stream, device))
 
 
-def gated_norm_forward(p, x, z, w, stream=None):
+def gated_norm_forward(p, x, z, w):
     """Allocate y, run gdn_gated_norm_fwd; returns y [rows, groups * width]."""
     y = x.new_empty(p.rows, p.groups * p.width)
-    gdn_gated_norm_fwd(p, x, z, w, y, stream)
+    gdn_gated_norm_fwd(p, x, z, w, y)
     return y
 
 
-def gated_norm_backward(p, x, z, w, dy, workspace=None, stream=None):
+def gated_norm_backward(p, x, z, w, dy, workspace=None):
     """Allocate gradients, run gdn_gated_norm_bwd; returns dict dx, dz, dw."""
     grads = dict(dx=x.new_empty(p.rows, p.groups * p.width), dz=x.new_empty(p.rows, p.groups * p.width),
                  dw=w.new_empty(w.shape))
     if workspace is None:
         workspace = _empty_bytes(gdn_gated_norm_bwd_workspace_bytes(p), x.device)
-    gdn_gated_norm_bwd(p, x, z, w, dy, grads["dx"], grads["dz"], grads["dw"], workspace, stream)
+    gdn_gated_norm_bwd(p, x, z, w, dy, grads["dx"], grads["dz"], grads["dw"], workspace)
     return grads
 
 
@@ -396,19 +399,19 @@ def gdn_add_norm_bwd(p, res, y, s, w, dout, dres, dh, dy, dw, ds, workspace, str
           None if ds is None else _array(ds, "ds", width, device, _f32), *_scratch(workspace, device), _on(stream, device))
 
 
-def add_norm_forward(p, h, y, s, w, stream=None):
+def add_norm_forward(p, h, y, s, w):
     """Allocate outputs, run gdn_add_norm_fwd; returns (res, out)."""
     res, out = h.new_empty(p.rows, p.width), h.new_empty(p.rows, p.width)
-    gdn_add_norm_fwd(p, h, y, s, w, res, out, stream)
+    gdn_add_norm_fwd(p, h, y, s, w, res, out)
     return res, out
 
 
-def add_norm_backward(p, res, y, s, w, dout, dres=None, workspace=None, stream=None):
+def add_norm_backward(p, res, y, s, w, dout, dres=None, workspace=None):
     """Allocate gradients, run gdn_add_norm_bwd; returns dict dh, dy, dw and, with a scale vector, ds."""
     grads = dict(dh=res.new_empty(p.rows, p.width), dy=res.new_empty(p.rows, p.width), dw=w.new_empty(p.width))
     if s is not None:
         grads["ds"] = s.new_empty(p.width)
     if workspace is None:
         workspace = _empty_bytes(gdn_add_norm_bwd_workspace_bytes(p), res.device)
-    gdn_add_norm_bwd(p, res, y, s, w, dout, dres, grads["dh"], grads["dy"], grads["dw"], grads.get("ds"), workspace, stream)
+    gdn_add_norm_bwd(p, res, y, s, w, dout, dres, grads["dh"], grads["dy"], grads["dw"], grads.get("ds"), workspace)
     return grads

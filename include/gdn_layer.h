@@ -41,7 +41,8 @@ typedef struct {
   int64_t T_total;  /* rows */
   const int32_t* cu_seqlens; /* DEVICE int32 [N + 1] as in gdn_problem, or NULL; empty sequences allowed */
   int32_t Hk, Hv;   /* groups (heads of b and c) and heads of x; Hv % Hk == 0 */
-  int32_t Dk, Dv;   /* state size and head size, each one of 16, 32, 64, 128 */
+  int32_t Dk, Dv;   /* state size and head size, each one of 16, 32, 64, 128; (N + 8) Hv, twice that for
+                       Dv = 128, and (T_total / 64 + N) Hv below 2^23; T_total up to 2^28 */
   int32_t dtype;    /* gdn_dtype of x, b, c, y and their gradients */
   const float* a_log;   /* [Hv] */
   const float* dt_bias; /* [Hv] or NULL (none) */
@@ -55,7 +56,7 @@ size_t gdn_ssm_bwd_workspace_bytes(const gdn_ssm_problem* p);
 size_t gdn_ssm_chunk_state_bytes(const gdn_ssm_problem* p);
 
 /*
- * Forward over prompts. S0 (float32 [N][Hv][Dk][Dv] or NULL) and S_T (or NULL to skip) 16-byte
+ * Forward over prompts. Outputs must not overlap inputs (here and in gdn_ssm_bwd). S0 (float32 [N][Hv][Dk][Dv] or NULL) and S_T (or NULL to skip) 16-byte
  * aligned; they must not overlap. chunk_states: gdn_ssm_chunk_state_bytes bytes, 16-byte
  * aligned, kept unchanged for gdn_ssm_bwd, or NULL when no backward follows. The workspace may
  * be NULL where its size query returns 0.
@@ -100,7 +101,7 @@ gdn_status gdn_conv1d_silu_prompt(const gdn_conv_problem* p, const void* x, int6
 
 /*
  * The same for one token of each of p->N sequences (p->T == 1, p->T_total == p->N, cu_seqlens
- * NULL): state [n_slots][K - 1][channels] (dtype, 16-byte aligned) holds each slot's last rows,
+ * NULL; x and y may be the same view): state [n_slots][K - 1][channels] (dtype, 16-byte aligned) holds each slot's last rows,
  * oldest first, and is moved on by one row in place. Slots as in gdn_ssm_decode. For K == 1 there
  * is no window: state may be NULL.
  */

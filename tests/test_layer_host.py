@@ -39,13 +39,14 @@ def call(G, name, p, *args):
     return G.layer._fn(name)(ctypes.byref(p), *args)
 
 
-def ssm_fwd(G, p, x=(A, 256), b=(A, 256), c=(A, 256), dt=A, S0=None, y=(A, 256), ST=None, sv=None, ws=(A, 1 << 40)):
+def ssm_fwd(G, p, x=(A, 256), b=(A, 256), c=(A, 256), dt=A, S0=None, y=(2 * A, 256), ST=None, sv=None, ws=(A, 1 << 40)):
     return call(G, "gdn_ssm_fwd", p, *x, *b, *c, dt, S0, *y, ST, sv, *ws, 0)
 
 
 def ssm_bwd(G, p, sv=A, ddt=A, dST=None, dS0=None, ws=(A, 1 << 40), **kw):
-    v = (A, 256)
-    return call(G, "gdn_ssm_bwd", p, *v, *v, *v, A, sv, *v, dST, *kw.get("dx", v), *v, *v, ddt, None, None, None, dS0, *ws, 0)
+    v, o = (A, 256), (2 * A, 256)
+    return call(G, "gdn_ssm_bwd", p, *v, *v, *v, 3 * A, sv, *kw.get("dy", v), dST, *kw.get("dx", o), *kw.get("db", o), *o, ddt, None,
+                None, None, dS0, *ws, 0)
 
 
 def ssm_dec(G, p, state=A, slots=2, idx=None, y=(A, 256)):
@@ -74,7 +75,12 @@ def test_scan_refusals(G):
     assert ssm_fwd(G, one, ws=(A + 16, need)) == L
     need = G.gdn_ssm_bwd_workspace_bytes(p)
     assert ssm_bwd(G, p, ws=(A, need - 1)) == W and ssm_bwd(G, p, sv=None) == E and ssm_bwd(G, p, ddt=None) == E
-    assert ssm_bwd(G, p, dST=A, dS0=A) == E and ssm_bwd(G, p, dx=(A, 8)) == E
+    assert ssm_bwd(G, p, dST=A, dS0=A) == E and ssm_bwd(G, p, dx=(2 * A, 8)) == E
+    # an output in place of an input
+    assert ssm_fwd(G, p, y=(A, 256)) == E and ssm_bwd(G, p, dx=(A, 256)) == E and ssm_bwd(G, p, db=(A, 256)) == E
+    assert ssm_bwd(G, p, dy=(2 * A, 256)) == E and ssm_bwd(G, p, ddt=3 * A) == E
+    for n in (2**31 - 1, 2**31 - 9):  # counts at the end of their type
+        assert ssm_fwd(G, ssm(G, N=n, T=0, T_total=0)) == E and ssm_fwd(G, ssm(G, Hk=1, Hv=n)) == E
 
 
 def test_scan_token_refusals(G):
@@ -98,7 +104,7 @@ def conv(G, **kw):
 def test_conv_refusals(G):
     E, U, L = G.GDN_EINVAL, G.GDN_EUNSUPPORTED, G.GDN_EALIGN
 
-    def prompt(p, x=(A, 256), w=A, bias=None, first=None, y=(A, 256), last=None):
+    def prompt(p, x=(A, 256), w=A, bias=None, first=None, y=(2 * A, 256), last=None):
         return call(G, "gdn_conv1d_silu_prompt", p, *x, w, bias, first, *y, last, 0)
 
     def token(p, x=(A, 256), state=A, slots=2, idx=None):
@@ -110,6 +116,7 @@ def test_conv_refusals(G):
     p = conv(G)
     assert prompt(p, x=(A, 250)) == E and prompt(p, x=(A + 2, 256)) == L and prompt(p, w=None) == E and prompt(p, bias=A + 2) == L
     assert prompt(p, first=A + 8) == L and prompt(p, last=A + 8) == L and prompt(p, first=A, last=A) == E and prompt(p, y=(None, 256)) == E
+    assert prompt(p, y=(A, 256)) == E  # in place
     one = dict(N=2, T=1, T_total=2)
     assert token(p) == E and token(conv(G, **one, cu_seqlens=A)) == E
     q = conv(G, **one)

@@ -300,13 +300,16 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
 // Segments per sequence: two workgroups to a compute unit, each with at least kMinChunks chunks on
 // average. A segment costs its states and a second read of its rows, so two gain nothing (4 x 4096
 // tokens, 64 heads: one segment 243 us, two 247), more do (16384 tokens, 32 heads: 8 of them 180 us,
-// 16 of them 150; without any some 900).
-constexpr int kWantGroups = 512, kMinChunks = 4, kMaxSegments = 32;
+// 16 of them 150; 16 x 512 tokens, 4 heads: one 34, four 28). A packed batch's lengths are not known
+// here, and its longest sequence may hold most of the tokens: short averages get three all the same
+// (lengths up to 777 with an average of 190, float32: 123 -> 77 us for both sweeps).
+constexpr int kWantGroups = 512, kMinChunks = 2, kMaxSegments = 32;
 static int ssm_segments(const SsmArgs& a) {
   if (a.N == 0) return 1;
-  const int64_t groups = (int64_t)a.N * a.Hv * ((a.Dv + SP - 1) / SP);
+  const int64_t groups = (int64_t)a.N * a.Hv * ((a.Dv + SP - 1) / SP), chunks = a.T_total / SC;
+  int64_t most = chunks / a.N / kMinChunks;
+  if (a.cu && a.N > 1 && most < 3 && chunks >= 3 * kMinChunks) most = 3;
   int64_t s = kWantGroups / groups;
-  const int64_t most = a.T_total / SC / a.N / kMinChunks;
   if (s > most) s = most;
   if (s > kMaxSegments) s = kMaxSegments;
   return s <= 2 ? 1 : (int)s;

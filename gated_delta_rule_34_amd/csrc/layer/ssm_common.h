@@ -177,11 +177,28 @@ __device__ __forceinline__ double lane_value_f64(double x, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// log1p(x) for x >= 0: log(u) x / (u - 1) with u = 1 + x as rounded, which takes the rounding back
-// out (Kahan); a few ulp, a third of the library function's operations.
-__device__ __forceinline__ float log1p_pos(float x) {
-  const float u = 1.f + x, d = u - 1.f;
-  return d == 0.f ? x : __logf(u) * (x * __builtin_amdgcn_rcpf(d));
+// -exp(a_log) in log2 units, to 1e-11 of it: e^a = 2^n e^r by the Taylor series of e^r, |r| <= ln 2 / 2.
+// An error of it is common to all decays of a head and would add up in the sums over tokens (as would
+// one of the step: both are float32 functions' last bits otherwise).
+__device__ __forceinline__ double neg_a_log2(float a_log) {
+  const double a = (double)a_log, n = rint(a * 1.4426950408889634), r = fma(n, -0.6931471805599453, a);
+  double e = 1.0 / 362880.0;
+  e = fma(e, r, 1.0 / 40320.0);
+  e = fma(e, r, 1.0 / 5040.0);
+  e = fma(e, r, 1.0 / 720.0);
+  e = fma(e, r, 1.0 / 120.0);
+  e = fma(e, r, 1.0 / 24.0);
+  e = fma(e, r, 1.0 / 6.0);
+  e = fma(e, r, 0.5);
+  e = fma(e, r, 1.0);
+  e = fma(e, r, 1.0);
+  return -1.4426950408889634 * ldexp(e, (int)n);
+}
+
+// 2^x with the part of x that a float32 drops.
+__device__ __forceinline__ float exp2_d(double x) {
+  const float hi = (float)x, lo = (float)(x - (double)hi), e = __builtin_amdgcn_exp2f(hi);
+  return fmaf(e, lo * 0.69314718f, e);
 }
 
 // Gates of one chunk, one token per lane: the step, gamma (log2), its sum over the chunk.
@@ -189,11 +206,11 @@ struct Gate {
   float z, step;
   double gam, tot;
 };
-__device__ __forceinline__ Gate chunk_gate(float dt, float bias, float neg_a_log2, bool valid) {
+__device__ __forceinline__ Gate chunk_gate(float dt, float bias, double neg_a, bool valid) {
   Gate q;
   q.z = dt + bias;
-  q.step = !valid ? 0.f : q.z > 20.f ? q.z : log1p_pos(expf(q.z));
-  q.gam = wave_scan_incl_f64(valid ? (double)(neg_a_log2 * q.step) : 0.0);
+  q.step = valid ? softplusf(q.z) : 0.f;
+  q.gam = wave_scan_incl_f64(valid ? neg_a * (double)q.step : 0.0);
   q.tot = lane_value_f64(q.gam, 63);
   return q;
 }

@@ -8,9 +8,9 @@
 //   q_t = d loss / d log a_t = sum_{i >= t} (row_i - D_i col_i + 2^gamma_i c_i . E_i)
 //                              + sum_{j < t} D_j e_j b_j . F_j + 2^gamma_n <S, dS>
 //   dD_j = W_jj + col_j + e_j b_j . F_j - exp(a_log) q_j,   ddt = dD sigmoid(dt + dt_bias)
-// with row_i = sum_{j < i} D_j W_ij and col_j = sum_{i > j} W_ij: what row_i and D_j col_j add for pairs
-// on one side of t cancels, and the diagonal, which alone carries no decay, is left out of both (under
-// strong decays it would drown q). The two products with Gamma D Q are linear in
+// with row_i = sum_{j < i} D_j W_ij and col_j = sum_{i > j} W_ij (what row_i and D_j col_j add for pairs
+// on one side of t cancels; the kernel forms that difference within tiles of 16 tokens only). The diagonal,
+// which alone carries no decay, is left out of both: under strong decays it would drown q. The two products with Gamma D Q are linear in
 // it, so they run once per group on the sum over its heads. b, c, x, dy are exact as bfloat16
 // operands; the states are split over three (24 bits), so that the float32 results keep float32
 // accuracy, and Gamma D Q over two, so that db and dc carry no rounding but their own. Bound by HBM: the two states of a chunk and head are 8 Dk Dv bytes.
@@ -129,16 +129,16 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
   auto gates = [&](int hh) {
     if (w >= HB || hh + w >= p.r) return;
     const int h = kh * p.r + hh + w, b = (hh / HB) & 1;
-    const Gate q = chunk_gate(rdt, p.dt_bias ? p.dt_bias[h] : 0.f, -expf(p.a_log[h]) * kLog2e, l < len);
+    const Gate q = chunk_gate(rdt, p.dt_bias ? p.dt_bias[h] : 0.f, neg_a_log2(p.a_log[h]), l < len);
     const float h32 = (float)q.gam;
     float(*gt)[SC] = sh[b][w];
     gt[0][l] = h32;
     gt[1][l] = (float)(q.gam - (double)h32);
     gt[2][l] = q.step;
-    gt[3][l] = __builtin_amdgcn_exp2f(h32);
-    gt[4][l] = __builtin_amdgcn_exp2f((float)(q.tot - q.gam));
+    gt[3][l] = exp2_d(q.gam);
+    gt[4][l] = exp2_d(q.tot - q.gam);
     gt[5][l] = q.z;
-    if (l == 63) sbn[b][w] = __builtin_amdgcn_exp2f((float)q.tot);
+    if (l == 63) sbn[b][w] = exp2_d(q.tot);
   };
 
   {
@@ -291,12 +291,17 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
         if (w <= hb) {  // one head, one token per lane
           const int h = kh * p.r + h0 + w, ti = l >> 4, b = (h0 / HB) & 1;
           const float(*gw)[SC] = sh[b][w];
-          float row = 0.f, col = 0.f, ce = 0.f, bf = 0.f, fr = 0.f, dsum8 = 0.f;
+          // Pairs (i, j) on both sides of t, by tiles of 16: those of t's own tile as a difference of row
+          // and column sums over that tile alone, the others as sums of what is on the far side (over
+          // the whole chunk the difference's rounding was common to the chunk's tokens and drowned da_log).
+          const int dg = ti * (ti + 1) / 2 + ti;
+          float rowo = 0.f, colo = 0.f, ce = 0.f, bf = 0.f, fr = 0.f, dsum8 = 0.f;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            if (x <= ti) row += srow[w][ti * (ti + 1) / 2 + x][r];
-            if (x >= ti) col += scol[w][x * (x + 1) / 2 + ti][r];
+            if (x < ti) rowo += srow[w][ti * (ti + 1) / 2 + x][r];
+            if (x > ti) colo += scol[w][x * (x + 1) / 2 + ti][r];
           }
+          const float s20 = row16_sum(srow[w][3][r]), s30 = row16_sum(srow[w][6][r]), s31 = row16_sum(srow[w][7][r]);
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
             ce += sE[w][x][l];
@@ -307,8 +312,21 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
           const float step = gw[2][l], z = gw[5][l];
           ce *= gw[3][l];
           bf *= gw[4][l];
+          const float cold = scol[w][dg][r], col = cold + colo;
+          float suf = rowo + srow[w][dg][r] - step * cold;  // over the tile's tokens from t on
+          suf += dpp<0x101>(suf);
+          suf += dpp<0x102>(suf);
+          suf += dpp<0x104>(suf);
+          suf += dpp<0x108>(suf);
+          float pre = step * colo;  // over the tile's tokens before t
+          pre += dpp<0x111>(pre);
+          pre += dpp<0x112>(pre);
+          pre += dpp<0x114>(pre);
+          pre += dpp<0x118>(pre);
+          pre = dpp<0x111>(pre);
+          const float far = ti == 1 ? s20 + s30 : ti == 2 ? s30 + s31 : 0.f;  // tiles on either side
           const float before = __shfl_up(wave_scan_incl(step * bf), 1);  // (the last token's own term carries no decay)
-          const float qt = wave_rscan_incl(row - step * col + ce) + (l > 0 ? before : 0.f) + sbn[b][w] * fr;
+          const float qt = suf + pre + far + wave_rscan_incl(ce) + (l > 0 ? before : 0.f) + sbn[b][w] * fr;
           const float na = -expf(p.a_log[h]);
           const bool live = l < len;
           const float ddt = live ? (sdiag[w][l] + col + bf + na * qt) / (1.f + expf(-z)) : 0.f;

@@ -79,7 +79,8 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   const int nch = (int)((hi - lo + SC - 1) / SC), cps = (nch + a.S - 1) / a.S;
   const int k0 = min(nch, sgm * cps), k1 = min(nch, k0 + cps);
 
-  const float neg_a = -expf(a.a_log[h]) * kLog2e, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  const double neg_a = neg_a_log2(a.a_log[h]);
+  const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   const float dsk = a.d_skip ? a.d_skip[h] : 0.f;
   const TI* kp = (const TI*)a.k + kh * DK;
   const TI* qp = (const TI*)a.q + kh * DK;
@@ -111,14 +112,14 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
     if (w >= GB) return;
     const bool valid = k < k1 && l < clen(chunk(k));
     const Gate q = chunk_gate(rdt, bias, neg_a, valid);
-    const float hi32 = (float)q.gam, eb = __builtin_amdgcn_exp2f(hi32), ee = __builtin_amdgcn_exp2f((float)(q.tot - q.gam));
+    const float hi32 = (float)q.gam, eb = exp2_d(q.gam), ee = exp2_d(q.tot - q.gam);
     float(*gt)[SC] = sg[(k - k0) & (2 * GB - 1)];
     gt[G_HI][l] = hi32;
     gt[G_LO][l] = (float)(q.gam - (double)hi32);
     gt[G_IN][l] = q.step;
     gt[G_RD][l] = REV ? ee : eb;
     gt[G_WR][l] = REV ? (valid ? eb : 0.f) : ee * q.step;
-    if (l == 63) sbn[(k - k0) & (2 * GB - 1)] = __builtin_amdgcn_exp2f((float)q.tot);
+    if (l == 63) sbn[(k - k0) & (2 * GB - 1)] = exp2_d(q.tot);
   };
   if (k0 < k1) {
     load_dt(k0 + w);

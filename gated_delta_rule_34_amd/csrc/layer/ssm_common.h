@@ -177,23 +177,9 @@ __device__ __forceinline__ double lane_value_f64(double x, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// -exp(a_log) in log2 units, to 1e-11 of it: e^a = 2^n e^r by the Taylor series of e^r, |r| <= ln 2 / 2.
-// An error of it is common to all decays of a head and would add up in the sums over tokens (as would
-// one of the step: both are float32 functions' last bits otherwise).
-__device__ __forceinline__ double neg_a_log2(float a_log) {
-  const double a = (double)a_log, n = rint(a * 1.4426950408889634), r = fma(n, -0.6931471805599453, a);
-  double e = 1.0 / 362880.0;
-  e = fma(e, r, 1.0 / 40320.0);
-  e = fma(e, r, 1.0 / 5040.0);
-  e = fma(e, r, 1.0 / 720.0);
-  e = fma(e, r, 1.0 / 120.0);
-  e = fma(e, r, 1.0 / 24.0);
-  e = fma(e, r, 1.0 / 6.0);
-  e = fma(e, r, 0.5);
-  e = fma(e, r, 1.0);
-  e = fma(e, r, 1.0);
-  return -1.4426950408889634 * ldexp(e, (int)n);
-}
+// -exp(a_log) in log2 units. Its last float32 bit is common to all decays of a head, as if a_log itself
+// were 1e-7 off, and no product of it with a step is rounded again before the sums of the gates.
+__device__ __forceinline__ double neg_a_log2(float a_log) { return (double)(-expf(a_log) * kLog2e); }
 
 // 2^x with the part of x that a float32 drops.
 __device__ __forceinline__ float exp2_d(double x) {

@@ -137,7 +137,7 @@ template <typename TI, int K, int R> __global__ __launch_bounds__(64) void k_con
   for (int u = 0; u < R; ++u) {
     const int n = (int)blockIdx.x * R + u;
     slot[u] = n >= a.N ? -1 : a.idx ? a.idx[n] : n;
-    if (K > 1 && slot[u] >= a.n_slots) slot[u] = -1;
+    if (slot[u] >= a.n_slots) slot[u] = -1;
     if (slot[u] < 0) continue;  // the row is skipped
     xr[u] = ldraw8<false, TI>((const TI*)a.x + (int64_t)n * a.x_rs + c0);
 #pragma unroll

@@ -239,8 +239,8 @@ def gdn_ssm_bwd(p, x, b, c, dt, chunk_states, dy, dS_T, dx, db, dc, ddt, da_log,
 def _pool(state, slot_idx, N, device, shape, dtype):
     """(address, slots, address of the slot map) of a pool of states [n_slots, *shape]."""
     if state is None:
-        if shape[0] == 0:  # a window of no rows
-            return None, N, None if slot_idx is None else _array(slot_idx, "slot_idx", (N,), device, _i32)
+        if shape[0] == 0:  # a window of no rows: any slot will do
+            return None, 0x7FFFFFFF, None if slot_idx is None else _array(slot_idx, "slot_idx", (N,), device, _i32)
         raise ValueError("state: missing")
     n_slots = state.shape[0]
     return (_array(state, "state", (n_slots, *shape), device, dtype), n_slots,

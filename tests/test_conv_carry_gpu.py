@@ -5,7 +5,7 @@ of the window's products (SiLU's slope is below 1.1). The carried rows are copie
 import numpy as np
 import pytest
 
-from layer_gpu import HALF, cu_of, dev, host, rounded, torch_dtype
+from layer_gpu import HALF, cu_of, dev, host, rel, rounded, torch_dtype
 
 pytestmark = pytest.mark.gpu
 
@@ -123,6 +123,22 @@ def test_token(dtype, K):
     assert np.array_equal(got[idx[live]], last[live])
     rest = [s for s in range(slots) if s not in set(idx[live])]
     assert np.array_equal(got[rest], pool[rest])
+
+
+def test_token_without_a_window():
+    """K == 1: rows are skipped by their slots all the same; without a pool only negative slots are."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    x, w = torch.randn(4, 16, device="cuda"), torch.randn(16, 1, device="cuda")
+    p = G.make_conv_problem(4, 4, 16, 1, T=1, dtype="f32")
+    idx = torch.tensor([5, -1, 0, 6], dtype=torch.int32, device="cuda")
+    for state, live in ((torch.empty(6, 0, 16, device="cuda"), [0, 2]), (None, [0, 2, 3])):
+        y = torch.full((4, 16), 7.0, device="cuda")
+        G.gdn_conv1d_silu_decode(p, x, w, None, state, idx, y)
+        dead = [i for i in range(4) if i not in live]
+        z = (x.double() * w[:, 0].double())[live]
+        assert rel(host(y)[live], host(z * z.sigmoid())) <= 1e-6 and bool((y[dead] == 7.0).all())
 
 
 def test_rows_of_no_sequence_and_malformed_tables():

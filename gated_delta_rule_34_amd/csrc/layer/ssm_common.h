@@ -179,7 +179,7 @@ __device__ __forceinline__ double lane_value_f64(double x, int lane) {
 
 // -exp(a_log) in log2 units. Its last float32 bit is common to all decays of a head, as if a_log itself
 // were 1e-7 off, and no product of it with a step is rounded again before the sums of the gates.
-__device__ __forceinline__ double neg_a_log2(float a_log) { return (double)(-expf(a_log) * kLog2e); }
+__device__ __forceinline__ double neg_a_log2(float a_log) { return (double)(-decay_rate(a_log) * kLog2e); }
 
 // 2^x with the part of x that a float32 drops.
 __device__ __forceinline__ float exp2_d(double x) {
@@ -196,7 +196,10 @@ __device__ __forceinline__ Gate chunk_gate(float dt, float bias, double neg_a, b
   Gate q;
   q.z = dt + bias;
   q.step = valid ? softplusf(q.z) : 0.f;
-  q.gam = wave_scan_incl_f64(valid ? neg_a * (double)q.step : 0.0);
+  // One token's exponent ends at -4096: 2^-4096 is zero in every use, and a larger one would cost the
+  // differences of its chunk's other tokens their accuracy (or, infinite, make them NaN).
+  const double e = neg_a * (double)q.step;
+  q.gam = wave_scan_incl_f64(valid ? (e < -4096.0 ? -4096.0 : e) : 0.0);
   q.tot = lane_value_f64(q.gam, 63);
   return q;
 }

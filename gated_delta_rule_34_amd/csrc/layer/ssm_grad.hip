@@ -326,8 +326,9 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
           pre = dpp<0x111>(pre);
           const float far = ti == 1 ? s20 + s30 : ti == 2 ? s30 + s31 : 0.f;  // tiles on either side
           const float before = __shfl_up(wave_scan_incl(step * bf), 1);  // (the last token's own term carries no decay)
-          const float qt = suf + pre + far + wave_rscan_incl(ce) + (l > 0 ? before : 0.f) + sbn[b][w] * fr;
-          const float na = -expf(p.a_log[h]);
+          float qt = suf + pre + far + wave_rscan_incl(ce) + (l > 0 ? before : 0.f) + sbn[b][w] * fr;
+          const float na = -decay_rate(p.a_log[h]);
+          if (na * step < -104.f) qt = 0.f;  // a decay of 2^-150: q holds rounding only, which a large rate would show
           const bool live = l < len;
           const float ddt = live ? (sdiag[w][l] + col + bf + na * qt) / (1.f + expf(-z)) : 0.f;
           if (live) p.ddt[(t0 + l) * p.Hv + h] = ddt;

@@ -95,4 +95,11 @@ __device__ __forceinline__ float softplusf(float z) { return z > 20.f ? z : log1
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// exp(a_log), kept finite: a rate of 2^100 already leaves nothing of a state unless the step is zero, and
+// then the decay is one (an infinite rate times a zero step would be NaN). NaN stays.
+__device__ __forceinline__ float decay_rate(float a_log) {
+  const float a = expf(a_log);
+  return a > 0x1p100f ? 0x1p100f : a;
+}
+
 }  // namespace gdn

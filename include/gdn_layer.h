@@ -9,7 +9,9 @@
  * allocates, frees or synchronises); rows are row-strided views whose strides are in elements,
  * 16-byte aligned in address and stride; float32 arrays named [..] are contiguous; arguments
  * are checked on the host before anything is enqueued; a malformed cu_seqlens or slot gives
- * wrong results but no access outside the caller's buffers. The device that owns the stream has
+ * wrong results but no access outside the caller's buffers. The scan works on chunks of 64 tokens: a
+ * NaN or an infinity stays in its sequence and head (in b and c: in its group of heads), but may reach
+ * the other rows of its chunk. The device that owns the stream has
  * to be current. Results are the same bits on every run (no atomics).
  */
 #ifndef GDN_LAYER_H
@@ -103,7 +105,7 @@ gdn_status gdn_conv1d_silu_prompt(const gdn_conv_problem* p, const void* x, int6
  * The same for one token of each of p->N sequences (p->T == 1, p->T_total == p->N, cu_seqlens
  * NULL; x and y may be the same view): state [n_slots][K - 1][channels] (dtype, 16-byte aligned) holds each slot's last rows,
  * oldest first, and is moved on by one row in place. Slots as in gdn_ssm_decode. For K == 1 there
- * is no window: state may be NULL.
+ * is no window: state may be NULL (rows are skipped by n_slots all the same).
  */
 gdn_status gdn_conv1d_silu_decode(const gdn_conv_problem* p, const void* x, int64_t x_rs, const float* w,
                                   const float* bias, void* state, int32_t n_slots, const int32_t* slot_idx,

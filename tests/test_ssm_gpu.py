@@ -126,6 +126,29 @@ def test_scan_extreme_steps(dtype, dt, a_log):
     check(a, up, cu, dtype, run(*place(a, up, cu, dtype)), more=min(m, 80) * 4 * 2.0 ** -23)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dt,a_log", [(2.0, 100.0), (-200.0, 100.0), (1e6, 20.0), (0.0, -200.0)])
+def test_scan_rates_past_float32(dtype, dt, a_log):
+    """Rates exp(a_log) and exponents beyond float32: nothing is left of a state, or (a step of zero, a
+    rate of zero) all of it; prompts, gradients and single tokens alike. In the second case the step is zero in
+    float32 and 1e-87 in the oracle, and 3e43 of it is still nothing."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    a, up, cu = make([130, 33], 1, 2, 32, 32, dtype, seed=12, dt=dt, a_log=a_log, bias=False)
+    a["dt"][[40, 100, 150]] = -200.0  # steps of zero between the others
+    p, d = place(a, up, cu, dtype)
+    check(a, up, cu, dtype, run(p, d))
+    from oracle import layer as L
+
+    one, up, cu = make([1, 1], 1, 2, 32, 32, dtype, seed=14, dt=dt, a_log=a_log, bias=False)
+    p, d = place(one, up, cu, dtype, varlen=False, lens=[1])
+    y, state = torch.empty(2, 64, dtype=torch_dtype(dtype), device="cuda"), d["S0"].clone()
+    G.gdn_ssm_decode(p, d["x"], d["b"], d["c"], d["dt"], state, None, y)
+    yr, STr = L.ssm_fwd(cu, *one.values())
+    assert rel(host(y), yr) <= TOL[dtype] and rel(host(state), STr) <= 1e-5
+
+
 def test_scan_forward_is_the_same_with_and_without_saving_and_on_every_run():
     import torch
 

@@ -5,7 +5,9 @@
 //
 // with ext the K - 1 carried rows followed by the sequence's rows. What a continuation needs is
 // the last K - 1 rows of ext, copied as they are. Pure streaming: each row is read and written
-// once (2 ch values per row), bound by HBM; the window lives in registers.
+// once (2 ch values per row), bound by HBM; the window lives in registers. Measured (bf16, K = 4):
+// 21488 rows x 10240 in 8 sequences 197 us, 4.5 TB/s (a large copy reaches 5.2); one token of 256
+// sequences 17.4 us with nothing in the caches, 11 us per call in a loop.
 #include "vec8.h"
 
 namespace gdn {

@@ -13,7 +13,11 @@
 // which alone carries no decay, is left out of both: under strong decays it would drown q. The two products with Gamma D Q are linear in
 // it, so they run once per group on the sum over its heads. b, c, x, dy are exact as bfloat16
 // operands; the states are split over three (24 bits), so that the float32 results keep float32
-// accuracy, and Gamma D Q over two, so that db and dc carry no rounding but their own. Bound by HBM: the two states of a chunk and head are 8 Dk Dv bytes.
+// accuracy, and Gamma D Q over two, so that db and dc carry no rounding but their own.
+//
+// Bound by HBM: the two states of a chunk and head are 8 Dk Dv bytes. Measured (bf16, 4 x 4096 tokens, 64 heads
+// of 128 x 64 in 8 groups): 426 to 440 us for the 1.5 GB of states and rows, which a copy would take 290 us
+// to move; the rest is the start of each workgroup (one to a compute unit), which nothing overlaps.
 //
 // Eight waves: wave w holds 16 rows of Dk (all tokens; with a smaller state some tokens) and one or two
 // tiles of the tokens' triangle. The next head's rows and states are on their way while a head is

@@ -9,11 +9,14 @@
 // columns of one token. The next chunk's rows are in registers while a chunk is computed. A chunk is
 // a chain of short dependent products, bound by their latency and the LDS: eight waves of 128 registers,
 // so that two workgroups (four waves per SIMD) share a compute unit, hide what four waves of 230 (or one
-// workgroup of eight with 165) did not.
+// workgroup of eight with 165) did not. Measured (bf16, 4 x 4096 tokens, 64 heads of 128 x 64 in 8
+// groups): 250 us without and 275 us with saved states (0.54 GB more written), 280 us in reverse; the
+// rows alone would take a copy 66 us. A chunk takes a workgroup some 8000 cycles.
 //
 // Few sequences and heads leave compute units idle over a long serial chain, so a sequence is then
 // cut into S segments: a first launch runs the state alone over all segments but the last, from
-// zero, and the second starts each segment from the earlier segments' states and decays.
+// zero, and the second starts each segment from the earlier segments' states and decays (16384 tokens, 32 heads in one group:
+// 47 us for the states, 94 us for the outputs).
 #include "ssm_common.h"
 
 namespace gdn {

@@ -10,7 +10,7 @@
 // a chain of short dependent products, bound by their latency and the LDS: eight waves of 128 registers,
 // so that two workgroups (four waves per SIMD) share a compute unit, hide what four waves of 230 (or one
 // workgroup of eight with 165) did not. Measured (bf16, 4 x 4096 tokens, 64 heads of 128 x 64 in 8
-// groups): 250 us without and 275 us with saved states (0.54 GB more written), 280 us in reverse; the
+// groups): 245 us without and 270 us with saved states (0.54 GB more written), 280 us in reverse; the
 // rows alone would take a copy 66 us. A chunk takes a workgroup some 8000 cycles.
 //
 // Few sequences and heads leave compute units idle over a long serial chain, so a sequence is then
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   constexpr int NT = 512, DH = DK >= 32 ? DK / 2 : 16, ND = DH / 16;  // this wave's rows of the state
   constexpr int KSD = ks_of<TI, DK>(), NSD = DK / KSD, KSC = ks_of<TI, SC>(), NSC = SC / KSC;
   constexpr int KSH = ks_of<TI, DH>(), NSH = DH / KSH;
-  constexpr int NS = ssm_split<TI>(), TRI = REV ? TRI_UP : TRI_LOW, GB = 2;
+  constexpr int NS = ssm_split<TI>(), TRI = REV ? TRI_UP : TRI_LOW, GB = 3, GR = GB + 1;
   using LK = PadRow<TI, DK>;
   using LX = Swz<TI, SP, true>;
   using LM = Swz<TI, SC, false>;
@@ -56,8 +56,8 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   __shared__ __align__(16) TI sX2[2][SC * SP];
   __shared__ __align__(16) TI sM[OUT ? SC * SC : 8];
   __shared__ __align__(16) f32x4 sP[OUT ? 8 * 2 * 64 : 1];  // shares of S^T Q for the other half
-  __shared__ __align__(16) float sg[2 * GB][G_ROWS][SC];
-  __shared__ float sbn[2 * GB];
+  __shared__ __align__(16) float sg[GR][G_ROWS][SC];
+  __shared__ float sbn[GR];
 
   const int segs = OUT ? a.S : a.S - 1;
   int grp, mem;
@@ -98,7 +98,8 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   rx.init(a.x_rs, ncols);
   const uint32_t orow = (uint32_t)a.o_rs * (uint32_t)sizeof(TI);
   // Gates come GB chunks at a time, one for each of GB waves: a chunk's are a long chain of dependent
-  // operations that by one wave in every chunk took a fifth of the step.
+  // operations that by one wave in every chunk took a fifth of the step (every second chunk 255 us for 4 x 4096
+  // tokens and 64 heads, every third 245). A ring of GB + 1 holds them: the chunk in work keeps its own.
   float rdt = 0.f;  // dt of this wave's chunk of the next ones
   auto load = [&](int k) {
     const int c = chunk(k), len = clen(c);
@@ -116,13 +117,13 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
     const bool valid = k < k1 && l < clen(chunk(k));
     const Gate q = chunk_gate(rdt, bias, neg_a, valid);
     const float hi32 = (float)q.gam, eb = exp2_d(q.gam), ee = exp2_d(q.tot - q.gam);
-    float(*gt)[SC] = sg[(k - k0) & (2 * GB - 1)];
+    float(*gt)[SC] = sg[(k - k0) & (GR - 1)];
     gt[G_HI][l] = hi32;
     gt[G_LO][l] = (float)(q.gam - (double)hi32);
     gt[G_IN][l] = q.step;
     gt[G_RD][l] = REV ? ee : eb;
     gt[G_WR][l] = REV ? (valid ? eb : 0.f) : ee * q.step;
-    if (l == 63) sbn[(k - k0) & (2 * GB - 1)] = exp2_d(q.tot);
+    if (l == 63) sbn[(k - k0) & (GR - 1)] = exp2_d(q.tot);
   };
   if (k0 < k1) {
     load_dt(k0 + w);
@@ -178,8 +179,8 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
     const TI* sX = sX2[buf];
     lds_barrier();  // the chunk's rows and gates are in LDS, M and the shares are free
     if (k + 1 < k1) load(k + 1);
-    const float(*gt)[SC] = sg[(k - k0) & (2 * GB - 1)];
-    const float bn = sbn[(k - k0) & (2 * GB - 1)];
+    const float(*gt)[SC] = sg[(k - k0) & (GR - 1)];
+    const float bn = sbn[(k - k0) & (GR - 1)];
     f32x4 o[4];
     if constexpr (OUT) {
       // M = Gamma o (Q K^T) o inputs' weights: its ten tiles dealt over the waves
@@ -275,7 +276,7 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
       }
     }
     if (k + 1 < k1) {
-      if (((k + 1 - k0) & (GB - 1)) == 0) {  // the next chunks' gates
+      if ((k + 1 - k0) % GB == 0) {  // the next chunks' gates
         gates(k + 1 + w);
         load_dt(k + 1 + GB + w);
       }

@@ -83,6 +83,7 @@ size_t ssm_bwd_ws_bytes(const SsmArgs& a);
 size_t ssm_saved_bytes(const SsmArgs& a);
 hipError_t launch_ssm_forward(const SsmArgs& a, int dtype, hipStream_t s);
 hipError_t launch_ssm_backward(const SsmArgs& a, int dtype, hipStream_t s);
-hipError_t launch_ssm_grad(const SsmArgs& a, int dtype, const float* ds, float* part, hipStream_t s);
+size_t ssm_fold_bytes(const SsmArgs& a);
+hipError_t launch_ssm_grad(const SsmArgs& a, int dtype, const float* ds, float* part, float* fold, hipStream_t s);
 
 }  // namespace gdn

@@ -1,6 +1,7 @@
 // ssm_grad.hip -- gradients of the selective state space scan inside each chunk, on gfx950.
 //
-// One workgroup per (chunk, group of heads that share b and c), walking over the group's heads.
+// One workgroup per (chunk, group of heads that share b and c), walking over the group's heads (a part of
+// them where there are few chunks, k_ssm_fold).
 // With Q = dy x^T, W = Gamma o G o Q (no step), E = S dy and F = dS x (S the state at the chunk's
 // start, dS the adjoint at its end, both float32), e_j = 2^(gamma_n - gamma_j):
 //   dc_i = sum_h [ sum_j Gamma_ij D_j Q_ij b_j + 2^gamma_i E_i ]
@@ -32,9 +33,37 @@ struct GradArgs {
   SsmArgs p;
   const float *sv, *ds;  // [slot][Hv][Dk][Dv]: states at the chunks' starts, adjoints at their ends
   float* part;           // [3][slots][Hv]: da_log, ddt_bias, dd_skip of each chunk
-  int nslab;
+  float* fold;           // [2][parts][T_total][Hk Dk]: each part's dc and db, where a group has several
+  int nslab, parts, hpp; // workgroups to a group, heads of each
   int64_t slots;
 };
+
+// The slot's sequence and its chunk there: the largest n whose first slot is not behind it, 64 probes at
+// a time (by whole waves). Returns the chunk's rows, none for a slot of no chunk.
+__device__ __forceinline__ int slot_chunk(const SsmArgs& p, int64_t slot, int64_t& t0) {
+  int n = 0;
+  int64_t lo, hi;
+  if (p.cu || p.N > 1) {
+    for (int m = p.N; m > 1;) {
+      const int stride = (m + 63) / 64, i = lane_id() * stride;
+      bool in = false;
+      if (i < m) {
+        int64_t x = p.cu ? (int64_t)p.cu[n + i] : (int64_t)(n + i) * p.T;
+        x = x < 0 ? 0 : (x > p.T_total ? p.T_total : x);
+        in = x / SC + n + i <= slot;
+      }
+      const uint64_t hit = __ballot(in);
+      const int at = (hit ? 63 - __builtin_clzll(hit) : 0) * stride;
+      n += at;
+      m = m - at < stride ? m - at : stride;
+    }
+  }
+  ssm_seq(p.cu, p.T, p.T_total, n, lo, hi);
+  const int64_t k = slot - (lo / SC + n);
+  t0 = lo + k * SC;
+  if (k < 0 || k >= (hi - lo + SC - 1) / SC) return 0;
+  return (int)(hi - t0 < SC ? hi - t0 : SC);
+}
 
 template <typename TI, int DK>
 __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
@@ -56,46 +85,27 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
   __shared__ __align__(16) float srow[HB][10][16], scol[HB][10][16];
   __shared__ float sdiag[HB][SC], sE[HB][8][SC], sF[HB][8][SC], sfr[HB][8], sdd[HB][8];
 
-  const int kh = (int)(blockIdx.x % p.Hk);
-  const int64_t slot = blockIdx.x / p.Hk;
+  const int pt = (int)(blockIdx.x % a.parts), kh = (int)(blockIdx.x / a.parts % p.Hk);
+  const int64_t slot = blockIdx.x / a.parts / p.Hk;
+  const int hd0 = kh * p.r + pt * a.hpp, nhd = min(a.hpp, p.r - pt * a.hpp);  // this workgroup's heads
   const int w = wave_id(), l = lane_id(), g = l >> 4, r = l & 15;
-  // the slot's sequence: the largest n whose first slot is not behind it, 64 probes at a time
-  int n = 0;
-  int64_t lo, hi;
-  if (p.cu || p.N > 1) {
-    for (int m = p.N; m > 1;) {
-      const int stride = (m + 63) / 64, i = l * stride;
-      bool in = false;
-      if (i < m) {
-        int64_t x = p.cu ? (int64_t)p.cu[n + i] : (int64_t)(n + i) * p.T;
-        x = x < 0 ? 0 : (x > p.T_total ? p.T_total : x);
-        in = x / SC + n + i <= slot;
-      }
-      const uint64_t hit = __ballot(in);
-      const int at = (hit ? 63 - __builtin_clzll(hit) : 0) * stride;
-      n += at;
-      m = m - at < stride ? m - at : stride;
-    }
-  }
-  ssm_seq(p.cu, p.T, p.T_total, n, lo, hi);
-  const int64_t k = slot - (lo / SC + n);
-  if (k < 0 || k >= (hi - lo + SC - 1) / SC) {  // a slot of no chunk
-    for (int i = threadIdx.x; i < 3 * p.r; i += NT)
-      a.part[((int64_t)(i / p.r) * a.slots + slot) * p.Hv + kh * p.r + i % p.r] = 0.f;
+  int64_t t0;
+  const int len = slot_chunk(p, slot, t0);
+  if (len == 0) {  // a slot of no chunk
+    for (int i = threadIdx.x; i < 3 * nhd; i += NT)
+      a.part[((int64_t)(i / nhd) * a.slots + slot) * p.Hv + hd0 + i % nhd] = 0.f;
     return;
   }
-  const int64_t t0 = lo + k * SC;
-  const int len = (int)(hi - t0 < SC ? hi - t0 : SC);
 
   const int dtile = w % NDT, ttile0 = (w / NDT) * TT;       // this wave's tiles of the [Dk][tokens] products
   const bool mine = NDT > 1 || w < 4;                       // (a state of 16 rows leaves four waves without)
-  const int pairs = p.r * a.nslab;                          // (head, slab) steps
+  const int pairs = nhd * a.nslab;                          // (head, slab) steps
 
   // rows and states of step q on their way
   TileRegs<TI, SP, LX, NT> rx, ry;
   float rs[NSC][KE], rd[NSC][KE];  // this lane's row of S and dS: 64 columns, KE per step
   auto load_rows = [&](int q) {
-    const int h = kh * p.r + q / a.nslab, slab = q % a.nslab;
+    const int h = hd0 + q / a.nslab, slab = q % a.nslab;
     const int ncols = p.Dv - slab * SP < SP ? p.Dv - slab * SP : SP;
     rx.init(p.x_rs, ncols);
     ry.init(p.dy_rs, ncols);
@@ -103,7 +113,7 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
     ry.template load<true>((const TI*)p.dy + t0 * p.dy_rs + (int64_t)h * p.Dv + slab * SP, len);
   };
   auto load_state = [&](int q, int s) {
-    const int h = kh * p.r + q / a.nslab, slab = q % a.nslab;
+    const int h = hd0 + q / a.nslab, slab = q % a.nslab;
     const int64_t base = (slot * p.Hv + h) * (int64_t)DK * p.Dv;
     const uint32_t bytes = (uint32_t)(DK * p.Dv) * 4u;
     const __amdgpu_buffer_rsrc_t bs = rows_rsrc(a.sv + base, bytes), bd = rows_rsrc(a.ds + base, bytes);
@@ -128,11 +138,11 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
   // the gates of head hh + w (one head of a batch to a wave)
   float rdt = 0.f;
   auto load_dt = [&](int hh) {
-    rdt = w < HB && hh + w < p.r && l < len ? p.dt[(t0 + l) * p.Hv + kh * p.r + hh + w] : 0.f;
+    rdt = w < HB && hh + w < nhd && l < len ? p.dt[(t0 + l) * p.Hv + hd0 + hh + w] : 0.f;
   };
   auto gates = [&](int hh) {
-    if (w >= HB || hh + w >= p.r) return;
-    const int h = kh * p.r + hh + w, b = (hh / HB) & 1;
+    if (w >= HB || hh + w >= nhd) return;
+    const int h = hd0 + hh + w, b = (hh / HB) & 1;
     const Gate q = chunk_gate(rdt, p.dt_bias ? p.dt_bias[h] : 0.f, neg_a_log2(p.a_log[h]), l < len);
     const float h32 = (float)q.gam;
     float(*gt)[SC] = sh[b][w];
@@ -289,11 +299,11 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
         sfr[hb][w] = mine && ttile0 == 0 ? fsum : 0.f;  // (each row of the states once)
         sdd[hb][w] = dsum;
       }
-      if (hb == HB - 1 || hh == p.r - 1) {
+      if (hb == HB - 1 || hh == nhd - 1) {
         lds_barrier();  // the batch's sums are complete
         const int h0 = hh - hb;
         if (w <= hb) {  // one head, one token per lane
-          const int h = kh * p.r + h0 + w, ti = l >> 4, b = (h0 / HB) & 1;
+          const int h = hd0 + h0 + w, ti = l >> 4, b = (h0 / HB) & 1;
           const float(*gw)[SC] = sh[b][w];
           // Pairs (i, j) on both sides of t, by tiles of 16: those of t's own tile as a difference of row
           // and column sums over that tile alone, the others as sums of what is on the far side (over
@@ -344,7 +354,7 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
             a.part[2 * plane + at] = dsum8;
           }
         }
-        if (hh + 1 < p.r) {
+        if (hh + 1 < nhd) {
           gates(hh + 1);
           load_dt(hh + 1 + HB);
         }
@@ -388,13 +398,57 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
   for (int y = 0; y < TT; ++y) {
     const int t = 16 * (ttile0 + y) + r, d0 = kh * DK + 16 * dtile + 4 * g;
     if (t >= len) continue;
+    if (a.parts > 1) {
+      float* f = a.fold + ((int64_t)pt * p.T_total + t0 + t) * (p.Hk * DK) + d0;
+      st4<float>(f, dC[y]);
+      st4<float>(f + (int64_t)a.parts * p.T_total * (p.Hk * DK), dB[y]);
+      continue;
+    }
     st4<TI>((TI*)p.dc + (t0 + t) * p.dc_rs + d0, dC[y]);
     st4<TI>((TI*)p.db + (t0 + t) * p.db_rs + d0, dB[y]);
   }
 }
 
+// dc and db of a chunk and group as the sum of the group's parts, in order, rounded once. Few bytes, bound
+// by latency: grid (slot and group, output, 256 threads of four values each), the parts' loads side by side.
+template <typename TI> __global__ __launch_bounds__(256) void k_ssm_fold(GradArgs a) {
+  const SsmArgs& p = a.p;
+  const int kh = (int)(blockIdx.x % p.Hk), kw = p.Hk * p.Dk;
+  int64_t t0;
+  const int len = slot_chunk(p, blockIdx.x / p.Hk, t0), cpr = p.Dk / 4;
+  const float* f = a.fold + (blockIdx.y ? (int64_t)a.parts * p.T_total * kw : 0);
+  TI* o = (TI*)(blockIdx.y ? p.db : p.dc);
+  const int64_t rs = blockIdx.y ? p.db_rs : p.dc_rs;
+  const int i = (int)(blockIdx.z * 256 + threadIdx.x);
+  if (i >= len * cpr) return;
+  const int64_t t = t0 + i / cpr;
+  const int d = kh * p.Dk + i % cpr * 4;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int q = 0; q < a.parts; ++q) v += ld4<float>(f + ((int64_t)q * p.T_total + t) * kw + d);
+  st4<TI>(o + t * rs + d, v);
+}
+
+// Workgroups to a group: a chunk's heads are a serial chain, so a short batch's groups are dealt over
+// several workgroups (one fits a compute unit) and their dc and db added afterwards. Measured (bf16, heads of
+// 128 x 64): 4096 tokens, 32 heads in one group 171 us, in four parts 70 + 6; 8192 tokens, 4 heads in one
+// group 36, in two 30 + 6; 512 tokens, 16 heads in one group 83, in 16 parts 18 + 5.
+constexpr int kGradGroups = 256;
+static int grad_hpp(const SsmArgs& p) {
+  const bool packed = p.cu && p.N > 1;  // (a packed batch's lengths are not known here)
+  const int64_t chunks = packed ? ssm_slots(p.T_total, p.N) : p.N * (((p.cu ? p.T_total : p.T) + SC - 1) / SC);
+  const int64_t groups = chunks * p.Hk;
+  int64_t parts = groups > 0 ? kGradGroups / groups : 1;
+  if (parts > p.r) parts = p.r;
+  return parts > 1 ? (int)((p.r + parts - 1) / parts) : p.r;
+}
+size_t ssm_fold_bytes(const SsmArgs& p) {
+  const int hpp = grad_hpp(p), parts = (p.r + hpp - 1) / hpp;
+  return parts > 1 ? (size_t)2 * parts * p.T_total * p.Hk * p.Dk * 4 : 0;
+}
+
 template <typename TI> static hipError_t grad_d(const GradArgs& a, hipStream_t s) {
-  const unsigned grid = (unsigned)(a.slots * a.p.Hk);
+  const unsigned grid = (unsigned)(a.slots * a.p.Hk * a.parts);
   switch (a.p.Dk) {
     case 16: traced("k_ssm_grad", s, [&] { k_ssm_grad<TI, 16><<<grid, 512, 0, s>>>(a); }); break;
     case 32: traced("k_ssm_grad", s, [&] { k_ssm_grad<TI, 32><<<grid, 512, 0, s>>>(a); }); break;
@@ -402,15 +456,21 @@ template <typename TI> static hipError_t grad_d(const GradArgs& a, hipStream_t s
     case 128: traced("k_ssm_grad", s, [&] { k_ssm_grad<TI, 128><<<grid, 512, 0, s>>>(a); }); break;
     default: return hipErrorInvalidValue;
   }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.parts == 1) return e;
+  traced("k_ssm_fold", s, [&] { k_ssm_fold<TI><<<dim3((unsigned)(a.slots * a.p.Hk), 2, (unsigned)(a.p.Dk / 16)), 256, 0, s>>>(a); });
   return hipGetLastError();
 }
 
-hipError_t launch_ssm_grad(const SsmArgs& p, int dtype, const float* ds, float* part, hipStream_t s) {
+hipError_t launch_ssm_grad(const SsmArgs& p, int dtype, const float* ds, float* part, float* fold, hipStream_t s) {
   GradArgs a;
   a.p = p;
   a.sv = p.sv;
   a.ds = ds;
   a.part = part;
+  a.fold = fold;
+  a.hpp = grad_hpp(p);
+  a.parts = (p.r + a.hpp - 1) / a.hpp;
   a.nslab = (p.Dv + SP - 1) / SP;
   a.slots = ssm_slots(p.T_total, p.N);
   return dtype == 0 ? grad_d<float>(a, s) : grad_d<__bf16>(a, s);

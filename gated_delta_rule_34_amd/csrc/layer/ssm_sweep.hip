@@ -377,19 +377,20 @@ hipError_t launch_ssm_forward(const SsmArgs& a, int dtype, hipStream_t s) {
   return dtype == 0 ? sweep_d<float, false>(a, a.sv, a.ws, s) : sweep_d<__bf16, false>(a, a.sv, a.ws, s);
 }
 
-// Backward workspace: the adjoints at the chunks' ends, the parameters' partials, the segments.
+// Backward workspace: the adjoints at the chunks' ends, the parameters' partials, the groups' parts, the segments.
 size_t ssm_bwd_ws_bytes(const SsmArgs& a) {
-  return up256(ssm_saved_bytes(a)) + up256((size_t)ssm_slots(a.T_total, a.N) * 3 * a.Hv * 4) + seg_bytes(a);
+  return up256(ssm_saved_bytes(a)) + up256((size_t)ssm_slots(a.T_total, a.N) * 3 * a.Hv * 4) + up256(ssm_fold_bytes(a)) + seg_bytes(a);
 }
 
 hipError_t launch_ssm_backward(const SsmArgs& a, int dtype, hipStream_t s) {
   float* ds = a.ws;
   float* part = ds + up256(ssm_saved_bytes(a)) / 4;
-  float* seg = part + up256((size_t)ssm_slots(a.T_total, a.N) * 3 * a.Hv * 4) / 4;
+  float* fold = part + up256((size_t)ssm_slots(a.T_total, a.N) * 3 * a.Hv * 4) / 4;
+  float* seg = fold + up256(ssm_fold_bytes(a)) / 4;
   hipError_t e = hipSuccess;
   if (a.N > 0) {
     e = dtype == 0 ? sweep_d<float, true>(a, ds, seg, s) : sweep_d<__bf16, true>(a, ds, seg, s);
-    if (e == hipSuccess && ssm_slots(a.T_total, a.N) > 0) e = launch_ssm_grad(a, dtype, ds, part, s);
+    if (e == hipSuccess && ssm_slots(a.T_total, a.N) > 0) e = launch_ssm_grad(a, dtype, ds, part, fold, s);
   }
   if (e == hipSuccess && (a.da_log || a.ddt_bias || a.dd_skip))
     e = launch_colsum(part, ssm_slots(a.T_total, a.N), a.Hv, ColsumOut{{a.da_log, a.ddt_bias, a.dd_skip}}, 3, s);

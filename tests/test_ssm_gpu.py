@@ -98,6 +98,15 @@ def test_scan_few_long_sequences(dtype, lens):
     check(a, up, cu, dtype, run(*place(a, up, cu, dtype, packed=False)))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("r,lens", [(7, [1000]), (9, [2500, 100]), (17, [70, 20])])
+def test_scan_groups_of_many_heads(dtype, r, lens):
+    """A group's heads by several workgroups with an uneven share, by one workgroup over more than it
+    takes at a time, and by one workgroup each."""
+    a, up, cu = make(lens, 4, 4 * r, 16, 32, dtype, seed=r)
+    check(a, up, cu, dtype, run(*place(a, up, cu, dtype)))
+
+
 @pytest.mark.parametrize("r", [1, 7])
 def test_scan_equal_lengths_and_missing_parts(r):
     """No cu_seqlens, no bias, no skip, no initial state, no dS_T; the gradients nobody asks for are skipped."""

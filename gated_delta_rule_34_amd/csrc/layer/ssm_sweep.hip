@@ -40,6 +40,8 @@ struct SweepArgs {
 // output), the decays with which a token reads and writes the state.
 enum { G_HI, G_LO, G_IN, G_RD, G_WR, G_ROWS };
 
+constexpr int kMinChunks = 2;  // least chunks of a segment
+
 template <typename TI, int DK> constexpr int sweep_waves() { return sizeof(TI) == 4 ? 2 : 4; }  // per SIMD
 
 template <typename TI, int DK, bool REV, bool OUT>
@@ -67,7 +69,7 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
     grp = blockIdx.x / (a.r * a.nslab);
     mem = blockIdx.x % (a.r * a.nslab);
   }
-  const int kh = grp % a.Hk, sgm = (grp / a.Hk) % segs, n = grp / a.Hk / segs;
+  const int kh = grp % a.Hk, n = (grp / a.Hk) % a.N, sgm = grp / a.Hk / a.N;
   const int h = kh * a.r + mem / a.nslab, slab = mem % a.nslab;
   const int w = wave_id(), l = lane_id(), g = l >> 4, r = l & 15;
   const int cw = w & 3, hf = w >> 2;            // this wave's columns and half
@@ -79,8 +81,11 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
 
   int64_t lo, hi;
   ssm_seq(a.cu, a.T, a.T_total, n, lo, hi);
-  const int nch = (int)((hi - lo + SC - 1) / SC), cps = (nch + a.S - 1) / a.S;
-  const int k0 = min(nch, sgm * cps), k1 = min(nch, k0 + cps);
+  // a short sequence takes fewer segments than the batch has: the workgroups of the others have nothing to do
+  const int nch = (int)((hi - lo + SC - 1) / SC), cps = max((nch + a.S - 1) / a.S, kMinChunks);
+  const int last = max(nch - 1, 0) / cps;  // the segment with the sequence's end
+  if (OUT ? sgm > last : sgm >= last) return;
+  const int k0 = sgm * cps, k1 = min(nch, k0 + cps);
 
   const double neg_a = neg_a_log2(a.a_log[h]);
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
@@ -286,7 +291,7 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
     }
   }
   if constexpr (OUT) {
-    if (a.st && has && sgm == a.S - 1) {
+    if (a.st && has && sgm == last) {
       float* st = a.st + nh * DK * a.Dv + col0 + r;
 #pragma unroll
       for (int t = 0; t < ND; ++t)
@@ -302,18 +307,18 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   }
 }
 
-// Segments per sequence: two workgroups to a compute unit, each with at least kMinChunks chunks on
-// average. A segment costs its states and a second read of its rows, so two gain nothing (4 x 4096
-// tokens, 64 heads: one segment 243 us, two 247), more do (16384 tokens, 32 heads: 8 of them 180 us,
-// 16 of them 150; 16 x 512 tokens, 4 heads: one 34, four 28). A packed batch's lengths are not known
-// here, and its longest sequence may hold most of the tokens: short averages get three all the same
-// (lengths up to 777 with an average of 190, float32: 123 -> 77 us for both sweeps).
-constexpr int kWantGroups = 512, kMinChunks = 2, kMaxSegments = 32;
+// Segments per sequence: two workgroups to a compute unit, at most one for every kMinChunks chunks of the
+// longest sequence there can be. A segment costs its states and a second read of its rows, so two gain
+// nothing (4 x 4096 tokens, 64 heads: one segment 243 us, two 247), more do (16384 tokens, 32 heads: 8 of
+// them 180 us, 16 of them 150; 300 tokens, 8 heads: one 21, three 18). A packed batch's lengths are not
+// known here: its short sequences leave their further segments empty (lengths up to 777, 6 heads of 32 x 32,
+// float32, training step: three segments 104 us, seven 72; 16 x 512 tokens, 4 heads: 27 and 24 us; 3000, 1000
+// and 200 tokens, 32 heads: 67 and 73).
+constexpr int kWantGroups = 512, kMaxSegments = 32;
 static int ssm_segments(const SsmArgs& a) {
   if (a.N == 0) return 1;
-  const int64_t groups = (int64_t)a.N * a.Hv * ((a.Dv + SP - 1) / SP), chunks = a.T_total / SC;
-  int64_t most = chunks / a.N / kMinChunks;
-  if (a.cu && a.N > 1 && most < 3 && chunks >= 3 * kMinChunks) most = 3;
+  const int64_t groups = (int64_t)a.N * a.Hv * ((a.Dv + SP - 1) / SP);
+  const int64_t longest = ((a.cu ? a.T_total : a.T) + SC - 1) / SC, most = (longest + kMinChunks - 1) / kMinChunks;
   int64_t s = kWantGroups / groups;
   if (s > most) s = most;
   if (s > kMaxSegments) s = kMaxSegments;
@@ -346,10 +351,12 @@ template <typename TI, int DK, bool REV> static hipError_t sweep_go(const SsmArg
   v.loc = seg;
   v.dec = seg + (v.S > 1 ? up256((size_t)a.N * v.S * a.Hv * v.nslab * (DK < 32 ? 32 : DK) * SP * 4) / 4 : 0);
   // A group's heads share b and c: with many groups they go to one XCD (workgroups are dealt to
-  // the eight XCDs in turn) and share its L2; few groups would leave XCDs idle.
+  // the eight XCDs in turn) and share its L2; few groups would leave XCDs idle. A packed batch's segments
+  // are dealt one by one: a long sequence's would else meet on a few compute units (1500, 20, 300, 44, 5
+  // and 700 tokens, 24 heads: 47 us, so 37). Later segments come last, the empty ones behind the others.
   auto grid = [&](int segs) {
     const int G = a.N * segs * a.Hk, m = a.r * v.nslab;
-    v.xcd = G >= 32;
+    v.xcd = G >= 32 && !(v.S > 1 && a.cu && a.N > 1);
     return v.xcd ? xcd_grid(G, m) : G * m;
   };
   if (v.S > 1) {

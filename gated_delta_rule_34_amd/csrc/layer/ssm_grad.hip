@@ -410,16 +410,37 @@ __global__ __launch_bounds__(512, 2) void k_ssm_grad(GradArgs a) {
 }
 
 // dc and db of a chunk and group as the sum of the group's parts, in order, rounded once. Few bytes, bound
-// by latency: grid (slot and group, output, 256 threads of four values each), the parts' loads side by side.
-template <typename TI> __global__ __launch_bounds__(256) void k_ssm_fold(GradArgs a) {
+// by latency: a thread takes four values, the parts' loads side by side. The first workgroups, 16 heads
+// each, do what k_colsum does for longer columns (a launch of its own took 5 us).
+template <typename TI> __global__ __launch_bounds__(256) void k_ssm_fold(GradArgs a, ColsumOut sums, int heads) {
   const SsmArgs& p = a.p;
-  const int kh = (int)(blockIdx.x % p.Hk), kw = p.Hk * p.Dk;
+  if ((int)blockIdx.x < 3 * heads) {
+    __shared__ double acc[16][17];
+    const int plane = (int)blockIdx.x / heads, c = threadIdx.x & 15, k = threadIdx.x >> 4;
+    const int h = (int)blockIdx.x % heads * 16 + c;
+    const float* in = a.part + (int64_t)plane * a.slots * p.Hv;
+    double s = 0.0;
+    if (h < p.Hv) {
+#pragma unroll 8
+      for (int64_t r = k; r < a.slots; r += 16) s += (double)in[r * p.Hv + h];
+    }
+    acc[k][c] = s;
+    __syncthreads();
+    if (k == 0 && h < p.Hv && sums.p[plane]) {
+#pragma unroll
+      for (int i = 1; i < 16; ++i) s += acc[i][c];
+      sums.p[plane][h] = (float)s;
+    }
+    return;
+  }
+  const int per = p.Dk / 16, kw = p.Hk * p.Dk, cpr = p.Dk / 4;
+  const int x = (int)blockIdx.x - 3 * heads, which = x / per & 1, sk = x / (2 * per), kh = sk % p.Hk;
   int64_t t0;
-  const int len = slot_chunk(p, blockIdx.x / p.Hk, t0), cpr = p.Dk / 4;
-  const float* f = a.fold + (blockIdx.y ? (int64_t)a.parts * p.T_total * kw : 0);
-  TI* o = (TI*)(blockIdx.y ? p.db : p.dc);
-  const int64_t rs = blockIdx.y ? p.db_rs : p.dc_rs;
-  const int i = (int)(blockIdx.z * 256 + threadIdx.x);
+  const int len = slot_chunk(p, sk / p.Hk, t0);
+  const float* f = a.fold + (which ? (int64_t)a.parts * p.T_total * kw : 0);
+  TI* o = (TI*)(which ? p.db : p.dc);
+  const int64_t rs = which ? p.db_rs : p.dc_rs;
+  const int i = x % per * 256 + (int)threadIdx.x;
   if (i >= len * cpr) return;
   const int64_t t = t0 + i / cpr;
   const int d = kh * p.Dk + i % cpr * 4;
@@ -457,8 +478,13 @@ template <typename TI> static hipError_t grad_d(const GradArgs& a, hipStream_t s
     default: return hipErrorInvalidValue;
   }
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.parts == 1) return e;
-  traced("k_ssm_fold", s, [&] { k_ssm_fold<TI><<<dim3((unsigned)(a.slots * a.p.Hk), 2, (unsigned)(a.p.Dk / 16)), 256, 0, s>>>(a); });
+  if (e != hipSuccess) return e;
+  const ColsumOut sums{{a.p.da_log, a.p.ddt_bias, a.p.dd_skip}};
+  const bool any = a.p.da_log || a.p.ddt_bias || a.p.dd_skip;
+  if (a.parts == 1) return any ? launch_colsum(a.part, a.slots, a.p.Hv, sums, 3, s) : hipSuccess;
+  const int heads = any ? (a.p.Hv + 15) / 16 : 0;
+  const unsigned blocks = (unsigned)(3 * heads + a.slots * a.p.Hk * 2 * (a.p.Dk / 16));
+  traced("k_ssm_fold", s, [&] { k_ssm_fold<TI><<<blocks, 256, 0, s>>>(a, sums, heads); });
   return hipGetLastError();
 }
 

@@ -397,10 +397,10 @@ hipError_t launch_ssm_backward(const SsmArgs& a, int dtype, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (a.N > 0) {
     e = dtype == 0 ? sweep_d<float, true>(a, ds, seg, s) : sweep_d<__bf16, true>(a, ds, seg, s);
-    if (e == hipSuccess && ssm_slots(a.T_total, a.N) > 0) e = launch_ssm_grad(a, dtype, ds, part, fold, s);
+    return e == hipSuccess ? launch_ssm_grad(a, dtype, ds, part, fold, s) : e;
   }
-  if (e == hipSuccess && (a.da_log || a.ddt_bias || a.dd_skip))
-    e = launch_colsum(part, ssm_slots(a.T_total, a.N), a.Hv, ColsumOut{{a.da_log, a.ddt_bias, a.dd_skip}}, 3, s);
+  if (a.da_log || a.ddt_bias || a.dd_skip)  // nothing to sum
+    e = launch_colsum(part, 0, a.Hv, ColsumOut{{a.da_log, a.ddt_bias, a.dd_skip}}, 3, s);
   return e;
 }
 

@@ -121,9 +121,23 @@ static PyObject *m_call(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return PyLong_FromLong(st);
 }
 
+/* size(function's address, problem) -> bytes. */
+static PyObject *m_size(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  if (n != 2) return PyErr_Format(PyExc_TypeError, "size takes 2 arguments");
+  size_t (*f)(const void *) = (size_t (*)(const void *))(uintptr_t)PyLong_AsUnsignedLongLong(a[0]);
+  if (PyErr_Occurred()) return NULL;
+  Py_buffer p;
+  if (PyObject_GetBuffer(a[1], &p, PyBUF_SIMPLE)) return NULL;
+  const size_t bytes = f(p.buf);
+  PyBuffer_Release(&p);
+  return PyLong_FromSize_t(bytes);
+}
+
 static PyMethodDef methods[] = {{"rows", (PyCFunction)(void (*)(void))m_rows, METH_FASTCALL, "layout of a row view"},
                                 {"array", (PyCFunction)(void (*)(void))m_array, METH_FASTCALL, "address of an array"},
                                 {"call", (PyCFunction)(void (*)(void))m_call, METH_FASTCALL, "call a function of the C ABI"},
+                                {"size", (PyCFunction)(void (*)(void))m_size, METH_FASTCALL, "call a size query of the C ABI"},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "inner steps of the binding", -1, methods,
                                     NULL, NULL, NULL, NULL};

@@ -74,13 +74,23 @@ def _fn(name):
 _address = {}
 
 
-def _call(name, p, *args):
+def _at(name):
     at = _address.get(name)
     if at is None:
         at = _address[name] = ctypes.cast(_fn(name), ctypes.c_void_p).value
-    st = _marshal.call(at, p, *args)
+    return at
+
+
+def _call(name, p, *args):
+    st = _marshal.call(_at(name), p, *args)
     if st != GDN_OK:
         raise GdnError(st, name)
+
+
+def _ws_bytes(name, p, kind):
+    if not isinstance(p, kind):
+        raise TypeError(f"{name}: expected a {kind.__name__}, got {type(p).__name__}")
+    return _marshal.size(_at(name), p)
 
 
 # ------------------------------------------------------------------------------------ checks
@@ -186,15 +196,15 @@ def make_ssm_problem(N, T_total, Hk, Hv, Dk, Dv, *, a_log, dt_bias=None, d_skip=
 
 
 def gdn_ssm_fwd_workspace_bytes(p) -> int:
-    return _fn("gdn_ssm_fwd_workspace_bytes")(p)
+    return _ws_bytes("gdn_ssm_fwd_workspace_bytes", p, gdn_ssm_problem)
 
 
 def gdn_ssm_bwd_workspace_bytes(p) -> int:
-    return _fn("gdn_ssm_bwd_workspace_bytes")(p)
+    return _ws_bytes("gdn_ssm_bwd_workspace_bytes", p, gdn_ssm_problem)
 
 
 def gdn_ssm_chunk_state_bytes(p) -> int:
-    return _fn("gdn_ssm_chunk_state_bytes")(p)
+    return _ws_bytes("gdn_ssm_chunk_state_bytes", p, gdn_ssm_problem)
 
 
 def _ssm_ins(p, x, b, c, dt, device, dtype):
@@ -207,9 +217,9 @@ def _saved(p, states, device):
     """Address of the saved chunk states, large enough for the problem."""
     if states is None:
         return None
-    at, size = _scratch(states, device)
-    if size < gdn_ssm_chunk_state_bytes(p):
-        raise ValueError(f"chunk_states: {gdn_ssm_chunk_state_bytes(p)} bytes needed, got {size}")
+    (at, size), need = _scratch(states, device), gdn_ssm_chunk_state_bytes(p)
+    if size < need:
+        raise ValueError(f"chunk_states: {need} bytes needed, got {size}")
     return at
 
 
@@ -334,16 +344,12 @@ def _weight(p, t, name, device):
     return _array(t, name, (groups, p.width) if t is not None and t.dim() == 2 else (groups * p.width,), device, _f32)
 
 
-def _ws_bytes(name, p):
-    return _fn(name)(p)
-
-
 def gdn_gated_norm_bwd_workspace_bytes(p) -> int:
-    return _ws_bytes("gdn_gated_norm_bwd_workspace_bytes", p)
+    return _ws_bytes("gdn_gated_norm_bwd_workspace_bytes", p, gdn_norm_problem)
 
 
 def gdn_add_norm_bwd_workspace_bytes(p) -> int:
-    return _ws_bytes("gdn_add_norm_bwd_workspace_bytes", p)
+    return _ws_bytes("gdn_add_norm_bwd_workspace_bytes", p, gdn_norm_problem)
 
 
 def gdn_gated_norm_fwd(p, x, z, w, y, stream=None):

@@ -269,6 +269,35 @@ def test_scan_empty_batches():
     assert y.shape[0] == 0 and ST.shape[0] == 0 and bool((g["da_log"] == 0).all())
 
 
+def test_scan_offsets_past_32_bits():
+    """Sequences behind nine million rows of none: rows, gradients and steps past 2^32 bytes."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    T, width = 9_000_000, 128
+    a, up, cu = make([100, 64], 1, 2, 16, 16, "f32", seed=29)
+    first = T - cu[-1]
+    rows = torch.empty(2, T, width, device="cuda")  # inputs (x, b, c, dy) and outputs (dx, db, dc, y)
+    cols = dict(x=(0, 32), b=(32, 16), c=(48, 16), dy=(64, 32))
+    d = {k: rows[0, :, at:at + n] for k, (at, n) in cols.items()}
+    outs = {k: rows[1, :, at:at + n] for k, (at, n) in zip(("dx", "db", "dc", "y"), cols.values())}
+    for k in d:
+        src = up["dy"] if k == "dy" else a[k]
+        d[k][first:] = dev(src.reshape(cu[-1], cols[k][1]), "f32")
+    dt = torch.empty(T, 2, device="cuda")
+    dt[first:] = dev(a["dt"])
+    p = G.make_ssm_problem(2, T, 1, 2, 16, 16, a_log=(al := dev(a["a_log"])), dt_bias=dev(a["dt_bias"]), d_skip=dev(a["d_skip"]),
+                           cu_seqlens=torch.tensor([first + c for c in cu], dtype=torch.int32, device="cuda"), dtype="f32")
+    y, ST, sv = G.ssm_forward(p, d["x"], d["b"], d["c"], dt, dev(a["S0"]), y=outs["y"])
+    g = dict(dx=outs["dx"], db=outs["db"], dc=outs["dc"], ddt=torch.empty_like(dt), da_log=torch.empty_like(al),
+             ddt_bias=torch.empty_like(al), dd_skip=torch.empty_like(al), dS0=torch.empty_like(ST))
+    G.ssm_backward(p, d["x"], d["b"], d["c"], dt, None, sv, d["dy"], dev(up["dST"]), grads=g)
+    out = dict(g, y=y, S_T=ST)
+    for k in ("y", "dx", "db", "dc", "ddt"):
+        out[k] = out[k][first:]
+    check(a, up, cu, "f32", out)
+
+
 # ------------------------------------------------------------------------------------ single tokens
 
 
@@ -320,3 +349,20 @@ def test_decode_continues_a_prompt():
         G.gdn_ssm_decode(G.make_ssm_problem(2, 2, 1, 3, 64, 64, T=1, **kw), *take(t), state, None, y)
         assert rel(host(y), host(whole["y"][rows[t]])) <= 1e-5
     assert rel(host(state), host(whole["S_T"])) <= 1e-5
+
+
+def test_decode_slots_past_32_bits():
+    """A pool of 1100 slots of 4 MiB: the last slot's state is behind 2^32 bytes."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    a, up, cu = make([1, 1], 1, 64, 128, 128, "bf16", seed=31)
+    _, d = place(a, up, cu, "bf16")
+    p = G.make_ssm_problem(2, 2, 1, 64, 128, 128, T=1, a_log=d["a_log"], dt_bias=d["dt_bias"], d_skip=d["d_skip"], dtype="bf16")
+    pool, small = torch.empty(1100, 64, 128, 128, device="cuda"), d["S0"].clone()
+    idx = torch.tensor([1099, 3], dtype=torch.int32, device="cuda")
+    pool[idx.long()] = small
+    y, want = (torch.empty(2, 64 * 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    G.gdn_ssm_decode(p, d["x"], d["b"], d["c"], d["dt"], pool, idx, y)
+    G.gdn_ssm_decode(p, d["x"], d["b"], d["c"], d["dt"], small, None, want)
+    assert torch.equal(y, want) and torch.equal(pool[idx.long()], small)

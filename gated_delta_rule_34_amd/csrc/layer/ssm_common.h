@@ -27,8 +27,10 @@ template <typename T, int Cn> struct PadRow {
 };
 
 // bfloat16 terms that a float32 factor is split into as a matrix operand: three (24 bits) where
-// the result is float32, one where it is rounded to bfloat16 anyway.
+// the result is float32, two (16 bits) where it is a bfloat16 row. One term's rounding would be as
+// large as the row's own, and larger where the row's terms cancel.
 template <typename TI> constexpr int ssm_split() { return sizeof(TI) == 2 ? 3 : 1; }
+template <typename TI> constexpr int out_split() { return sizeof(TI) == 2 ? 2 : 1; }
 
 template <typename TI, int KS> using FragT = typename Mf<TI, KS>::frag;
 

@@ -6,17 +6,19 @@
 // (w mod 4) and half of the state's rows (w / 4) in its accumulators; columns of the state never mix,
 // and the two halves' shares of S^T Q meet in LDS. Per chunk the products K Q^T, S^T Q, K^T (w X) and
 // M X run on the matrix cores; every product is formed transposed, so that a lane holds four adjacent
-// columns of one token. The next chunk's rows are in registers while a chunk is computed. A chunk is
-// a chain of short dependent products, bound by their latency and the LDS: eight waves of 128 registers,
-// so that two workgroups (four waves per SIMD) share a compute unit, hide what four waves of 230 (or one
-// workgroup of eight with 165) did not. Measured (bf16, 4 x 4096 tokens, 64 heads of 128 x 64 in 8
-// groups): 245 us without and 270 us with saved states (0.54 GB more written), 280 us in reverse; the
-// rows alone would take a copy 66 us. A chunk takes a workgroup some 8000 cycles.
+// columns of one token. M and the state enter the products of an output as two bfloat16 terms each, so that a
+// row carries no rounding but its own (as one term each, whose rounding does not shrink where a row's terms
+// cancel, y and dx were 1.9e-3 off the 64-bit result instead of 1.66e-3, for 5% less time). The next chunk's
+// rows are in registers while a chunk is computed. A chunk is a chain of short dependent products with three
+// barriers. Eight waves of 128 registers and 81 KB of LDS let two workgroups (four waves per SIMD) share
+// a compute unit where there are that many. Measured (bf16, 4 x 4096 tokens, 64 heads of 128 x 64 in 8 groups,
+// which is one workgroup to a compute unit): 264 us without and 298 us with saved states (0.54 GB more written),
+// 300 us in reverse; the rows alone would take a copy 66 us. A chunk takes a workgroup some 9000 cycles.
 //
 // Few sequences and heads leave compute units idle over a long serial chain, so a sequence is then
 // cut into S segments: a first launch runs the state alone over all segments but the last, from
 // zero, and the second starts each segment from the earlier segments' states and decays (16384 tokens, 32 heads in one group:
-// 47 us for the states, 94 us for the outputs).
+// 49 us for the states, 109 us for the outputs).
 #include "ssm_common.h"
 
 namespace gdn {
@@ -49,14 +51,14 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   constexpr int NT = 512, DH = DK >= 32 ? DK / 2 : 16, ND = DH / 16;  // this wave's rows of the state
   constexpr int KSD = ks_of<TI, DK>(), NSD = DK / KSD, KSC = ks_of<TI, SC>(), NSC = SC / KSC;
   constexpr int KSH = ks_of<TI, DH>(), NSH = DH / KSH;
-  constexpr int NS = ssm_split<TI>(), TRI = REV ? TRI_UP : TRI_LOW, GB = 3, GR = GB + 1;
+  constexpr int NS = ssm_split<TI>(), NO = out_split<TI>(), TRI = REV ? TRI_UP : TRI_LOW, GB = 3, GR = GB + 1;
   using LK = PadRow<TI, DK>;
   using LX = Swz<TI, SP, true>;
   using LM = Swz<TI, SC, false>;
   __shared__ __align__(16) TI sK[LK::size(SC)];
   __shared__ __align__(16) TI sQ[OUT ? LK::size(SC) : 8];
-  __shared__ __align__(16) TI sX2[2][SC * SP];
-  __shared__ __align__(16) TI sM[OUT ? SC * SC : 8];
+  __shared__ __align__(16) TI sX[SC * SP];
+  __shared__ __align__(16) TI sM[OUT ? NO : 1][OUT ? SC * SC : 8];  // M, as NO terms that add up to it
   __shared__ __align__(16) f32x4 sP[OUT ? 8 * 2 * 64 : 1];  // shares of S^T Q for the other half
   __shared__ __align__(16) float sg[GR][G_ROWS][SC];
   __shared__ float sbn[GR];
@@ -155,11 +157,11 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
 #pragma unroll
       for (int t = 0; t < ND; ++t) S[t] = d * S[t] + p[t * NT];
     }
-    for (int i = threadIdx.x; i < SC * SC; i += NT) sM[i] = (TI)0.f;  // the tiles past the diagonal stay zero
+    for (int i = threadIdx.x; i < NO * SC * SC; i += NT) sM[0][i] = (TI)0.f;  // the tiles past the diagonal stay zero
   }
   float dec = 1.f;
-  auto save = [&](int k) {  // the state before chunk k
-    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(a.sv + ((lo / SC + n + chunk(k)) * a.Hv + h) * (int64_t)DK * a.Dv, DK * a.Dv * 4);
+  auto put = [&](float* st) {  // the state as [Dk][Dv] of one head
+    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(st, DK * a.Dv * 4);
     const uint32_t voff = (uint32_t)(d0 * a.Dv + col0 + r) * 4u;
 #pragma unroll
     for (int t = 0; t < ND; ++t)
@@ -169,6 +171,9 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rs, (int)voff, (16 * t + e) * a.Dv * 4, 0);
       }
   };
+  auto save = [&](int k) {  // the state before chunk k
+    put(a.sv + ((lo / SC + n + chunk(k)) * a.Hv + h) * (int64_t)DK * a.Dv);
+  };
 
   if (k0 < k1) {
     if (OUT && a.sv && has) save(k0);
@@ -176,12 +181,11 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
     load_dt(k0 + GB + w);
     rk.store(sK);
     if constexpr (OUT) rq.store(sQ);
-    rx.store(sX2[k0 & 1]);
+    rx.store(sX);
   }
   for (int k = k0; k < k1; ++k) {
-    const int buf = k & 1, c = chunk(k), len = clen(c);
+    const int c = chunk(k), len = clen(c);
     const int64_t t0 = lo + (int64_t)c * SC;
-    const TI* sX = sX2[buf];
     lds_barrier();  // the chunk's rows and gates are in LDS, M and the shares are free
     if (k + 1 < k1) load(k + 1);
     const float(*gt)[SC] = sg[(k - k0) & (GR - 1)];
@@ -210,7 +214,14 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
           if constexpr (!REV) m[e] *= wi[e];
           m[e] = in ? m[e] : 0.f;
         }
-        st4<TI>(sM + LM::at(i, j0), m);
+#pragma unroll
+        for (int q = 0; q < NO; ++q) {
+          st4<TI>(sM[q] + LM::at(i, j0), m);
+          if (q + 1 < NO) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m[e] -= (float)(TI)m[e];
+          }
+        }
       }
       // this half's share of S^T Q, decayed; two token tiles of it go to the other half
 #pragma unroll
@@ -218,11 +229,14 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
       if (has) {
 #pragma unroll
         for (int s = 0; s < NSH; ++s) {
-          FragT<TI, KSH> sf[1];
-          acc_split<TI, KSH, 1>(S, s, sf);
+          FragT<TI, KSH> sf[NO];
+          acc_split<TI, KSH, NO>(S, s, sf);
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
-            o[t] = Mf<TI, KSH>::run(sf[0], ld_n<TI, KSH, ACC, LK>(sQ, 16 * t, hf * NSH + s), o[t]);
+          for (int t = 0; t < 4; ++t) {
+            const FragT<TI, KSH> qf = ld_n<TI, KSH, ACC, LK>(sQ, 16 * t, hf * NSH + s);
+#pragma unroll
+            for (int m = NO - 1; m >= 0; --m) o[t] = Mf<TI, KSH>::run(sf[m], qf, o[t]);
+          }
         }
       }
       if (hf == 0) {
@@ -268,8 +282,11 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
         for (int s = 0; s < NSC; ++s)
 #pragma unroll
           for (int t = 0; t < 2; ++t)
-            if (hf == 0 ? !tri_skip<TRI, KSC>(s, t) : !tri_skip<TRI, KSC>(s, 2 + t))
-              o[t] = Mf<TI, KSC>::run(xf[s], ld_n<TI, KSC, STD, LM>(sM, 32 * hf + 16 * t, s), o[t]);
+            if (hf == 0 ? !tri_skip<TRI, KSC>(s, t) : !tri_skip<TRI, KSC>(s, 2 + t)) {
+#pragma unroll
+              for (int m = NO - 1; m >= 0; --m)
+                o[t] = Mf<TI, KSC>::run(xf[s], ld_n<TI, KSC, STD, LM>(sM[m], 32 * hf + 16 * t, s), o[t]);
+            }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int i = 32 * hf + 16 * t + r;  // (rows past the chunk's end are dropped)
@@ -286,18 +303,15 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
         load_dt(k + 1 + GB + w);
       }
       rk.store(sK);
-      if constexpr (OUT) rq.store(sQ);
-      rx.store(sX2[buf ^ 1]);
+      if constexpr (OUT) {
+        rq.store(sQ);
+        lds_barrier();  // X and M are used up
+      }
+      rx.store(sX);
     }
   }
   if constexpr (OUT) {
-    if (a.st && has && sgm == last) {
-      float* st = a.st + nh * DK * a.Dv + col0 + r;
-#pragma unroll
-      for (int t = 0; t < ND; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st[(int64_t)(d0 + 16 * t + e) * a.Dv] = S[t][e];
-    }
+    if (a.st && has && sgm == last) put(a.st + nh * DK * a.Dv);
   } else {
     const int64_t nj = ((int64_t)n * a.S + sgm) * a.Hv + h;
     f32x4* p = reinterpret_cast<f32x4*>(a.loc) + ((nj * a.nslab + slab) * ND) * NT + threadIdx.x;

@@ -298,6 +298,25 @@ def test_scan_offsets_past_32_bits():
     check(a, up, cu, "f32", out)
 
 
+@pytest.mark.parametrize("Dk,Dv", [(16, 16), (32, 128), (64, 32), (128, 64)])
+@pytest.mark.parametrize("lens", [[130, 70], [1500]])
+def test_scan_rows_carry_no_rounding_but_their_own(Dk, Dv, lens):
+    """Every element of y and dx in bfloat16, where a carried state dominates and terms cancel: half a step of
+    the row's type, and the operands' remainder. The state and the weights between tokens enter as two bfloat16
+    terms, which leave at most 2^-8 of 2^-8 of each; the sums of float32 products and the decays add some 2^-17:
+    together below 2^-15 of the sum of the terms' sizes."""
+    from oracle import layer as L
+
+    a, up, cu = make(lens, 1, 3, Dk, Dv, "bf16", seed=Dk + len(lens), skip=False, a_log=-3.0)
+    out = run(*place(a, up, cu, "bf16"))
+    size = {k: v if k in ("dt", "a_log", "dt_bias") or v is None else np.abs(v) for k, v in a.items()}
+    absup = [np.abs(up["dy"]), np.abs(up["dST"])]
+    for k, want, most in (("y", L.ssm_fwd(cu, *a.values())[0], L.ssm_fwd(cu, *size.values())[0]),
+                          ("dx", L.ssm_bwd(cu, *a.values(), up["dy"], up["dST"])["dx"], L.ssm_bwd(cu, *size.values(), *absup)["dx"])):
+        off = np.abs(host(out[k]).reshape(want.shape) - want) / (2.0 ** -8 * np.abs(want) + 2.0 ** -15 * most + 1e-30)
+        assert off.max() <= 1, (k, float(off.max()))
+
+
 # ------------------------------------------------------------------------------------ single tokens
 
 

@@ -117,7 +117,7 @@ __global__ __launch_bounds__(64) void k_conv_prompt(ConvCarryArgs a) {
         float z = bias[i] + w[K - 1][i] * xt.v[i];
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) z += w[j][i] * win[j].v[i];
-        out.v[i] = z * sigmoidf(z);
+        out.v[i] = z * sigmoidf<TI>(z);
       }
       if (on && t >= lo && t < hi) st8nt<TI>(y + t * a.y_rs, out);  // rows of no sequence stay as they were
 #pragma unroll
@@ -166,7 +166,7 @@ template <typename TI, int K, int R> __global__ __launch_bounds__(64) void k_con
       for (int i = 0; i < 8; ++i) out.v[i] += w[j][i] * s.v[i];
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out.v[i] *= sigmoidf(out.v[i]);
+    for (int i = 0; i < 8; ++i) out.v[i] *= sigmoidf<TI>(out.v[i]);
     TI* st = (TI*)a.state + (int64_t)slot[u] * (K - 1) * a.ch + c0;
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) straw8<TI>(st + (int64_t)j * a.ch, j + 1 < K - 1 ? sr[u][j + 1 < K - 1 ? j + 1 : j] : xr[u]);

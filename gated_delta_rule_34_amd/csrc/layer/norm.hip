@@ -121,7 +121,7 @@ __global__ __launch_bounds__(NT) void k_norm_fwd(NormArgs a, int L) {
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          gt[j].v[i] = zz.v[i] * sigmoidf(zz.v[i]);
+          gt[j].v[i] = zz.v[i] * sigmoidf<TI>(zz.v[i]);
           v[j].v[i] = a.gate_first ? xx.v[i] * gt[j].v[i] : xx.v[i];
         }
       }
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(NT) void k_norm_bwd(NormArgs a, int L, int gpb) {
         const F8 zz = cvt8<TI>(rz[j]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          sg[j].v[i] = sigmoidf(zz.v[i]);
+          sg[j].v[i] = sigmoidf<TI>(zz.v[i]);
           const float gt = zz.v[i] * sg[j].v[i];
           if (a.gate_first) v[j].v[i] *= gt;
           const float dn = a.gate_first ? dy[j].v[i] : dy[j].v[i] * gt;

@@ -179,9 +179,10 @@ __device__ __forceinline__ double lane_value_f64(double x, int lane) {
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// -exp(a_log) in log2 units. Its last float32 bit is common to all decays of a head, as if a_log itself
-// were 1e-7 off, and no product of it with a step is rounded again before the sums of the gates.
-__device__ __forceinline__ double neg_a_log2(float a_log) { return (double)(-decay_rate(a_log) * kLog2e); }
+// -exp(a_log) in log2 units. The float32 exponential's ulp (1e-7 of a_log, as in the elementary operations) is common
+// to all decays of a head; nothing behind it is rounded again before the sums of the gates. (An exponential in
+// 64 bits, be it a short series, costs the gradient kernel some 18 spilled registers more.)
+__device__ __forceinline__ double neg_a_log2(float a_log) { return -(double)decay_rate(a_log) * 1.4426950408889634; }
 
 // 2^x with the part of x that a float32 drops.
 __device__ __forceinline__ float exp2_d(double x) {

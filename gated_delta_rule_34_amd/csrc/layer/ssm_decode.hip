@@ -39,7 +39,7 @@ __global__ __launch_bounds__((SsmDecCfg<DK, DV>::NT)) void k_ssm_decode(SsmDecAr
     sc[d] = (float)cr[d];
   }
   const float z = a.dt[(int64_t)n * a.Hv + h] + (a.dt_bias ? a.dt_bias[h] : 0.f);
-  const float step = softplusf(z), dec = exp2f(-decay_rate(a.a_log[h]) * step * kLog2e);
+  const float step = softplusf(z), dec = expf(-decay_rate(a.a_log[h]) * step);
   const TI* xr = (const TI*)a.x + (int64_t)n * a.x_rs + h * DV + c4;
   const f32x4 x = {(float)xr[0], (float)xr[1], (float)xr[2], (float)xr[3]};
   const f32x4 u = step * x;

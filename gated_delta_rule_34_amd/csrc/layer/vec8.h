@@ -86,14 +86,18 @@ template <typename TI> __device__ __forceinline__ void st8nt(TI* p, const F8& x)
 
 __device__ __forceinline__ F8 zero8() { return F8{{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}}; }
 
-// 1 / (1 + e^-z) with the hardware reciprocal and exponential (about 1 ulp each; 0 where e^-z
-// overflows, NaN for NaN).
-__device__ __forceinline__ float sigmoidf(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
+// 1 / (1 + e^-z); 0 where e^-z overflows, NaN for NaN. For float32 rows the exponential is within an ulp and
+// the quotient rounded once. For bfloat16 rows both are the hardware's: e^-z is then some |z| 2^-24 off
+// (its argument is rounded after the product with log2 e), 2^-17 at the most and far below a row's own 2^-8, and
+// the accurate form would cost the streaming kernels a third (21488 rows x 10240 of the conv: 196 -> 265 us, float32:
+// 9393 rows 189 -> 198).
+template <typename TI> __device__ __forceinline__ float sigmoidf(float z) {
+  if constexpr (sizeof(TI) == 2) return __builtin_amdgcn_rcpf(1.f + __expf(-z));
+  else return 1.f / (1.f + expf(-z));
+}
 
 // The step of the scan: softplus(z), z itself past 20 (where they agree to float32).
 __device__ __forceinline__ float softplusf(float z) { return z > 20.f ? z : log1pf(expf(z)); }
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 // exp(a_log), kept finite: a rate of 2^100 already leaves nothing of a state unless the step is zero, and
 // then the decay is one (an infinite rate times a zero step would be NaN). NaN stays.

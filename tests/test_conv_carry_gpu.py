@@ -169,3 +169,23 @@ def test_offsets_past_32_bits():
     alone = torch.empty(40, 64, dtype=torch.bfloat16, device="cuda")
     G.gdn_conv1d_silu_prompt(G.make_conv_problem(1, 40, 64, 4, T=40), big[-40:, :64].contiguous(), w, None, None, alone, None)
     assert torch.equal(big[-40:, 64:128], alone) and bool((alone != 0).any())
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_silu_keeps_float32_far_from_zero(decode):
+    """One tap of weight 1: y = z sigma(z) of z = x itself, relative to y: the exponential within an ulp (two
+    halves), 1 + e^-z, the quotient and the product round: at most 5 2^-24, and e^-z past float32 gives 0."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    z = np.float32(np.random.default_rng(5).uniform(-87, 87, (64, 64))).astype(np.float64)
+    z[0, :8] = [0, -200, 200, 1e-30, -1e-30, -103, 88.8, -88.8]
+    x, w = dev(z), torch.ones(64, 1, device="cuda")
+    y = torch.empty_like(x)
+    if decode:
+        G.gdn_conv1d_silu_decode(G.make_conv_problem(64, 64, 64, 1, T=1, dtype="f32"), x, w, None, None, None, y)
+    else:
+        G.gdn_conv1d_silu_prompt(G.make_conv_problem(1, 64, 64, 1, T=64, dtype="f32"), x, w, None, None, y, None)
+    want = z / (1 + np.exp(-z))
+    off = np.abs(host(y) - want) / (5 * 2.0 ** -24 * np.abs(want) + 100 * 2.0 ** -126)
+    assert off.max() <= 1, (float(off.max()), z.reshape(-1)[off.argmax()])

@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "layer_internal.h"
 
@@ -37,6 +38,40 @@ gdn_status check_view(const void* ptr, int64_t rs, int64_t width, int dtype, int
 gdn_status check_arr(const void* ptr, bool required, size_t align = 4) {
   if (!ptr) return required ? GDN_EINVAL : GDN_OK;
   return aligned(ptr, align) ? GDN_OK : GDN_EALIGN;
+}
+
+// A row view among a call's arguments.
+struct View {
+  const void* p;
+  int64_t rs;
+};
+
+// For calls whose threads read what they need of the inputs before they write the same places: an output may be
+// an input's very view. At an input's address with another stride, its rows would be rows that other threads
+// still read. Two outputs are never at one address.
+gdn_status check_in_place(int64_t rows, std::initializer_list<View> ins, std::initializer_list<View> outs) {
+  if (rows == 0) return GDN_OK;
+  for (const View* o = outs.begin(); o != outs.end(); ++o) {
+    if (!o->p) continue;
+    for (const View& i : ins)
+      if (o->p == i.p && o->rs != i.rs && rows > 1) return GDN_EINVAL;
+    for (const View* q = outs.begin(); q != o; ++q)
+      if (o->p == q->p) return GDN_EINVAL;
+  }
+  return GDN_OK;
+}
+
+// For calls whose workgroups read what others write: an output is at no input's address, nor at another output's.
+gdn_status check_apart(int64_t rows, std::initializer_list<const void*> ins, std::initializer_list<const void*> outs) {
+  if (rows == 0) return GDN_OK;
+  for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+    if (!*o) continue;
+    for (const void* i : ins)
+      if (*o == i) return GDN_EINVAL;
+    for (const void* const* q = outs.begin(); q != o; ++q)
+      if (*o == *q) return GDN_EINVAL;
+  }
+  return GDN_OK;
 }
 
 gdn_status check_ws(const void* ws, size_t have, size_t need) {
@@ -206,7 +241,7 @@ gdn_status gdn_ssm_fwd(const gdn_ssm_problem* p, const void* x, int64_t x_rs, co
   gdn::SsmArgs a = ssm_args(p);
   GDN_TRY(ssm_inputs(p, x, x_rs, b, b_rs, c, c_rs, dt, a));
   GDN_TRY(ssm_view(y, y_rs, (int64_t)p->Hv * p->Dv, p->dtype, p->T_total));
-  if (p->T_total > 0 && (y == x || y == b || y == c)) return GDN_EINVAL;  // outputs must not overlap inputs
+  GDN_TRY(check_apart(p->T_total, {x, b, c}, {y}));
   GDN_TRY(check_arr(S0, false, 16));
   GDN_TRY(check_arr(S_T, false, 16));
   if (S0 && S0 == S_T) return GDN_EINVAL;
@@ -232,8 +267,11 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_problem* p, const void* x, int64_t x_rs, co
   GDN_TRY(ssm_view(dx, dx_rs, xw, p->dtype, p->T_total));
   GDN_TRY(ssm_view(db, db_rs, kw, p->dtype, p->T_total));
   GDN_TRY(ssm_view(dc, dc_rs, kw, p->dtype, p->T_total));
-  // dx is written before x and dy are read for the last time
-  if (p->T_total > 0 && (dx == x || dx == dy || db == b || dc == c || ddt == dt)) return GDN_EINVAL;
+  // dx is written before x and dy are read for the last time, db and dc while other chunks' groups read theirs
+  GDN_TRY(check_apart(p->T_total, {x, b, c, dy}, {dx}));
+  GDN_TRY(check_apart(p->T_total, {x, b, c, dy}, {db}));
+  GDN_TRY(check_apart(p->T_total, {x, b, c, dy}, {dc}));
+  if (p->T_total > 0 && ddt == dt) return GDN_EINVAL;
   GDN_TRY(check_arr(ddt, p->T_total > 0));
   GDN_TRY(check_arr(da_log, false));
   GDN_TRY(check_arr(ddt_bias, false));
@@ -243,6 +281,7 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_problem* p, const void* x, int64_t x_rs, co
   if (dS_T && dS_T == dS0) return GDN_EINVAL;
   GDN_TRY(check_arr(chunk_states, p->T_total > 0, 16));
   GDN_TRY(check_ws(workspace, workspace_bytes, gdn::ssm_bwd_ws_bytes(a)));
+  GDN_TRY(check_apart(p->T_total, {}, {dx, db, dc}));
   a.dy = dy; a.dy_rs = dy_rs; a.dST = dS_T;
   a.dx = dx; a.dx_rs = dx_rs; a.db = db; a.db_rs = db_rs; a.dc = dc; a.dc_rs = dc_rs;
   a.ddt = ddt; a.da_log = da_log; a.ddt_bias = ddt_bias; a.dd_skip = dd_skip; a.dS0 = dS0;
@@ -261,6 +300,8 @@ gdn_status gdn_ssm_decode(const gdn_ssm_problem* p, const void* x, int64_t x_rs,
   GDN_TRY(check_view(y, y_rs, (int64_t)p->Hv * p->Dv, p->dtype, p->N));
   GDN_TRY(check_arr(state, p->N > 0, 16));
   GDN_TRY(check_slots(p->N, n_slots, slot_idx));
+  GDN_TRY(check_apart(p->N, {b, c}, {y}));  // a row's other heads may still read them
+  GDN_TRY(check_in_place(p->N, {{x, x_rs}}, {{y, y_rs}}));
   gdn::SsmDecArgs a{};
   a.N = p->N; a.Hv = p->Hv; a.r = p->Hv / p->Hk; a.Dk = p->Dk; a.Dv = p->Dv; a.n_slots = n_slots;
   a.x = x; a.b = b; a.c = c; a.x_rs = x_rs; a.b_rs = b_rs; a.c_rs = c_rs; a.y = y; a.y_rs = y_rs;
@@ -276,8 +317,12 @@ gdn_status gdn_conv1d_silu_prompt(const gdn_conv_problem* p, const void* x, int6
   GDN_TRY(conv_views(p, x, x_rs, w, bias, y, y_rs));
   GDN_TRY(check_arr(first, false, 16));
   GDN_TRY(check_arr(last, false, 16));
-  if (first && first == last && p->N > 0 && p->kernel_size > 1) return GDN_EINVAL;  // they must not overlap
-  if (p->T_total > 0 && y == x) return GDN_EINVAL;
+  // runs and sequences' ends are written by workgroups of their own
+  GDN_TRY(check_apart(p->T_total, {x}, {y}));
+  if (p->kernel_size > 1) {
+    GDN_TRY(check_apart(p->N, {first}, {last}));
+    GDN_TRY(check_apart(p->T_total, {x, first}, {y, last}));
+  }
   gdn::ConvCarryArgs a = conv_args(p, x, x_rs, w, bias, y, y_rs);
   a.first = first;
   a.last = last;
@@ -292,6 +337,8 @@ gdn_status gdn_conv1d_silu_decode(const gdn_conv_problem* p, const void* x, int6
   GDN_TRY(conv_views(p, x, x_rs, w, bias, y, y_rs));
   GDN_TRY(check_arr(state, p->N > 0 && p->kernel_size > 1, 16));
   GDN_TRY(check_slots(p->N, n_slots, slot_idx));
+  GDN_TRY(check_in_place(p->N, {{x, x_rs}}, {{y, y_rs}}));
+  if (p->kernel_size > 1) GDN_TRY(check_apart(p->N, {x, y}, {state}));
   gdn::ConvCarryArgs a = conv_args(p, x, x_rs, w, bias, y, y_rs);
   a.state = state;
   a.n_slots = n_slots;
@@ -313,6 +360,7 @@ gdn_status gdn_gated_norm_fwd(const gdn_norm_problem* p, const void* x, int64_t 
   GDN_TRY(norm_view(p, z, z_rs));
   GDN_TRY(norm_view(p, y, y_rs));
   GDN_TRY(check_arr(w, true, 16));
+  GDN_TRY(check_in_place(p->rows, {{x, x_rs}, {z, z_rs}}, {{y, y_rs}}));
   gdn::NormArgs a = norm_args(p);
   a.x = x; a.x_rs = x_rs; a.z = z; a.z_rs = z_rs; a.w = w; a.o = y; a.o_rs = y_rs;
   return status_of(gdn::launch_norm(gdn::GATE_FWD, a, p->dtype, static_cast<hipStream_t>(stream)));
@@ -331,6 +379,7 @@ gdn_status gdn_gated_norm_bwd(const gdn_norm_problem* p, const void* x, int64_t 
   GDN_TRY(check_arr(dw, false));
   gdn::NormArgs a = norm_args(p);
   if (dw) GDN_TRY(check_ws(workspace, workspace_bytes, gdn::norm_ws_bytes(a, false)));
+  GDN_TRY(check_in_place(p->rows, {{x, x_rs}, {z, z_rs}, {dy, dy_rs}}, {{dx, dx_rs}, {dz, dz_rs}}));
   a.x = x; a.x_rs = x_rs; a.z = z; a.z_rs = z_rs; a.w = w; a.g = dy; a.g_rs = dy_rs;
   a.o = dx; a.o_rs = dx_rs; a.o2 = dz; a.o2_rs = dz_rs; a.dw = dw;
   a.ws = static_cast<float*>(workspace);
@@ -347,6 +396,7 @@ gdn_status gdn_add_norm_fwd(const gdn_norm_problem* p, const void* h, int64_t h_
   GDN_TRY(norm_view(p, out, out_rs));
   GDN_TRY(check_arr(s, false, 16));
   GDN_TRY(check_arr(w, true, 16));
+  GDN_TRY(check_in_place(p->rows, {{h, h_rs}, {y, y_rs}}, {{res, res_rs}, {out, out_rs}}));
   gdn::NormArgs a = norm_args(p);
   a.x = h; a.x_rs = h_rs; a.z = y; a.z_rs = y_rs; a.s = s; a.w = w;
   a.o = res; a.o_rs = res_rs; a.o2 = out; a.o2_rs = out_rs;
@@ -370,6 +420,8 @@ gdn_status gdn_add_norm_bwd(const gdn_norm_problem* p, const void* res, int64_t 
   GDN_TRY(check_arr(ds, false));
   gdn::NormArgs a = norm_args(p);
   if (dw || ds) GDN_TRY(check_ws(workspace, workspace_bytes, gdn::norm_ws_bytes(a, true)));
+  GDN_TRY(check_in_place(p->rows, {{res, res_rs}, {ds ? y : nullptr, y_rs}, {dout, dout_rs}, {dres, dres_rs}},
+                         {{dh, dh_rs}, {dy, dy_rs}}));
   a.x = res; a.x_rs = res_rs; a.z = y; a.z_rs = y_rs; a.s = s; a.w = w;
   a.g = dout; a.g_rs = dout_rs; a.g2 = dres; a.g2_rs = dres_rs;
   a.o = dh; a.o_rs = dh_rs; a.o2 = dy; a.o2_rs = dy_rs; a.dw = dw; a.ds = ds;

@@ -58,7 +58,7 @@ size_t gdn_ssm_bwd_workspace_bytes(const gdn_ssm_problem* p);
 size_t gdn_ssm_chunk_state_bytes(const gdn_ssm_problem* p);
 
 /*
- * Forward over prompts. Outputs must not overlap inputs (here and in gdn_ssm_bwd). S0 (float32 [N][Hv][Dk][Dv] or NULL) and S_T (or NULL to skip) 16-byte
+ * Forward over prompts. Outputs must not overlap inputs or one another (here and in gdn_ssm_bwd). S0 (float32 [N][Hv][Dk][Dv] or NULL) and S_T (or NULL to skip) 16-byte
  * aligned; they must not overlap. chunk_states: gdn_ssm_chunk_state_bytes bytes, 16-byte
  * aligned, kept unchanged for gdn_ssm_bwd, or NULL when no backward follows. The workspace may
  * be NULL where its size query returns 0.
@@ -84,7 +84,8 @@ gdn_status gdn_ssm_bwd(const gdn_ssm_problem* p, const void* x, int64_t x_rs, co
  * One step of the scan for each of p->N rows (p->T == 1, p->T_total == p->N, cu_seqlens NULL).
  * state: float32 [n_slots][Hv][Dk][Dv], 16-byte aligned, updated in place; slot_idx: int32 [N] or
  * NULL (row n -> slot n, n_slots >= N). A row whose slot is outside [0, n_slots) is skipped: its
- * y row and every state stay untouched. Two rows of one slot race (their result is undefined).
+ * y row and every state stay untouched. Two rows of one slot race (their result is undefined). y may be
+ * x's very view and must not overlap any other argument.
  */
 gdn_status gdn_ssm_decode(const gdn_ssm_problem* p, const void* x, int64_t x_rs, const void* b, int64_t b_rs,
                           const void* c, int64_t c_rs, const float* dt, float* state, int32_t n_slots,
@@ -95,7 +96,7 @@ gdn_status gdn_ssm_decode(const gdn_ssm_problem* p, const void* x, int64_t x_rs,
  * (float32 [channels] or NULL) and with the K - 1 rows before each sequence in
  * first [N][K - 1][channels] (dtype; oldest row first; NULL = zeros). last [N][K - 1][channels]
  * (NULL to skip) receives the rows that a continuation needs: the last K - 1 rows of first and x
- * together. first and last are 16-byte aligned and must not overlap; y must not overlap x.
+ * together. first and last are 16-byte aligned; y and last must not overlap one another or an input.
  */
 gdn_status gdn_conv1d_silu_prompt(const gdn_conv_problem* p, const void* x, int64_t x_rs, const float* w,
                                   const float* bias, const void* first, void* y, int64_t y_rs, void* last,
@@ -103,7 +104,7 @@ gdn_status gdn_conv1d_silu_prompt(const gdn_conv_problem* p, const void* x, int6
 
 /*
  * The same for one token of each of p->N sequences (p->T == 1, p->T_total == p->N, cu_seqlens
- * NULL; x and y may be the same view): state [n_slots][K - 1][channels] (dtype, 16-byte aligned) holds each slot's last rows,
+ * NULL; y may be x's very view; state overlaps neither): state [n_slots][K - 1][channels] (dtype, 16-byte aligned) holds each slot's last rows,
  * oldest first, and is moved on by one row in place. Slots as in gdn_ssm_decode. For K == 1 there
  * is no window: state may be NULL (rows are skipped by n_slots all the same).
  */
@@ -131,7 +132,8 @@ size_t gdn_gated_norm_bwd_workspace_bytes(const gdn_norm_problem* p);
 size_t gdn_add_norm_bwd_workspace_bytes(const gdn_norm_problem* p);
 
 /* The norm behind a recurrence with its gate: y = norm(x) silu(z), or norm(x silu(z)). An output
- * may be the very view of an input of the same call (here and in the calls below). */
+ * may be the very view of an input of the same call, address and stride, and must not overlap one otherwise,
+ * nor another output (here and in the calls below). */
 gdn_status gdn_gated_norm_fwd(const gdn_norm_problem* p, const void* x, int64_t x_rs, const void* z, int64_t z_rs,
                               const float* w, void* y, int64_t y_rs, void* stream);
 /* dx, dz (dtype) and dw (float32, w's shape; NULL to skip) for dy. */

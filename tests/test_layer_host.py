@@ -166,6 +166,54 @@ def test_norm_refusals(G):
     assert addb(q, ds=None, dw=None, y=(None, 0), dh=(A, 8)) == E
 
 
+def test_outputs_at_the_address_of_other_arguments(G):
+    """An output where another workgroup still reads (or writes) would race: refused. The very view of an input is
+    allowed where one thread reads what it writes, another row stride at its address is not."""
+    E, W = G.GDN_EINVAL, G.GDN_EWORKSPACE
+    p, one = ssm(G), ssm(G, N=2, T=1, T_total=2)
+    a, o = [(k * A, 256) for k in range(1, 5)], [(k * A, 256) for k in range(11, 14)]  # x, b, c, dy; dx, db, dc
+
+    def bwd(outs, ws=1 << 40):
+        x, b, c, dy = a
+        return call(G, "gdn_ssm_bwd", p, *x, *b, *c, 5 * A, 6 * A, *dy, None, *outs[0], *outs[1], *outs[2], 7 * A, None, None, None, None, A, ws, 0)
+
+    def dec(y, x=a[0], b=a[1], c=a[2]):
+        return call(G, "gdn_ssm_decode", one, *x, *b, *c, 5 * A, 6 * A, 2, None, *y, 0)
+
+    assert bwd(o, 16) == W
+    for i in range(3):
+        for taken in a + [o[j] for j in range(3) if j != i]:
+            assert bwd([taken if j == i else o[j] for j in range(3)]) == E, (i, taken)
+    for y in (a[1], a[2], (A, 512)):
+        assert dec(y) == E, y
+    q, tok = conv(G), conv(G, N=2, T=1, T_total=2)
+
+    def prompt(first=21 * A, y=22 * A, last=23 * A):
+        return call(G, "gdn_conv1d_silu_prompt", q, A, 256, 2 * A, None, first, y, 256, last, 0)
+
+    def token(y=(22 * A, 256), state=23 * A):
+        return call(G, "gdn_conv1d_silu_decode", tok, A, 256, 2 * A, None, state, 2, None, *y, 0)
+
+    for kw in (dict(y=21 * A), dict(last=A), dict(last=22 * A)):
+        assert prompt(**kw) == E, kw
+    for kw in (dict(y=(A, 512)), dict(state=A), dict(state=22 * A)):
+        assert token(**kw) == E, kw
+    n, m = norm(G), norm(G, groups=1, width=128)
+    v, far = [(k * A, 128) for k in range(1, 9)], lambda k: (k * A, 256)
+    for k in (1, 2):
+        assert call(G, "gdn_gated_norm_fwd", n, *v[0], *v[1], 31 * A, *far(k), 0) == E
+        for outs in ((far(k), v[6]), (v[5], far(k))):  # res and out
+            assert call(G, "gdn_add_norm_fwd", m, *v[0], *v[1], None, 31 * A, *outs[0], *outs[1], 0) == E
+    for k in (1, 2, 3):
+        for outs in ((far(k), v[6]), (v[5], far(k))):
+            assert call(G, "gdn_gated_norm_bwd", n, *v[0], *v[1], 31 * A, *v[2], *outs[0], *outs[1], None, None, 0, 0) == E
+    for k in (1, 2, 3, 4):
+        for outs in ((far(k), v[6]), (v[5], far(k))):
+            assert call(G, "gdn_add_norm_bwd", m, *v[0], *v[1], None, 31 * A, *v[2], *v[3], *outs[0], *outs[1], 33 * A, 34 * A, A, 1 << 30, 0) == E
+    assert call(G, "gdn_gated_norm_bwd", n, *v[0], *v[1], 31 * A, *v[2], *v[5], *v[5], None, None, 0, 0) == E
+    assert call(G, "gdn_add_norm_fwd", m, *v[0], *v[1], None, 31 * A, *v[5], *v[5], 0) == E
+
+
 def test_binding_refuses_wrong_tensors(G):
     """CPU tensors, and problems whose parameters are no float32 GPU vectors, are refused in the binding."""
     import torch

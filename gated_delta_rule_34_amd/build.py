@@ -1,5 +1,5 @@
-"""Build libgdn.so (HIP kernels for gfx950 + the C ABI) in-tree with hipcc, and the binding's module
-_marshal.so with the host compiler."""
+"""Build libgdn.so (HIP kernels for gfx950 + the C ABI) in-tree with hipcc, and then the binding's
+module _marshal with the host compiler."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -40,19 +40,21 @@ def _compile(src: str) -> str:
 
 
 def _marshal() -> None:
-    """The binding's C module (no GPU code)."""
-    out = os.path.join(PKG, "_marshal.so")
+    """The binding's C module (no GPU code), for the interpreter that runs this: its tag is in the name."""
+    out = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
     cmd = [os.environ.get("CC", "gcc"), "-O2", "-Wall", "-shared", "-fPIC", f"-I{sysconfig.get_paths()['include']}",
            os.path.join(CSRC, "layer", "marshal.c"), "-o", out + ".tmp"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"{cmd[0]} for marshal.c: {e} ({LIB} is built; the operators of gdn.h work without)") from e
     if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed for marshal.c:\n{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed for marshal.c ({LIB} is built; the operators of gdn.h work without):\n{r.stderr}")
     os.replace(out + ".tmp", out)
 
 
 def build(verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
-    _marshal()
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB + ".tmp"
@@ -61,6 +63,7 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _marshal()
     if verbose:
         print(f"built {LIB}")
     return LIB

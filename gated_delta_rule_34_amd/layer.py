@@ -19,8 +19,17 @@ from . import GDN_BF16, GDN_F32, GDN_OK, GdnError, _empty_bytes, _lib, gdn_conv_
 try:
     from . import _marshal
 except ImportError as e:
-    raise ImportError("gated_delta_rule_34_amd/_marshal.so is missing: build the package first "
-                      "(python gated_delta_rule_34_amd/build.py, or __graft_entry__.build())") from e
+    class _Missing:
+        """Stands in for the module, so that the rest of the package loads; a call of this file's raises."""
+
+        def __init__(self, reason):
+            self._reason = reason
+
+        def __getattr__(self, name):
+            raise ImportError(f"the binding's module _marshal cannot be loaded ({self._reason}): build the package first "
+                              "(python gated_delta_rule_34_amd/build.py, or __graft_entry__.build())")
+
+    _marshal = _Missing(str(e))
 
 P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 

@@ -225,3 +225,35 @@ def test_binding_refuses_wrong_tensors(G):
         G.make_ssm_problem(1, 4, 1, 1, 16, 16, a_log=torch.zeros(1))
     with pytest.raises(KeyError):
         G.make_norm_problem(2, 64, dtype="f16")
+
+
+def test_package_loads_without_the_binding_module(G, tmp_path):
+    """Without _marshal the operators of gdn.h are there as before; the layer's calls say what is missing."""
+    import shutil
+    import subprocess
+    import sys
+
+    pkg = tmp_path / "gated_delta_rule_34_amd"
+    pkg.mkdir()
+    for name in ("__init__.py", "layer.py"):
+        shutil.copy(os.path.join(ROOT, "gated_delta_rule_34_amd", name), pkg / name)
+    code = """
+import gated_delta_rule_34_amd as G
+assert G.gdn_strerror(G.GDN_EINVAL) and G.gdn_fwd_workspace_bytes(G.make_problem(1, 64, 1, 1, 16)) > 0
+for call in (lambda: G.gdn_ssm_chunk_state_bytes(G.gdn_ssm_problem()), lambda: G.gdn_add_norm_bwd_workspace_bytes(G.make_norm_problem(1, 8))):
+    try:
+        call()
+    except ImportError as e:
+        assert "_marshal" in str(e) and "build" in str(e), e
+    else:
+        raise AssertionError("no error")
+"""
+    r = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, GDN_LIBRARY=G.LIB_PATH), cwd=tmp_path, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_binding_module_is_this_interpreters(G):
+    """Its name carries the interpreter's tag, so that another one does not load it."""
+    import sysconfig
+
+    assert G.layer._marshal.__file__.endswith("_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))

@@ -321,7 +321,8 @@ def _conv_ins(p, x, w, bias, device, dtype):
 
 def gdn_conv1d_silu_prompt(p, x, w, bias, first, y, last, stream=None):
     """Call gdn_conv1d_silu_prompt: y = SiLU(bias + causal conv1d(x, w)) per sequence, continuing from
-    ``first`` [N, K - 1, channels] (None: zeros); ``last`` (None: skip) gets the rows a continuation needs."""
+    ``first`` [N, K - 1, channels] (None: zeros); ``last`` (None: skip) gets the rows a continuation needs. No
+    backward: gdn_conv1d_silu_bwd is that of the form without bias and first."""
     device, dtype = _begin(p, x, "x")
     win = (p.N, p.kernel_size - 1, p.channels)
     _call("gdn_conv1d_silu_prompt", p, *_conv_ins(p, x, w, bias, device, dtype),

@@ -97,6 +97,8 @@ gdn_status gdn_ssm_decode(const gdn_ssm_problem* p, const void* x, int64_t x_rs,
  * first [N][K - 1][channels] (dtype; oldest row first; NULL = zeros). last [N][K - 1][channels]
  * (NULL to skip) receives the rows that a continuation needs: the last K - 1 rows of first and x
  * together. first and last are 16-byte aligned; y and last must not overlap one another or an input.
+ * There is no backward of this form: gdn_conv1d_silu_bwd is the gradient of sequences that start empty,
+ * without a bias, and SiLU's derivative depends on both.
  */
 gdn_status gdn_conv1d_silu_prompt(const gdn_conv_problem* p, const void* x, int64_t x_rs, const float* w,
                                   const float* bias, const void* first, void* y, int64_t y_rs, void* last,

@@ -1,10 +1,12 @@
-// vec8.h -- eight adjacent values of a row (one 16-byte bf16 piece, two float32 ones) as float32.
+// vec8.h -- eight adjacent values of a row (one 16-byte bf16 piece, two float32 ones) as float32. In a
+// namespace of its own: gdn_conv.hip has types of the same names, with another layout.
 #pragma once
 #include "../gdn_frag.h"
 #include "../gdn_internal.h"
 #include "layer_internal.h"
 
 namespace gdn {
+namespace layer {
 
 struct F8 {
   float v[8];
@@ -106,4 +108,6 @@ __device__ __forceinline__ float decay_rate(float a_log) {
   return a > 0x1p100f ? 0x1p100f : a;
 }
 
+}  // namespace layer
+using namespace layer;
 }  // namespace gdn

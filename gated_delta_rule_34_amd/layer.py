@@ -262,7 +262,7 @@ def _pool(state, slot_idx, N, device, shape, dtype):
             return None, 0x7FFFFFFF, None if slot_idx is None else _array(slot_idx, "slot_idx", (N,), device, _i32)
         raise ValueError("state: missing")
     n_slots = state.shape[0]
-    return (_array(state, "state", (n_slots, *shape), device, dtype), n_slots,
+    return (_array(state, "state", (n_slots, *shape), device, dtype), min(n_slots, 0x7FFFFFFF),  # (int32 in the C ABI)
             None if slot_idx is None else _array(slot_idx, "slot_idx", (N,), device, _i32))
 
 

@@ -257,3 +257,16 @@ def test_binding_module_is_this_interpreters(G):
     import sysconfig
 
     assert G.layer._marshal.__file__.endswith("_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def test_pool_of_more_slots_than_int32(G):
+    """slot_idx reaches 2^31 - 1 slots: a larger pool counts as that many, not as its low 32 bits (here 5)."""
+    import torch
+
+    class Pool:  # what the binding asks of a tensor, of a size that no test allocates
+        dtype, device, shape = torch.bfloat16, "cuda:0", torch.Size(((1 << 32) + 5, 1, 8))
+        get_device, data_ptr, is_contiguous = lambda self: 0, lambda self: A, lambda self: True
+        stride = lambda self: (8, 8, 1)
+
+    G.layer._use_torch()
+    assert G.layer._pool(Pool(), None, 2, 0, (1, 8), torch.bfloat16) == (A, (1 << 31) - 1, None)

@@ -189,3 +189,110 @@ def test_silu_keeps_float32_far_from_zero(decode):
     want = z / (1 + np.exp(-z))
     off = np.abs(host(y) - want) / (5 * 2.0 ** -24 * np.abs(want) + 100 * 2.0 ** -126)
     assert off.max() <= 1, (float(off.max()), z.reshape(-1)[off.argmax()])
+
+
+def plain(a, cu):
+    """y, the sum of the window's |products| and the last rows, for many rows at once: the rows of every window
+    gathered from the sequences' rows and the carried ones behind them."""
+    x, w, K, N = a["x"], a["w"], a["w"].shape[1], len(cu) - 1
+    first = np.zeros((N, K - 1, x.shape[1])) if a["first"] is None else a["first"]
+    rows = np.concatenate([x, first.reshape(N * (K - 1), x.shape[1])])
+    n = np.repeat(np.arange(N), np.diff(cu))
+    at = lambda t, n: np.where(t >= 0, np.asarray(cu)[n] + t, len(x) + n * (K - 1) + (K - 1) + t)  # place t of sequence n
+    t = np.arange(len(x)) - np.asarray(cu)[n]
+    z, size = np.zeros(x.shape), np.zeros(x.shape)
+    for j in range(K):
+        v = rows[at(t - (K - 1) + j, n)] * w[:, j]
+        z, size = z + v, size + np.abs(v)
+    b = 0.0 if a["bias"] is None else a["bias"]
+    seqs = np.arange(N)[:, None]
+    last = rows[at(np.diff(cu)[:, None] - (K - 1) + np.arange(K - 1)[None], seqs)]
+    return (z + b) / (1 + np.exp(-(z + b))), size + np.abs(b), last
+
+
+def test_plain_is_the_oracle():
+    from oracle import layer as L
+
+    lens = [1, 0, 2, 3, 9]
+    a, cu = make(lens, 8, 4, "f32", 1), cu_of(lens)
+    (y, size, last), (yo, lo) = plain(a, cu), L.conv_prompt(cu, *a.values())
+    assert np.allclose(y, yo, rtol=1e-13, atol=0) and np.array_equal(last, lo) and np.allclose(size, size_of(a, cu), rtol=1e-13, atol=0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+@pytest.mark.parametrize("rows,ch", [(8333, 520), (131111, 24)])
+def test_prompt_of_many_rows(dtype, K, rows, ch):
+    """Runs of 16 rows and of 64: sequences of none to three rows, others that start and end inside a run, a last
+    run that is not full, with bias and carried rows; the rows behind the last sequence stay as they were."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    rng = np.random.default_rng(K)
+    lens, left = [1, 0, 2, 3, 1, 64, 65, 0, 127, 16, 17], rows
+    left -= sum(lens)
+    while left:
+        lens.append(min(left, int(rng.choice([0, 1, 3, 15, 33, 100, 700, 2500]))))
+        left -= lens[-1]
+    a, cu = make(lens, ch, K, dtype, K + ch), cu_of(lens)
+    want, size, ends = plain(a, cu)
+    x = torch.full((rows + 5, ch + 8), float("nan"), dtype=torch_dtype(dtype), device="cuda")[:, :ch]
+    x[:rows] = dev(a["x"], dtype)
+    y = torch.full((rows + 5, ch), 7.0, dtype=x.dtype, device="cuda")
+    last = torch.empty(len(lens), K - 1, ch, dtype=x.dtype, device="cuda")
+    t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    p = G.make_conv_problem(len(lens), rows + 5, ch, K, cu_seqlens=t, dtype=dtype)
+    G.gdn_conv1d_silu_prompt(p, x, dev(a["w"]), dev(a["bias"]), dev(a["first"], dtype), y, last)
+    check(host(y[:rows]), want, size, dtype)
+    assert np.array_equal(host(last), ends) and bool((y[rows:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+def test_tokens_of_many_rows(dtype, K):
+    """Four rows to a thread, the last thread's not all there, slots outside the pool at every place among the four."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    N, ch, slots = 1027, 520, 1040
+    a = make([1] * N, ch, K, dtype, 70 + K)
+    rng = np.random.default_rng(3)
+    idx = rng.permutation(slots)[:N]
+    pool = rounded(rng.standard_normal((slots, K - 1, ch)), dtype)
+    a["first"] = pool[idx]
+    want, size, last = plain(a, cu_of([1] * N))
+    use = idx.copy()
+    use[[0, 5, 10, 15, 17, 18, 20, 21, 22, 23, 500, 1026]] = [-1, slots, -7, slots, -1, -1, -1, slots, -1, -1, 2**31 - 1, -2**31]
+    state, x = dev(pool, dtype), dev(a["x"], dtype)
+    p = G.make_conv_problem(N, N, ch, K, T=1, dtype=dtype)
+    G.gdn_conv1d_silu_decode(p, x, dev(a["w"]), dev(a["bias"]), state, torch.from_numpy(use.astype(np.int32)).cuda(), x)  # in place
+    live = use == idx
+    y = host(x)
+    check(y[live], want[live], size[live], dtype)
+    assert np.array_equal(y[~live], a["x"][~live])
+    pool[idx[live]] = last[live]
+    assert np.array_equal(host(state), pool)
+
+
+def test_nan_and_infinities_stay_in_their_windows():
+    """A carried row reaches the first K - 1 rows of its sequence and channel, a row the next K - 1."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    a, cu = make([20, 40, 20], 16, 4, "f32", 4), cu_of([20, 40, 20])
+    x, w, bias, first = dev(a["x"]), dev(a["w"]), dev(a["bias"]), dev(a["first"])
+    p = G.make_conv_problem(3, 80, 16, 4, cu_seqlens=(t := torch.tensor(cu, dtype=torch.int32, device="cuda")), dtype="f32")
+
+    def go():
+        y, last = torch.empty_like(x), torch.empty_like(first)
+        G.gdn_conv1d_silu_prompt(p, x, w, bias, first, y, last)
+        return y, last
+
+    y, last = go()
+    first[1, 2, 3], first[2, 0, 5], x[59, 7], x[30, 9] = float("nan"), float("inf"), float("-inf"), float("nan")
+    y2, last2 = go()
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[20:23, 3], hit[60, 5], hit[59, 7], hit[30:34, 9] = True, True, True, True
+    assert torch.equal(y2[~hit], y[~hit]) and bool(y2[20:23, 3].isnan().all()) and bool(y2[30:34, 9].isnan().all()) and t is not None
+    assert last2[1, 2, 7] == float("-inf") and torch.equal(last2[[0, 2]], last[[0, 2]])
+

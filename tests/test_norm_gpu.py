@@ -208,3 +208,51 @@ def test_norm_graph_replays():
         torch.cuda.synchronize()
         assert all(torch.equal(out[k], eager[k]) for k in eager), rep
         step()
+
+
+@pytest.mark.parametrize("rows,groups,W", [(2101, 48, 128), (5001, 3, 512), (1201, 1, 2568)])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("dtype,gate_first", [("bf16", False), ("f32", True)])
+def test_gated_norm_several_rows_to_a_workgroup(rows, groups, W, shared, dtype, gate_first):
+    """More passes than row splits: the weights' gradients add up over a workgroup's rows, and some workgroups
+    have one row more than others."""
+    gate_check(*gate_case(rows, groups, W, shared, dtype, rows + W), shared, gate_first, dtype)
+
+
+@pytest.mark.parametrize("rows,W", [(9001, 520), (1201, 2568), (140001, 24)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_add_norm_several_rows_to_a_workgroup(rows, W, dtype):
+    add_check(rows, W, dtype, True, True, rows)
+
+
+def test_norms_nan_and_infinities_stay_in_their_groups():
+    """A NaN or an infinity in a group reaches that group's values and the column sums, nothing else."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    for width, groups in ((64, 3), (2056, 2)):
+        x, z, w, dy = (dev(a.reshape(a.shape[0], -1), t) for a, t in zip(gate_case(9, groups, width, False, "bf16", 6), ("bf16", "bf16", "f32", "bf16")))
+        w = w.view(-1)
+        p = G.make_norm_problem(9, width, groups=groups)
+        run = lambda: dict(y=G.gated_norm_forward(p, x, z, w), **G.gated_norm_backward(p, x, z, w, dy))
+        clean = run()
+        x[1, 0], x[4, width], z[6, 2], dy[7, width + 1] = float("nan"), float("inf"), float("nan"), float("-inf")
+        out = run()
+        hit = torch.zeros(9, groups, dtype=torch.bool, device="cuda")
+        hit[1, 0], hit[4, 1], hit[6, 0], hit[7, 1] = True, True, True, True
+        for k in ("y", "dx", "dz"):
+            a, b = (v[k].view(9, groups, width)[~hit] for v in (out, clean))
+            assert torch.equal(a, b), k
+        assert bool(out["y"].view(9, groups, width)[1, 0].isnan().all())
+        q = G.make_norm_problem(9, width * groups)
+        h, y = clean["y"].clone(), clean["dx"]
+        wide = torch.ones(width * groups, device="cuda")
+        res, o = G.add_norm_forward(q, h, y, wide, wide)
+        g = G.add_norm_backward(q, res, y, wide, wide, dy.nan_to_num(0, 0, 0), None)
+        h[3, 5] = float("inf")
+        res2, o2 = G.add_norm_forward(q, h, y, wide, wide)
+        g2 = G.add_norm_backward(q, res2, y, wide, wide, dy.nan_to_num(0, 0, 0), None)
+        rest = [0, 1, 2, 4, 5, 6, 7, 8]
+        for a, b in ((res, res2), (o, o2), (g["dh"], g2["dh"]), (g["dy"], g2["dy"])):
+            assert torch.equal(a[rest], b[rest])
+

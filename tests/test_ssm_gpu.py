@@ -317,6 +317,24 @@ def test_scan_rows_carry_no_rounding_but_their_own(Dk, Dv, lens):
         assert off.max() <= 1, (k, float(off.max()))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 64)])
+def test_scan_gradients_of_many_heads_in_one_workgroup(dtype, Dk, Dv):
+    """Two groups of nine heads over more chunks than half the compute units: a workgroup's heads come in a second
+    batch (float32: in five), with one and two slabs of a head."""
+    lens = [70, 0, 1, 2] + [1, 0, 2] * 21
+    a, up, cu = make(lens, 2, 18, Dk, Dv, dtype, seed=Dk)
+    check(a, up, cu, dtype, run(*place(a, up, cu, dtype)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,T,Hk,r", [(9, 70, 4, 5), (5, 700, 2, 2)])
+def test_scan_groups_dealt_to_one_xcd(dtype, N, T, Hk, r):
+    """Groups whose heads go to one XCD, their number no multiple of eight; sequences whole, and in segments."""
+    a, up, cu = make([T] * N, Hk, Hk * r, 16, 16, dtype, seed=T)
+    check(a, up, cu, dtype, run(*place(a, up, cu, dtype, varlen=False, lens=[T])))
+
+
 # ------------------------------------------------------------------------------------ single tokens
 
 
@@ -385,3 +403,17 @@ def test_decode_slots_past_32_bits():
     G.gdn_ssm_decode(p, d["x"], d["b"], d["c"], d["dt"], pool, idx, y)
     G.gdn_ssm_decode(p, d["x"], d["b"], d["c"], d["dt"], small, None, want)
     assert torch.equal(y, want) and torch.equal(pool[idx.long()], small)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_in_place_of_x(dtype):
+    """y as the very view of x, inside a packed row beside b and c."""
+    import torch
+    import gated_delta_rule_34_amd as G
+
+    a, up, cu = make([1] * 5, 2, 6, 64, 128, dtype, seed=33)
+    p, d = place(a, up, cu, dtype, varlen=False, lens=[1])
+    state, y = d["S0"].clone(), torch.empty(5, 6 * 128, dtype=torch_dtype(dtype), device="cuda")
+    G.gdn_ssm_decode(p, d["x"], d["b"], d["c"], d["dt"], state, None, y)
+    G.gdn_ssm_decode(p, d["x"], d["b"], d["c"], d["dt"], d["S0"], None, d["x"])
+    assert torch.equal(d["x"], y) and torch.equal(d["S0"], state)

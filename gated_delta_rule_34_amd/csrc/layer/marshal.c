@@ -37,6 +37,7 @@ static PyObject *m_rows(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   if (n != 5) return PyErr_Format(PyExc_TypeError, "rows takes 5 arguments");
   PyObject *t = a[0], *shape = NULL, *st = NULL, *out = NULL;
   const long long rows = PyLong_AsLongLong(a[1]), width = PyLong_AsLongLong(a[2]);
+  if (PyErr_Occurred()) return NULL;
   const int ok = placed(t, a[3], a[4]);
   if (ok < 0) return NULL;
   if (!ok) Py_RETURN_NONE;
@@ -54,9 +55,9 @@ static PyObject *m_rows(PyObject *self, PyObject *const *a, Py_ssize_t n) {
       flat = (item(st, 2) == 1 || d == 1) && (heads == 1 || item(st, 1) == d);
     }
     if (!PyErr_Occurred() && inner == width && item(shape, 0) == rows && (flat || rows == 0)) {
-      const long long p = ask(t, s_data_ptr);
       /* (without a second row there is no stride to speak of) */
-      if (!PyErr_Occurred()) out = Py_BuildValue("(LL)", p, rows > 1 ? item(st, 0) : width);
+      const long long rs = rows > 1 ? item(st, 0) : width, p = PyErr_Occurred() ? -1 : ask(t, s_data_ptr);
+      if (!PyErr_Occurred()) out = Py_BuildValue("(LL)", p, rs);
       goto end;
     }
   }

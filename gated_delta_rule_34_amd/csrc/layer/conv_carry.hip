@@ -6,8 +6,10 @@
 // with ext the K - 1 carried rows followed by the sequence's rows. What a continuation needs is
 // the last K - 1 rows of ext, copied as they are. Pure streaming: each row is read and written
 // once (2 ch values per row), bound by HBM; the window lives in registers. Measured (bf16, K = 4):
-// 21488 rows x 10240 in 8 sequences 197 us, 4.5 TB/s (a large copy reaches 5.2); one token of 256
-// sequences 17.4 us with nothing in the caches, 11 us per call in a loop.
+// 21488 rows x 10240 in 8 sequences 195 us, 4.5 TB/s (a large copy reaches 5.2); one token of 256
+// sequences 17.2 us with nothing in the caches, 11 us per call in a loop; float32: 9393 rows x 10240 198 us, 3.9 TB/s.
+// A wave covers 512 channels whatever their number: channels that are no multiple of 512 leave lanes of the last
+// wave idle (of 16 channels, all but two).
 #include "vec8.h"
 
 namespace gdn {

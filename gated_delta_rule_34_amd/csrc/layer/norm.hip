@@ -11,8 +11,10 @@
 // Streaming work: every row element is read and written once, bound by HBM. A group is held in
 // registers by NL lanes (eight adjacent values per lane and vector, V vectors): the 64 / L groups
 // side by side in one wave up to 2048 values, a whole workgroup beyond. All arithmetic is
-// float32; results are rounded once. Measured (bf16, 16384 rows): gated norm of 48 x 128 forward 121 us
-// (5.0 TB/s), backward 204 + 6 us (4.9); add norm of 5120 forward 130 us (5.2), backward 206 + 9 us (4.9).
+// float32; results are rounded once. Measured (bf16, 16384 rows): gated norm of 48 x 128 forward 126 us
+// (4.8 TB/s), backward 215 + 6 us (4.7); add norm of 5120 forward 130 us (5.2), backward 203 + 9 us (5.0). float32, 8192
+// rows: gated norm 118 and 224 + 6 us, add norm 140 and 236 + 9 us. Lanes to a group are a power of two with 1, 2
+// or 4 vectors each, so that widths between waste some (520 values, 65 vectors, take 64 lanes twice).
 #include "vec8.h"
 
 namespace gdn {

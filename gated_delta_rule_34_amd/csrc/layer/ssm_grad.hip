@@ -17,7 +17,7 @@
 // accuracy, and Gamma D Q over two, so that db and dc carry no rounding but their own.
 //
 // Bound by HBM: the two states of a chunk and head are 8 Dk Dv bytes. Measured (bf16, 4 x 4096 tokens, 64 heads
-// of 128 x 64 in 8 groups): 426 to 440 us for the 1.5 GB of states and rows, which a copy would take 290 us
+// of 128 x 64 in 8 groups): 422 to 457 us for the 1.5 GB of states and rows, which a copy would take 290 us
 // to move; the rest is the start of each workgroup (one to a compute unit), which nothing overlaps.
 //
 // Eight waves: wave w holds 16 rows of Dk (all tokens; with a smaller state some tokens) and one or two

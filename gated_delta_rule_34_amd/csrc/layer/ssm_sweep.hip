@@ -105,8 +105,8 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
   rx.init(a.x_rs, ncols);
   const uint32_t orow = (uint32_t)a.o_rs * (uint32_t)sizeof(TI);
   // Gates come GB chunks at a time, one for each of GB waves: a chunk's are a long chain of dependent
-  // operations that by one wave in every chunk took a fifth of the step (every second chunk 255 us for 4 x 4096
-  // tokens and 64 heads, every third 245). A ring of GB + 1 holds them: the chunk in work keeps its own.
+  // operations that by one wave in every chunk took a fifth of the step (every third chunk takes 4% less than
+  // every second one: 4 x 4096 tokens, 64 heads). A ring of GB + 1 holds them: the chunk in work keeps its own.
   float rdt = 0.f;  // dt of this wave's chunk of the next ones
   auto load = [&](int k) {
     const int c = chunk(k), len = clen(c);
@@ -323,11 +323,13 @@ __global__ __launch_bounds__(512, (sweep_waves<TI, DK>())) void k_ssm_sweep(Swee
 
 // Segments per sequence: two workgroups to a compute unit, at most one for every kMinChunks chunks of the
 // longest sequence there can be. A segment costs its states and a second read of its rows, so two gain
-// nothing (4 x 4096 tokens, 64 heads: one segment 243 us, two 247), more do (16384 tokens, 32 heads: 8 of
-// them 180 us, 16 of them 150; 300 tokens, 8 heads: one 21, three 18). A packed batch's lengths are not
-// known here: its short sequences leave their further segments empty (lengths up to 777, 6 heads of 32 x 32,
-// float32, training step: three segments 104 us, seven 72; 16 x 512 tokens, 4 heads: 27 and 24 us; 3000, 1000
-// and 200 tokens, 32 heads: 67 and 73).
+// nothing (4 x 4096 tokens, 64 heads: one segment 263 us, two 261), more do (16384 tokens, 32 heads: 8 of
+// them 187 us, 16 of them 151, 32 of them 202; 300 tokens, 8 heads: one 23, three 20). A packed batch's lengths
+// are not known here: its short sequences leave their further segments empty (lengths up to 777, 6 heads of
+// 32 x 32, float32, training step: three segments 98 us, seven 68; 16 x 512 tokens, 4 heads: one 35 us, four 26; 3000, 1000
+// and 200 tokens, 32 heads: one 169, three 94, five 77). A float32 workgroup with a state of 128 rows has its compute unit
+// to itself, so that the rule cuts such sequences finer than is best: 2048 tokens, 32 heads of 128 x 64 in 16 segments 77 us,
+// in 8 of them 70 (training step 294 and 278).
 constexpr int kWantGroups = 512, kMaxSegments = 32;
 static int ssm_segments(const SsmArgs& a) {
   if (a.N == 0) return 1;
@@ -367,7 +369,7 @@ template <typename TI, int DK, bool REV> static hipError_t sweep_go(const SsmArg
   // A group's heads share b and c: with many groups they go to one XCD (workgroups are dealt to
   // the eight XCDs in turn) and share its L2; few groups would leave XCDs idle. A packed batch's segments
   // are dealt one by one: a long sequence's would else meet on a few compute units (1500, 20, 300, 44, 5
-  // and 700 tokens, 24 heads: 47 us, so 37). Later segments come last, the empty ones behind the others.
+  // and 700 tokens, 24 heads: 50 us, so 39). Later segments come last, the empty ones behind the others.
   auto grid = [&](int segs) {
     const int G = a.N * segs * a.Hk, m = a.r * v.nslab;
     v.xcd = G >= 32 && !(v.S > 1 && a.cu && a.N > 1);

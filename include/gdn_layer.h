@@ -34,8 +34,8 @@ extern "C" {
  *
  * starting from S0 (zero when NULL). x, y: [rows][Hv*Dv]; b, c: [rows][Hk*Dk]; dt: float32
  * [T_total][Hv]; a row stride is below 2^25 bytes. Sums and states are float32; products of bfloat16 inputs run on the matrix
- * cores with every float32 factor split over several bfloat16 operands where the result is
- * float32.
+ * cores with every float32 factor split over bfloat16 operands, three where the result is float32 (24 bits), two
+ * where it is a bfloat16 row, which so carries no rounding but its own.
  */
 typedef struct {
   int32_t N;        /* sequences (>= 0) */
@@ -72,7 +72,8 @@ gdn_status gdn_ssm_fwd(const gdn_ssm_problem* p, const void* x, int64_t x_rs, co
  * zeros). The inputs and chunk_states must be those of the forward call. Writes dx [rows][Hv*Dv],
  * db, dc [rows][Hk*Dk] (dtype; a group's heads summed in float32, rounded once), ddt float32
  * [T_total][Hv], da_log, ddt_bias, dd_skip float32 [Hv] (each NULL to skip) and dS0 (or NULL to
- * skip; it must not overlap dS_T). Sums over tokens run in float32 in a fixed order.
+ * skip; it must not overlap dS_T). Sums over tokens run in a fixed order: in float32 inside a chunk, of the
+ * chunks' partials (da_log, ddt_bias, dd_skip) in 64 bits.
  */
 gdn_status gdn_ssm_bwd(const gdn_ssm_problem* p, const void* x, int64_t x_rs, const void* b, int64_t b_rs,
                        const void* c, int64_t c_rs, const float* dt, const void* chunk_states,

@@ -11,7 +11,9 @@ states and the workspace with torch and call ``gdn_fwd`` / ``gdn_bwd``.
 
 The operators around the recurrence (``include/gdn_layer.h``: the selective state space scan,
 the conv1d with a carried window, the gated norm and the residual addition with its norm) are
-bound in ``layer`` and are names of this package too.
+bound in ``layer``, the other token mixers of a hybrid model (``include/gdn_hybrid.h``: the gated
+linear recurrence, the norm of queries and keys with the rotation of positions, attention over a paged
+cache) in ``hybrid``; both are names of this package too.
 """
 from __future__ import annotations
 
@@ -323,3 +325,8 @@ from .layer import (  # noqa: E402,F401  (the operators of gdn_layer.h)
     gdn_gated_norm_bwd, gdn_gated_norm_bwd_workspace_bytes, gdn_gated_norm_fwd, gdn_norm_problem, gdn_ssm_bwd,
     gdn_ssm_bwd_workspace_bytes, gdn_ssm_chunk_state_bytes, gdn_ssm_decode, gdn_ssm_fwd, gdn_ssm_fwd_workspace_bytes,
     gdn_ssm_problem, make_norm_problem, make_ssm_problem, ssm_backward, ssm_forward)
+from .hybrid import (  # noqa: E402,F401  (the operators of gdn_hybrid.h)
+    HYBRID_EXPORTED, gdn_glr_bwd, gdn_glr_bwd_workspace_bytes, gdn_glr_decode, gdn_glr_fwd, gdn_glr_fwd_workspace_bytes,
+    gdn_glr_problem, gdn_glr_state_bytes, gdn_paged_attn_decode, gdn_paged_attn_workspace_bytes, gdn_paged_problem,
+    gdn_qk_rope_bwd, gdn_qk_rope_bwd_workspace_bytes, gdn_qk_rope_cache, gdn_qk_rope_fwd, gdn_qk_rope_problem, glr_backward,
+    glr_forward, make_glr_problem, make_paged_problem, make_qk_rope_problem, paged_attention, qk_rope_backward, qk_rope_forward)

@@ -17,7 +17,8 @@ LIB = os.path.join(PKG, "libgdn.so")
 
 SOURCES = ["gdn_fwd.hip", "gdn_bwd.hip", "gdn_decode.hip", "gdn_conv.hip", "gdn_scratch.hip", "gdn_abi.cpp",
            "gdn_trace.cpp", "layer/conv_carry.hip", "layer/norm.hip", "layer/ssm_decode.hip", "layer/ssm_sweep.hip",
-           "layer/ssm_grad.hip", "layer/layer_abi.cpp"]
+           "layer/ssm_grad.hip", "layer/layer_abi.cpp", "hybrid/glr.hip", "hybrid/qk_rope.hip", "hybrid/paged_attn.hip",
+           "hybrid/hybrid_abi.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 # Packed-FP32 instructions are disabled for every device pass.

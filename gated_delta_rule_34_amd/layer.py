@@ -67,7 +67,7 @@ SIGNATURES = {
 }
 LAYER_EXPORTED = tuple(SIGNATURES)
 
-
+_signatures = dict(SIGNATURES)  # those of gdn_hybrid.h join them
 _bound = {}
 
 
@@ -75,7 +75,7 @@ def _fn(name):
     fn = _bound.get(name)
     if fn is None:
         fn = getattr(_lib, name)
-        fn.argtypes, fn.restype = SIGNATURES[name]
+        fn.argtypes, fn.restype = _signatures[name]
         _bound[name] = fn
     return fn
 

@@ -325,8 +325,24 @@ from .layer import (  # noqa: E402,F401  (the operators of gdn_layer.h)
     gdn_gated_norm_bwd, gdn_gated_norm_bwd_workspace_bytes, gdn_gated_norm_fwd, gdn_norm_problem, gdn_ssm_bwd,
     gdn_ssm_bwd_workspace_bytes, gdn_ssm_chunk_state_bytes, gdn_ssm_decode, gdn_ssm_fwd, gdn_ssm_fwd_workspace_bytes,
     gdn_ssm_problem, make_norm_problem, make_ssm_problem, ssm_backward, ssm_forward)
-from .hybrid import (  # noqa: E402,F401  (the operators of gdn_hybrid.h)
-    HYBRID_EXPORTED, gdn_glr_bwd, gdn_glr_bwd_workspace_bytes, gdn_glr_decode, gdn_glr_fwd, gdn_glr_fwd_workspace_bytes,
-    gdn_glr_problem, gdn_glr_state_bytes, gdn_paged_attn_decode, gdn_paged_attn_workspace_bytes, gdn_paged_problem,
-    gdn_qk_rope_bwd, gdn_qk_rope_bwd_workspace_bytes, gdn_qk_rope_cache, gdn_qk_rope_fwd, gdn_qk_rope_problem, glr_backward,
-    glr_forward, make_glr_problem, make_paged_problem, make_qk_rope_problem, paged_attention, qk_rope_backward, qk_rope_forward)
+
+# The operators of gdn_hybrid.h: the module is imported at the first use of one of its names.
+_HYBRID = (
+    "HYBRID_EXPORTED", "gdn_glr_bwd", "gdn_glr_bwd_workspace_bytes", "gdn_glr_decode", "gdn_glr_fwd", "gdn_glr_fwd_workspace_bytes",
+    "gdn_glr_problem", "gdn_glr_state_bytes", "gdn_paged_attn_decode", "gdn_paged_attn_workspace_bytes", "gdn_paged_problem",
+    "gdn_qk_rope_bwd", "gdn_qk_rope_bwd_workspace_bytes", "gdn_qk_rope_cache", "gdn_qk_rope_fwd", "gdn_qk_rope_problem", "glr_backward",
+    "glr_forward", "make_glr_problem", "make_paged_problem", "make_qk_rope_problem", "paged_attention", "qk_rope_backward", "qk_rope_forward")
+
+
+def __getattr__(name):
+    if name != "hybrid" and name not in _HYBRID:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+
+    hybrid = importlib.import_module(".hybrid", __name__)
+    globals().update((n, getattr(hybrid, n)) for n in _HYBRID)
+    return hybrid if name == "hybrid" else globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_HYBRID})

@@ -97,20 +97,6 @@ gdn_status check_pool(int64_t n_pages, int64_t page_size, int64_t Hk) {
   return GDN_OK;
 }
 
-gdn_status check_paged(const gdn_paged_problem* p) {
-  if (!p || p->N < 0 || p->Hq <= 0 || p->Hk <= 0 || p->Hq % p->Hk) return GDN_EINVAL;
-  if (!known_dtype(p->dtype) || (p->D != 32 && p->D != 64 && p->D != 128 && p->D != 256)) return GDN_EUNSUPPORTED;
-  GDN_TRY(check_pool(p->n_pages, p->page_size, p->Hk));
-  if (p->max_pages < 0 || p->max_pages > INT32_MAX / p->page_size) return GDN_EINVAL;
-  if (p->max_len < 0 || p->max_len > p->max_pages * p->page_size || p->window < 0 || !std::isfinite(p->scale)) return GDN_EINVAL;
-  if (p->max_len > INT32_MAX - (1 << 20)) return GDN_EINVAL;  // tokens past a chunk's end are counted too
-  // a workgroup per head and sequence, or chunk of at least 256 tokens
-  const int64_t rows = (int64_t)p->N * p->Hq;
-  if (rows > kMaxBlocks || rows * (p->max_len / 256 + 1) > kMaxBlocks) return GDN_EINVAL;
-  GDN_TRY(check_arr(p->page_table, p->N > 0 && p->max_len > 0));
-  return check_arr(p->lens, p->N > 0);
-}
-
 gdn::PagedArgs paged_args(const gdn_paged_problem* p) {
   gdn::PagedArgs a{};
   a.N = p->N;
@@ -126,6 +112,19 @@ gdn::PagedArgs paged_args(const gdn_paged_problem* p) {
   a.table = p->page_table;
   a.lens = p->lens;
   return a;
+}
+
+gdn_status check_paged(const gdn_paged_problem* p) {
+  if (!p || p->N < 0 || p->Hq <= 0 || p->Hk <= 0 || p->Hq % p->Hk) return GDN_EINVAL;
+  if (!known_dtype(p->dtype) || (p->D != 32 && p->D != 64 && p->D != 128 && p->D != 256)) return GDN_EUNSUPPORTED;
+  GDN_TRY(check_pool(p->n_pages, p->page_size, p->Hk));
+  if (p->max_pages < 0 || p->max_pages > INT32_MAX / p->page_size) return GDN_EINVAL;
+  if (p->max_len < 0 || p->max_len > p->max_pages * p->page_size || p->window < 0 || !std::isfinite(p->scale)) return GDN_EINVAL;
+  if (p->max_len > INT32_MAX - (1 << 20)) return GDN_EINVAL;  // tokens past a chunk's end are counted too
+  // launch limits: a workgroup per query head and sequence, and per chunk of a key head
+  if ((int64_t)p->N * p->Hq > kMaxBlocks || gdn::paged_blocks(paged_args(p), p->dtype) > kMaxBlocks) return GDN_EINVAL;
+  GDN_TRY(check_arr(p->page_table, p->N > 0 && p->max_len > 0));
+  return check_arr(p->lens, p->N > 0);
 }
 
 }  // namespace

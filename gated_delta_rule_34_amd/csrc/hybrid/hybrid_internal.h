@@ -68,6 +68,7 @@ struct PagedArgs {
   float* lse;
   float* ws;
 };
+int64_t paged_blocks(const PagedArgs& a, int dtype);  // workgroups of a launch
 size_t paged_ws_bytes(const PagedArgs& a, int dtype);
 hipError_t launch_paged(const PagedArgs& a, int dtype, hipStream_t s);
 

@@ -22,38 +22,101 @@ constexpr int PW = 4;        // waves per workgroup
 constexpr int PT = 16;       // tokens per tile
 constexpr float kNone = -__builtin_inff();
 
+// How a launch cuts its sequences into chunks, each a workgroup per key head and 16 query heads.
+//   even: chunks of one length, found on the device from the lengths as they are, so that there are at most `slots`
+//     of them (up to kPagedEven sequences); chunk c takes slot c of the workspace;
+//   else: `chunk` tokens each, `splits` of them to every sequence, in use or not; slot n splits + split.
+constexpr int kPagedEven = 256;
+struct PagedPlan {
+  int gt, splits, slots, chunk;
+  bool even;
+};
+
 // What a sequence's length and window leave: tokens [lo, len), chunks from `base` on.
 struct PagedSpan {
-  int lo, len, base, chunks;
+  int lo, len, base;
 };
-__device__ __forceinline__ PagedSpan paged_span(const PagedArgs& a, int n, int chunk) {
+__device__ __forceinline__ PagedSpan paged_span(const PagedArgs& a, int n) {
   PagedSpan s;
-  int len = a.lens[n];
+  const int len = a.lens[n];
   s.len = len < 0 ? 0 : len > a.max_len ? a.max_len : len;
   s.lo = a.window > 0 && s.len > a.window ? s.len - a.window : 0;
   s.base = s.lo & ~(PT - 1);
-  s.chunks = (s.len - s.base + chunk - 1) / chunk;
   return s;
+}
+
+// Chunk `id` of a launch (ROWS = false), or the first chunk of sequence `id`: every sequence has one at least.
+struct PagedChunk {
+  int n, split, chunks, chunk, slot;
+};
+template <bool ROWS> __device__ __forceinline__ PagedChunk paged_chunk(const PagedArgs& a, const PagedPlan& p, int id) {
+  PagedChunk c;
+  if (!p.even) {
+    c.n = ROWS ? id : id / p.splits;
+    // turned from row to row, so that the launch's order (and with it an XCD) does not go with a chunk's number
+    c.split = ROWS ? 0 : (id + c.n) % p.splits;
+    c.chunk = p.chunk;
+    const PagedSpan s = paged_span(a, c.n);
+    c.chunks = s.len - s.base <= c.chunk ? 1 : (s.len - s.base + c.chunk - 1) / c.chunk;
+    c.slot = c.n * p.splits + c.split;
+    return c;
+  }
+  constexpr int U = kPagedEven / 64;  // lane l holds the sequences U l .. U l + U - 1
+  int w[U];
+  int64_t total = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int n = lane_id() * U + u;
+    w[u] = 0;
+    if (n < a.N) {
+      const PagedSpan s = paged_span(a, n);
+      w[u] = s.len - s.base;
+    }
+    total += w[u];
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+  // at most total / chunk + N chunks
+  const int64_t want = (total + p.slots - a.N - 1) / (p.slots - a.N);
+  c.chunk = want <= p.chunk ? p.chunk : (int)((want + PT * PW - 1) / (PT * PW)) * (PT * PW);
+  int cnt[U], sum = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    cnt[u] = lane_id() * U + u >= a.N ? 0 : w[u] <= c.chunk ? 1 : (w[u] + c.chunk - 1) / c.chunk;
+    sum += cnt[u];
+  }
+  int at = wave_scan_incl_int(sum) - sum, n = -1, split = 0, chunks = 0, slot = 0;  // chunks in front of this lane's
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const bool here = ROWS ? lane_id() * U + u == id : id >= at && id < at + cnt[u];
+    if (here) {
+      n = lane_id() * U + u;
+      split = ROWS ? 0 : id - at;
+      chunks = cnt[u];
+      slot = ROWS ? at : id;
+    }
+    at += cnt[u];
+  }
+  const uint64_t who = __ballot(n >= 0);
+  c.n = -1;
+  if (who == 0) return c;
+  const int l = __builtin_ctzll(who);
+  c.n = __builtin_amdgcn_readlane(n, l);
+  c.split = __builtin_amdgcn_readlane(split, l);
+  c.chunks = __builtin_amdgcn_readlane(chunks, l);
+  c.slot = __builtin_amdgcn_readlane(slot, l);
+  return c;
 }
 
 // A lane's pieces of one key (KP of 16 bytes) and of one value row (VP pieces of PE values: D / 16 of them).
 template <typename TI, int D> struct PagedTile {
   static constexpr int KP = D / (64 / (int)sizeof(TI));
   static constexpr int VE = D / 16, PE = VE < 16 / (int)sizeof(TI) ? VE : 16 / (int)sizeof(TI), VP = VE / PE;
-  static constexpr int W = PE * (int)sizeof(TI) / 4;  // dwords of a piece of V
-  typedef int32_t vpiece __attribute__((ext_vector_type(W)));
-  i32x4 k[KP];
-  vpiece v[4][VP];
-  bool full;      // every token counts (wave-uniform)
-  uint32_t mask;  // else: bit i: token 4g + i counts
+  typedef int32_t vpiece __attribute__((ext_vector_type(PE * (int)sizeof(TI) / 4)));
 };
 template <> struct PagedTile<__bf16, 32> {
-  static constexpr int KP = 1, VE = 2, PE = 2, VP = 1, W = 1;
+  static constexpr int KP = 1, VE = 2, PE = 2, VP = 1;
   typedef int32_t vpiece;
-  i32x4 k[1];
-  int32_t v[4][1];
-  bool full;
-  uint32_t mask;
 };
 
 // Value e of a piece as float32.
@@ -65,23 +128,26 @@ template <typename TI, typename P> __device__ __forceinline__ float piece_at(con
   return __uint_as_float(w);
 }
 
-template <typename TI, int D, bool UNI, bool PART>
-__global__ __launch_bounds__(64 * PW) void k_paged(PagedArgs a, int chunk, int splits, int gt) {
+// Workgroups per compute unit of k_paged, whose registers grow with a head's bytes.
+constexpr int paged_resident(int head_bytes) { return head_bytes <= 256 ? 4 : head_bytes <= 512 ? 2 : 1; }
+
+template <typename TI, int D, bool UNI>
+__global__ __launch_bounds__(64 * PW, paged_resident(D * (int)sizeof(TI))) void k_paged(PagedArgs a, PagedPlan plan) {
   typedef PagedTile<TI, D> Tile;
   constexpr int KP = Tile::KP, VE = Tile::VE, PE = Tile::PE, VP = Tile::VP;
   __shared__ __align__(16) float so[PW][8][D];
   __shared__ float sm[PW][16], sl[PW][16];
+  // heads run fastest: those of a page lie together
   int bx = (int)blockIdx.x;
-  const int split = bx % splits;
-  bx /= splits;
-  const int ht = bx % gt;
-  bx /= gt;
-  const int hk = bx % a.Hk, n = bx / a.Hk;
-  const int r = a.Hq / a.Hk, h0 = hk * r + ht * 16, nh = r - ht * 16 < 16 ? r - ht * 16 : 16;
-  const PagedSpan sp = paged_span(a, n, chunk);
-  if (PART && split >= sp.chunks) return;
+  const int hk = bx % a.Hk;
+  bx /= a.Hk;
+  const int ht = bx % plan.gt;
+  const PagedChunk ch = paged_chunk<false>(a, plan, bx / plan.gt);
+  if (ch.n < 0 || ch.split >= ch.chunks) return;
+  const int n = ch.n, r = a.Hq / a.Hk, h0 = hk * r + ht * 16, nh = r - ht * 16 < 16 ? r - ht * 16 : 16;
+  const PagedSpan sp = paged_span(a, n);
   const int w = wave_id(), g = lane_id() >> 4, j = lane_id() & 15;
-  const int t0 = sp.base + split * chunk, t1 = t0 + chunk < sp.len ? t0 + chunk : sp.len;
+  const int t0 = sp.base + ch.split * ch.chunk, t1 = sp.len - t0 < ch.chunk ? sp.len : t0 + ch.chunk;
   const TI *kp = (const TI*)a.kp, *vp = (const TI*)a.vp;
   const int* table = a.table + (int64_t)n * a.max_pages;
 
@@ -97,86 +163,75 @@ __global__ __launch_bounds__(64 * PW) void k_paged(PagedArgs a, int chunk, int s
   for (int e = 0; e < VE; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = kNone, l = 0.f;  // of head j; l: this lane's tokens only
 
-  // Row of token t among the pool's rows of this key head, or none.
-  auto row_of = [&](int t, bool& ok) -> uint32_t {
-    const uint32_t pg = (uint32_t)t / (uint32_t)a.page;
-    ok = t >= sp.lo && t < t1;
-    const int page = ok ? table[pg] : -1;
-    ok = page >= 0 && page < a.n_pages;
-    return ((uint32_t)page * (uint32_t)a.Hk + (uint32_t)hk) * (uint32_t)a.page + ((uint32_t)t - pg * (uint32_t)a.page);
+  // Where a tile's tokens are. UNI: a tile lies in one page, and `row` is that of its first token; else `row` is that of
+  // token t + j. mask: bit i: token 4g + i counts; full: every token does (wave-uniform). Every load is issued, that of a token
+  // which does not count at a place inside the pool: a load that a branch may skip would make each wait one for all loads.
+  struct Place {
+    uint32_t row, mask;
+    bool full;
   };
-  auto load_k = [&](Tile& x, const TI* p) {
-#pragma unroll
-    for (int c = 0; c < KP; ++c) x.k[c] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p + (c * 64 + g * 16) / (int)sizeof(TI)));
+  auto entry = [&](int t) -> int {  // of the page table
+    int u = UNI ? t : t + j;
+    u = u < sp.lo ? sp.lo : u < t1 ? u : t1 - 1;
+    if constexpr (UNI) return __builtin_amdgcn_readfirstlane(table[(uint32_t)u / (uint32_t)a.page]);
+    else return table[(uint32_t)u / (uint32_t)a.page];
   };
-  auto load_v = [&](Tile& x, int i, const TI* p) {
-#pragma unroll
-    for (int c = 0; c < VP; ++c)
-      x.v[i][c] = __builtin_nontemporal_load(reinterpret_cast<const typename Tile::vpiece*>(p + c * 16 * PE + j * PE));
-  };
-  auto load = [&](Tile& x, int t) {
-    if constexpr (UNI) {  // a tile lies in one page
-      const uint32_t pg = (uint32_t)t / (uint32_t)a.page;
-      const int page = __builtin_amdgcn_readfirstlane(table[pg]);
-      const bool ok = page >= 0 && page < a.n_pages;
-      x.full = ok && t >= sp.lo && t + PT <= t1;
-      const int64_t row = ((int64_t)page * a.Hk + hk) * a.page + ((uint32_t)t - pg * (uint32_t)a.page);
-      if (x.full) {
-        load_k(x, kp + (row + j) * D);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) load_v(x, i, vp + (row + 4 * g + i) * D);
-        return;
-      }
+  auto place = [&](int t, int page) -> Place {
+    Place x;
+    const bool in = page >= 0 && page < a.n_pages;
+    const uint32_t base = ((uint32_t)(in ? page : 0) * (uint32_t)a.Hk + (uint32_t)hk) * (uint32_t)a.page;
+    if constexpr (UNI) {
+      x.row = base + (uint32_t)t % (uint32_t)a.page;
+      x.full = in && t >= sp.lo && t + PT <= t1;
       x.mask = 0;
 #pragma unroll
-      for (int c = 0; c < KP; ++c) x.k[c] = i32x4{0, 0, 0, 0};
-      if (ok && t + j >= sp.lo && t + j < t1) load_k(x, kp + (row + j) * D);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int c = 0; c < VP; ++c) x.v[i][c] = typename Tile::vpiece{};
-        if (ok && t + 4 * g + i >= sp.lo && t + 4 * g + i < t1) {
-          x.mask |= 1u << i;
-          load_v(x, i, vp + (row + 4 * g + i) * D);
-        }
-      }
+      for (int i = 0; i < 4; ++i) x.mask |= in && t + 4 * g + i >= sp.lo && t + 4 * g + i < t1 ? 1u << i : 0u;
     } else {
-      bool ok;
-      const uint32_t row = row_of(t + j, ok);
-      const uint64_t all = __ballot(ok);
+      x.row = base + (uint32_t)(t + j) % (uint32_t)a.page;
+      const uint64_t all = __ballot(in && t + j >= sp.lo && t + j < t1);
       x.full = all == ~0ull;
       x.mask = (uint32_t)(all >> (4 * g)) & 15;  // (lanes 0 .. 15 hold the tile's tokens)
+    }
+    return x;
+  };
+  i32x4 k[KP];
+  typename Tile::vpiece v[4][VP];
+  auto load_k = [&](const Place& x) {
+    const TI* p = kp + (int64_t)(UNI ? x.row + j : x.row) * D;
 #pragma unroll
-      for (int c = 0; c < KP; ++c) x.k[c] = i32x4{0, 0, 0, 0};
-      if (ok) load_k(x, kp + (int64_t)row * D);
+    for (int c = 0; c < KP; ++c) k[c] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p + (c * 64 + g * 16) / (int)sizeof(TI)));
+  };
+  auto load_v = [&](const Place& x) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t vrow = (uint32_t)__builtin_amdgcn_ds_bpermute((4 * g + i) << 2, (int)row);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t row;
+      if constexpr (UNI) row = x.row + 4 * g + i;
+      else row = (uint32_t)__builtin_amdgcn_ds_bpermute((4 * g + i) << 2, (int)x.row);
+      const TI* p = vp + (int64_t)row * D;
 #pragma unroll
-        for (int c = 0; c < VP; ++c) x.v[i][c] = typename Tile::vpiece{};
-        if (x.mask >> i & 1) load_v(x, i, vp + (int64_t)vrow * D);
-      }
+      for (int c = 0; c < VP; ++c)
+        v[i][c] = __builtin_nontemporal_load(reinterpret_cast<const typename Tile::vpiece*>(p + c * 16 * PE + j * PE));
     }
   };
-  auto use = [&](const Tile& x) {
+  auto score = [&]() {
     f32x4 s{0.f, 0.f, 0.f, 0.f};
     if constexpr (sizeof(TI) == 2) {
 #pragma unroll
       for (int c = 0; c < KP; ++c)
-        s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x.k[c]), __builtin_bit_cast(bf16x8, q[c]), s, 0, 0, 0);
+        s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[c]), __builtin_bit_cast(bf16x8, q[c]), s, 0, 0, 0);
     } else {
 #pragma unroll
       for (int c = 0; c < KP; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          s = __builtin_amdgcn_mfma_f32_16x16x4f32(__int_as_float(x.k[c][e]), __int_as_float(q[c][e]), s, 0, 0, 0);
+          s = __builtin_amdgcn_mfma_f32_16x16x4f32(__int_as_float(k[c][e]), __int_as_float(q[c][e]), s, 0, 0, 0);
     }
+    return s;
+  };
+  auto add = [&](const f32x4& s, const Place& x) {
     float z[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      z[i] = s[i] * sc;
-      if (!x.full && !(x.mask >> i & 1)) z[i] = kNone;
-    }
+    for (int i = 0; i < 4; ++i) z[i] = x.full || x.mask >> i & 1 ? s[i] * sc : kNone;
     const float top = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
     if (__any(top > m + 8.f)) {  // (the first score exceeds any)
       float mx = fmaxf(top, m);
@@ -199,25 +254,40 @@ __global__ __launch_bounds__(64 * PW) void k_paged(PagedArgs a, int chunk, int s
       p[i] = __builtin_amdgcn_exp2f(z[i] - ref);
       l += p[i];
     }
+    if (!x.full)  // what lies in a place that does not count may be anything, NaN too
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < VP; ++c) v[i][c] = x.mask >> i & 1 ? v[i][c] : typename Tile::vpiece{};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < VE; ++e)
-        o[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], piece_at<TI>(x.v[i][e / PE], e % PE), o[e], 0, 0, 0);
+        o[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i], piece_at<TI>(v[i][e / PE], e % PE), o[e], 0, 0, 0);
   };
 
-  Tile A, B;
   constexpr int STEP = PT * PW;
   int t = t0 + w * PT;
-  if (t < t1) load(A, t);
-  while (t < t1) {
-    if (t + STEP < t1) load(B, t + STEP);
-    use(A);
-    t += STEP;
-    if (t >= t1) break;
-    if (t + STEP < t1) load(A, t + STEP);
-    use(B);
-    t += STEP;
+  if (t < t1 && a.n_pages > 0) {
+    int e1 = entry(t + STEP);
+    Place at = place(t, entry(t));
+    load_k(at);
+    load_v(at);
+    for (; t + STEP < t1; t += STEP) {
+      const f32x4 s = score();
+      __builtin_amdgcn_sched_barrier(0);  // (loads moved up would need registers of their own, and spill)
+      // the keys are used up: the next tile's take their registers while this one's weights and values are worked on
+      const Place next = place(t + STEP, e1);
+      e1 = entry(t + 2 * STEP);
+      load_k(next);
+      __builtin_amdgcn_sched_barrier(0);
+      add(s, at);
+      __builtin_amdgcn_sched_barrier(0);
+      load_v(next);
+      __builtin_amdgcn_sched_barrier(0);
+      at = next;
+    }
+    add(score(), at);
   }
 
   // the waves' parts, eight heads at a time
@@ -247,16 +317,16 @@ __global__ __launch_bounds__(64 * PW) void k_paged(PagedArgs a, int chunk, int s
       float sum = 0.f, val = 0.f;
 #pragma unroll
       for (int u = 0; u < PW; ++u) {
-        const float f = sm[u][h] == kNone ? (sl[u][h] == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(sm[u][h] - mx);
+        const float f = sm[u][h] == kNone ? 1.f : __builtin_amdgcn_exp2f(sm[u][h] - mx);  // (of none: no sum, or a NaN)
         sum += f * sl[u][h];
         val += f * so[u][hh][d];
       }
       const int64_t head = (int64_t)n * a.Hq + h0 + h;
-      if constexpr (PART) {
-        const int64_t at = head * splits + split;
+      if (ch.chunks > 1) {
+        const int64_t at = (int64_t)ch.slot * a.Hq + h0 + h;
         a.ws[at * D + d] = val;
         if (d == 0) {
-          float* ml = a.ws + (int64_t)a.N * a.Hq * splits * D + at * 2;
+          float* ml = a.ws + (int64_t)plan.slots * a.Hq * D + at * 2;
           ml[0] = mx;
           ml[1] = sum;
         }
@@ -268,83 +338,108 @@ __global__ __launch_bounds__(64 * PW) void k_paged(PagedArgs a, int chunk, int s
   }
 }
 
-// Joins a head's chunks: one workgroup per (sequence, query head).
-template <typename TI, int D> __global__ __launch_bounds__(256) void k_paged_join(PagedArgs a, int chunk, int splits) {
-  constexpr int CG = D / 4, RG = 256 / CG;  // threads to a row of O, rows side by side
-  __shared__ float red[8];
-  __shared__ __align__(16) float acc[RG][D];
-  const int n = (int)blockIdx.x / a.Hq;
-  const PagedSpan sp = paged_span(a, n, chunk);
-  const int64_t head = blockIdx.x;
-  const float* O = a.ws + head * splits * D;
-  const float* ml = a.ws + (int64_t)a.N * a.Hq * splits * D + head * splits * 2;
-  float mx = kNone;
-  for (int s = (int)threadIdx.x; s < sp.chunks; s += 256) mx = fmaxf(mx, ml[s * 2]);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-  if (lane_id() == 0) red[wave_id()] = mx;
-  __syncthreads();
-  mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const int cg = (int)threadIdx.x % CG, rg = (int)threadIdx.x / CG;
+// Joins the chunks of HB heads of a sequence, 64 columns of each (JC): SG groups of threads take every SG-th chunk, with a
+// running maximum of their own.
+template <typename TI, int D, int SG> __global__ __launch_bounds__(256) void k_paged_join(PagedArgs a, PagedPlan plan) {
+  constexpr int JC = D < 64 ? D : 64, CG = JC / 4, HB = 256 / CG / SG;
+  __shared__ float sm[SG][HB], sl[SG][HB];
+  __shared__ __align__(16) float acc[SG][HB][JC];
+  const int hblocks = (a.Hq + HB - 1) / HB, n = (int)blockIdx.x / hblocks, c0 = (int)blockIdx.y * JC;
+  const PagedChunk ch = paged_chunk<true>(a, plan, n);
+  if (ch.chunks == 1) return;
+  const int cg = (int)threadIdx.x % CG, unit = (int)threadIdx.x / CG, sg = unit % SG, hb = unit / SG;
+  const int h = ((int)blockIdx.x - n * hblocks) * HB + hb;
+  float m = kNone, l = 0.f;
   f32x4 val{0.f, 0.f, 0.f, 0.f};
-  float sum = 0.f;
-  for (int s = rg; s < sp.chunks; s += RG) {
-    const float ms = ml[s * 2], ls = ml[s * 2 + 1];
-    const float f = ms == kNone ? (ls == 0.f ? 0.f : 1.f) : __builtin_amdgcn_exp2f(ms - mx);
-    sum += f * ls;
-    val += f * *reinterpret_cast<const f32x4*>(O + (int64_t)s * D + cg * 4);
-  }
-  *reinterpret_cast<f32x4*>(&acc[rg][cg * 4]) = val;
-  __shared__ float sums[RG];
-  if (cg == 0) sums[rg] = sum;
-  __syncthreads();
-  if ((int)threadIdx.x < D) {
-    float v = 0.f, t = 0.f;
-#pragma unroll
-    for (int i = 0; i < RG; ++i) {
-      v += acc[i][threadIdx.x];
-      t += sums[i];
+  if (h < a.Hq) {
+    const float* O = a.ws + ((int64_t)ch.slot * a.Hq + h) * D + c0 + cg * 4;
+    const float* ml = a.ws + (int64_t)plan.slots * a.Hq * D + ((int64_t)ch.slot * a.Hq + h) * 2;
+#pragma unroll 4
+    for (int s = sg; s < ch.chunks; s += SG) {
+      const float ms = ml[(int64_t)s * a.Hq * 2], ls = ml[(int64_t)s * a.Hq * 2 + 1];
+      const f32x4 os = *reinterpret_cast<const f32x4*>(O + (int64_t)s * a.Hq * D);
+      const float mx = fmaxf(m, ms), f = m == kNone ? 0.f : __builtin_amdgcn_exp2f(m - mx);
+      // (a chunk of which nothing is left has no sum, or a NaN)
+      const float fs = ms == kNone ? 1.f : __builtin_amdgcn_exp2f(ms - mx);
+      m = mx;
+      l = l * f + fs * ls;
+      val = val * f + fs * os;
     }
-    ((TI*)a.out)[(int64_t)n * a.out_rs + (head - (int64_t)n * a.Hq) * D + threadIdx.x] = (TI)(t == 0.f ? 0.f : v / t);
-    if (threadIdx.x == 0 && a.lse) a.lse[head] = t == 0.f ? kNone : (mx + log2f(t)) * 0.69314718f;
+  }
+  *reinterpret_cast<f32x4*>(&acc[sg][hb][cg * 4]) = val;
+  if (cg == 0) {
+    sm[sg][hb] = m;
+    sl[sg][hb] = l;
+  }
+  __syncthreads();
+  for (int x = (int)threadIdx.x; x < HB * JC; x += 256) {
+    const int hh = x / JC, c = x % JC, head = ((int)blockIdx.x - n * hblocks) * HB + hh;
+    if (head >= a.Hq) continue;
+    float mx = sm[0][hh], v = 0.f, t = 0.f;
+#pragma unroll
+    for (int i = 1; i < SG; ++i) mx = fmaxf(mx, sm[i][hh]);
+#pragma unroll
+    for (int i = 0; i < SG; ++i) {
+      const float f = sm[i][hh] == kNone ? 1.f : __builtin_amdgcn_exp2f(sm[i][hh] - mx);
+      t += f * sl[i][hh];
+      v += f * acc[i][hh][c];
+    }
+    ((TI*)a.out)[(int64_t)n * a.out_rs + (int64_t)head * D + c0 + c] = (TI)(t == 0.f ? 0.f : v / t);
+    if (c0 + c == 0 && a.lse) a.lse[(int64_t)n * a.Hq + head] = t == 0.f ? kNone : (mx + log2f(t)) * 0.69314718f;
   }
 }
 
 // ------------------------------------------------------------------ launches
-// Tokens per chunk: as many workgroups as fill the chip several times over, none with less than 256 tokens.
-struct PagedPlan {
-  int chunk, splits, gt;
-};
-static PagedPlan paged_plan(const PagedArgs& a) {
+// Chunks: as many as the chip holds workgroups at once, so that equal ones end together (one sequence of 131072 tokens, 4 heads
+// of 256: 93 us with 512 of them, 99 with 1024, 114 with 2048), and four more for every sequence, whose last chunks are
+// of unequal lengths (64 sequences of up to 8192 tokens, 8 heads of 128: 217 us with 1024, 195 with 2048, 190 with
+// 4096). None of less than 128 tokens, two tiles for each wave.
+static PagedPlan paged_plan(const PagedArgs& a, int dtype) {
   PagedPlan p;
-  const int r = a.Hq / a.Hk;
-  p.gt = (r + 15) / 16;
-  const int64_t span = (a.window > 0 && a.window < a.max_len ? a.window + PT - 1 : a.max_len);
-  const int64_t rows = (int64_t)a.N * a.Hk * p.gt;
-  int64_t want = rows ? (1024 + rows - 1) / rows : 1;
-  int64_t chunk = (span + want - 1) / want;
-  if (chunk < 256) chunk = 256;
-  chunk = (chunk + PT * PW - 1) / (PT * PW) * (PT * PW);
-  p.chunk = (int)(chunk < (1 << 30) ? chunk : 1 << 30);
-  p.splits = (int)((span + p.chunk - 1) / p.chunk);
-  if (p.splits < 1) p.splits = 1;
+  p.gt = (a.Hq / a.Hk + 15) / 16;
+  const int64_t span = a.window > 0 && a.window < a.max_len ? (int64_t)a.window + PT - 1 : a.max_len;
+  const int64_t heads = (int64_t)a.Hk * p.gt, full = 256 * paged_resident(a.D * (dtype == 0 ? 4 : 2));
+  const int64_t want = (full + heads - 1) / heads + 4 * (int64_t)a.N;
+  constexpr int least = 128;
+  p.even = a.N <= kPagedEven && span > least;
+  if (p.even) {
+    const int64_t most = a.N * ((span + least - 1) / least);
+    p.chunk = least;
+    p.splits = 0;
+    p.slots = (int)(want < most ? want : most) + a.N;
+  } else {
+    const int64_t each = (want + a.N - 1) / (a.N > 0 ? a.N : 1);
+    int64_t chunk = (span + each - 1) / each;
+    chunk = chunk < least ? least : (chunk + PT * PW - 1) / (PT * PW) * (PT * PW);
+    p.chunk = (int)(chunk < (1 << 30) ? chunk : 1 << 30);
+    p.splits = span > 0 ? (int)((span + p.chunk - 1) / p.chunk) : 1;
+    p.slots = a.N * p.splits;
+  }
   return p;
 }
-size_t paged_ws_bytes(const PagedArgs& a, int) {
-  const PagedPlan p = paged_plan(a);
-  return p.splits == 1 ? 0 : (size_t)a.N * a.Hq * p.splits * (a.D + 2) * sizeof(float);
+int64_t paged_blocks(const PagedArgs& a, int dtype) {
+  const PagedPlan p = paged_plan(a, dtype);
+  return (int64_t)p.slots * a.Hk * p.gt;
+}
+size_t paged_ws_bytes(const PagedArgs& a, int dtype) {
+  const PagedPlan p = paged_plan(a, dtype);
+  return p.splits == 1 ? 0 : (size_t)p.slots * a.Hq * (a.D + 2) * sizeof(float);
 }
 
 template <typename TI, int D, bool UNI> static hipError_t paged_go(const PagedArgs& a, hipStream_t s) {
-  const PagedPlan p = paged_plan(a);
-  const unsigned grid = (unsigned)((int64_t)a.N * a.Hk * p.gt * p.splits);
-  traced("k_paged", s, [&] {
-    if (p.splits == 1) k_paged<TI, D, UNI, false><<<grid, 64 * PW, 0, s>>>(a, p.chunk, 1, p.gt);
-    else k_paged<TI, D, UNI, true><<<grid, 64 * PW, 0, s>>>(a, p.chunk, p.splits, p.gt);
-  });
+  constexpr int dtype = sizeof(TI) == 2;
+  const PagedPlan p = paged_plan(a, dtype);
+  const unsigned grid = (unsigned)paged_blocks(a, dtype);
+  traced("k_paged", s, [&] { k_paged<TI, D, UNI><<<grid, 64 * PW, 0, s>>>(a, p); });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  traced("k_paged_join", s, [&] { k_paged_join<TI, D><<<(unsigned)((int64_t)a.N * a.Hq), 256, 0, s>>>(a, p.chunk, p.splits); });
+  // few sequences may have many chunks each, many have few
+  constexpr int units = D < 64 ? 32 : 16;
+  const unsigned cols = D < 64 ? 1 : D / 64;
+  traced("k_paged_join", s, [&] {
+    if ((int64_t)a.N * a.Hq * cols <= 512) k_paged_join<TI, D, units><<<dim3((unsigned)(a.N * a.Hq), cols), 256, 0, s>>>(a, p);
+    else k_paged_join<TI, D, 2><<<dim3((unsigned)(a.N * ((a.Hq + units / 2 - 1) / (units / 2))), cols), 256, 0, s>>>(a, p);
+  });
   return hipGetLastError();
 }
 template <typename TI, int D> static hipError_t paged_uni(const PagedArgs& a, hipStream_t s) {

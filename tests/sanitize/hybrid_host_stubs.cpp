@@ -13,6 +13,7 @@ hipError_t launch_glr_backward(const GlrArgs&, int, hipStream_t) { return hipSuc
 hipError_t launch_glr_decode(const GlrArgs&, int, hipStream_t) { return hipSuccess; }
 size_t rope_bwd_ws_bytes(const RopeArgs&) { return 4096; }
 hipError_t launch_rope(RopeKind, const RopeArgs&, int, hipStream_t) { return hipSuccess; }
+int64_t paged_blocks(const PagedArgs& a, int) { return (int64_t)a.N * a.Hk * (a.max_len / 128 + 1); }
 size_t paged_ws_bytes(const PagedArgs&, int) { return 4096; }
 hipError_t launch_paged(const PagedArgs&, int, hipStream_t) { return hipSuccess; }
 }  // namespace gdn

@@ -144,7 +144,7 @@ def test_attention_refusals(G):
                      (dict(page_size=0), E), (dict(n_pages=-1), E), (dict(n_pages=1 << 30, page_size=4), E), (dict(max_pages=-1), E),
                      (dict(max_len=81), E), (dict(max_len=-1), E), (dict(window=-1), E), (dict(scale=float("nan")), E), (dict(page_table=None), E),
                      (dict(lens=None), E), (dict(page_table=A + 2), L), (dict(lens=A + 1), L), (dict(N=1 << 24), E),
-                     (dict(Hk=8, n_pages=1 << 29, page_size=2), E), (dict(N=1 << 15, max_pages=1 << 20, max_len=1 << 24), E),
+                     (dict(Hk=8, n_pages=1 << 29, page_size=2), E), (dict(N=1 << 21), E),
                      (dict(N=1, max_pages=2**27 - 1, max_len=2**31 - 16), E)):
         p = paged(G, **kw)
         assert run(p) == want, kw

@@ -19,6 +19,7 @@
 // leaves compute units idle, sequences are cut into segments, whose maps an extra pass over the inputs
 // finds first.
 #include "../gdn_common.h"
+#include "../layer/rows.h"
 #include "../layer/vec8.h"
 #include "hybrid_internal.h"
 
@@ -32,9 +33,20 @@ constexpr int GE = GNT / 32;       // groups of four thread rows
 
 // V adjacent values of a row (16 bytes).
 template <typename TI> constexpr int glr_v() { return 16 / (int)sizeof(TI); }
-template <typename TI> __device__ __forceinline__ i32x4 glr_ld(const void* p, int64_t at) {
-  return __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(static_cast<const TI*>(p) + at));
-}
+// A thread's piece of the rows of a tensor, from row `row` of a tile on (kNowhere: of no row).
+template <typename TI> struct GlrView {
+  const TI* p;
+  int64_t rs;
+  uint32_t rsb, voff;
+  __device__ __forceinline__ GlrView(const void* base, int64_t stride, bool on, int row, int c)
+      : p(static_cast<const TI*>(base)), rs(stride), rsb((uint32_t)stride * (uint32_t)sizeof(TI)) {
+    voff = on ? (uint32_t)row * rsb + (uint32_t)c * (uint32_t)sizeof(TI) : kNowhere;
+  }
+  // The `rows` rows from t on (a tile's at the most).
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(int64_t t, int rows) const { return rows_rsrc(p + t * rs, (uint32_t)rows * rsb); }
+  template <bool NT> __device__ __forceinline__ i32x4 load(__amdgpu_buffer_rsrc_t r, int k) const { return buf_ld16<NT>(r, voff + (uint32_t)k * rsb); }
+  __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, int k, i32x4 v) const { buf_st16<true>(r, voff + (uint32_t)k * rsb, v); }
+};
 template <typename TI, int V> __device__ __forceinline__ void glr_cvt(i32x4 r, float (&v)[V]) {
   if constexpr (sizeof(TI) == 2) {
     const bf16x8 b = __builtin_bit_cast(bf16x8, r);
@@ -46,17 +58,15 @@ template <typename TI, int V> __device__ __forceinline__ void glr_cvt(i32x4 r, f
     for (int j = 0; j < V; ++j) v[j] = b[j];
   }
 }
-template <typename TI, int V> __device__ __forceinline__ void glr_st(void* p, int64_t at, const float (&v)[V]) {
-  i32x4 r;
+template <typename TI, int V> __device__ __forceinline__ i32x4 glr_raw(const float (&v)[V]) {
   if constexpr (sizeof(TI) == 2) {
     bf16x8 b;
 #pragma unroll
     for (int j = 0; j < V; ++j) b[j] = (__bf16)v[j];
-    r = __builtin_bit_cast(i32x4, b);
+    return __builtin_bit_cast(i32x4, b);
   } else {
-    r = __builtin_bit_cast(i32x4, f32x4{v[0], v[1], v[2], v[3]});
+    return __builtin_bit_cast(i32x4, f32x4{v[0], v[1], v[2], v[3]});
   }
-  store_nt(reinterpret_cast<i32x4*>(static_cast<TI*>(p) + at), r);
 }
 
 // rate softplus(lambda), kept finite (an infinite exponent times a state would be NaN where a is zero).
@@ -70,31 +80,34 @@ template <typename TI> __device__ __forceinline__ float glr_exp(float L) {
   if constexpr (sizeof(TI) == 2) return __builtin_amdgcn_exp2f(L * -1.44269504f);
   else return expf(-L);
 }
-// 1 - exp(-L): its series up to L^6 below a quarter (the next term is 5e-8 of it).
-template <typename TI> __device__ __forceinline__ float one_minus_exp(float L) {
-  float p = fmaf(L, -1.f / 720.f, 1.f / 120.f);
-  p = fmaf(L, p, -1.f / 24.f) * L;
-  p = fmaf(L, p + 1.f / 6.f, -0.5f);
-  p = fmaf(L * L, p, L);
-  return L < 0.25f ? p : 1.f - glr_exp<TI>(L);
+// 1 - exp(-L): its series up to L^6 below a quarter (the next term is 5e-8 of it). `deep` (wave-uniform): some L may
+// be more; where no channel's rate is, the exponentials are left out.
+template <typename TI, int V> __device__ __forceinline__ void one_minus_exp(const float (&L)[V], bool deep, float (&e)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float p = fmaf(L[j], -1.f / 720.f, 1.f / 120.f);
+    p = fmaf(L[j], p, -1.f / 24.f);
+    p = fmaf(L[j], p, 1.f / 6.f);
+    p = fmaf(L[j], p, -0.5f) * L[j];
+    e[j] = fmaf(L[j], p, L[j]);
+  }
+  if (deep) {
+    asm volatile("");  // (a branch, not eight exponentials for nothing)
+#pragma unroll
+    for (int j = 0; j < V; ++j) e[j] = L[j] < 0.25f ? e[j] : 1.f - glr_exp<TI>(L[j]);
+  }
 }
 
-// w = sqrt(1 - a^2) of e = 1 - a, and 1 / w, which ends at 2^63 (L / w is then zero where L is): a w below
-// 2^-63, whose square no float32 holds in full, may come out as less.
-struct GlrWeight {
-  float w, rw;
-};
-template <typename TI> __device__ __forceinline__ GlrWeight glr_weight(float e) {
-  const float w2 = e * (2.f - e);
-  GlrWeight g;
-  if constexpr (sizeof(TI) == 2) {
-    g.rw = __builtin_amdgcn_rsqf(fmaxf(w2, 0x1p-126f));
-    g.w = w2 * g.rw;
-  } else {
-    g.w = sqrtf(w2);
-    g.rw = 1.f / fmaxf(g.w, 0x1p-63f);
-  }
-  return g;
+// w = sqrt(1 - a^2) of e = 1 - a. A w below 2^-63, whose square no float32 holds in full, may come out as less.
+template <typename TI> __device__ __forceinline__ float glr_weight(float e) {
+  if constexpr (sizeof(TI) == 2) return __builtin_amdgcn_sqrtf(e * (2.f - e));
+  else return sqrtf(e * (2.f - e));
+}
+// 1 / w, which ends at 2^63 (L / w is then zero where L is).
+template <typename TI> __device__ __forceinline__ float glr_inv_weight(float e) {
+  const float w2 = fmaxf(e * (2.f - e), 0x1p-126f);
+  if constexpr (sizeof(TI) == 2) return __builtin_amdgcn_rsqf(w2);
+  else return 1.f / sqrtf(w2);
 }
 
 // (E, B) <- first (E1, B1), then (E, B).
@@ -103,9 +116,9 @@ __device__ __forceinline__ void glr_after(float E1, float B1, float& E, float& B
   E = fmaf(-E1, E, E1) + E;
 }
 
-// x of the lane that CTRL names, `none` where it lies outside the row of 16.
-template <int CTRL> __device__ __forceinline__ float dpp_or(float none, float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+// x of the lane that CTRL names, zero where it lies outside the row of 16 (e = 0, b = 0: the map that changes nothing).
+template <int CTRL> __device__ __forceinline__ float dpp_or0(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
 }
 // The four thread rows of a DPP row: (E, B) composed with those in front of it (FWD, row_shr) or behind it
 // (row_shl), and (Ex, Bx) that of the others alone.
@@ -113,10 +126,10 @@ template <bool FWD, int V> __device__ __forceinline__ void glr_scan4(float (&E)[
   constexpr int S4 = FWD ? 0x114 : 0x104, S8 = FWD ? 0x118 : 0x108;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    glr_after(dpp_or<S4>(0.f, E[j]), dpp_or<S4>(0.f, B[j]), E[j], B[j]);
-    glr_after(dpp_or<S8>(0.f, E[j]), dpp_or<S8>(0.f, B[j]), E[j], B[j]);
-    Ex[j] = dpp_or<S4>(0.f, E[j]);
-    Bx[j] = dpp_or<S4>(0.f, B[j]);
+    glr_after(dpp_or0<S4>(E[j]), dpp_or0<S4>(B[j]), E[j], B[j]);
+    glr_after(dpp_or0<S8>(E[j]), dpp_or0<S8>(B[j]), E[j], B[j]);
+    Ex[j] = dpp_or0<S4>(E[j]);
+    Bx[j] = dpp_or0<S4>(B[j]);
   }
 }
 
@@ -179,7 +192,12 @@ __device__ __forceinline__ bool glr_seg(const GlrArgs& a, int slot, int seg, int
   const int c = on ? c0 + me.cg * V : 0, ci = c0 + lane_id();                            \
   const bool mine = lane_id() < CB && ci < a.ch; /* a channel of the scanning waves */   \
   float rate[V];                                                                         \
-  _Pragma("unroll") for (int j = 0; j < V; ++j) rate[j] = glr_rate(a.rate, a.lam[c + j])
+  bool deep = false;                                                                     \
+  _Pragma("unroll") for (int j = 0; j < V; ++j) {                                        \
+    rate[j] = glr_rate(a.rate, a.lam[c + j]);                                            \
+    deep |= !(rate[j] < 0.25f);                                                          \
+  }                                                                                      \
+  deep = __any(deep)
 
 // ------------------------------------------------------------------ maps of segments
 // The map of each segment that another one continues from: forward every one but a sequence's last, backward
@@ -189,44 +207,56 @@ template <typename TI, bool FWD> __global__ __launch_bounds__(GNT) void k_glr_ma
   GlrSeg q;
   GLR_BEGIN;
   if (!glr_seg(a, slot, seg, per, q) || (FWD ? q.t1 == q.hi : q.k == 0)) return;
-  const int run = (int)((q.t1 - q.t0 + GROWS - 1) / GROWS);
-  const int64_t t0 = q.t0 + (int64_t)me.tt * run, t1 = t0 + run < q.t1 ? t0 + run : q.t1;
+  constexpr int U = 4;  // tokens of a run in flight; a run is a multiple of them
+  const int run = (int)((q.t1 - q.t0 + GROWS * U - 1) / (GROWS * U)) * U;
   const bool fresh = FWD && a.fresh && q.k == 0 && a.fresh[q.n] != 0;
   float E[V], B[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) E[j] = B[j] = 0.f;
-  constexpr int U = 4;
-  for (int64_t b = 0; b < run; b += U) {
-    i32x4 rr[U], ra[U], rb[U];
+  // the segment's rows in steps of U: thread row tt takes row tt run + b (backward: run - U - b) of it
+  const int64_t mine0 = q.t0 + (int64_t)me.tt * run;
+  const TI *pr = static_cast<const TI*>(a.r) + c, *px = static_cast<const TI*>(FWD ? a.x : a.dy) + c, *pi = static_cast<const TI*>(a.i) + c;
+  const int64_t x_rs = FWD ? a.x_rs : a.dy_rs;
+  i32x4 rr[U], rx[U], ri[U];
+  auto load = [&](int64_t t) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      int64_t t = FWD ? t0 + b + u : t1 - 1 - b - u;
-      t = t < q.t0 ? q.t0 : t >= q.t1 ? q.t1 - 1 : t;
-      rr[u] = *reinterpret_cast<const i32x4*>(static_cast<const TI*>(a.r) + t * a.r_rs + c);
-      ra[u] = *reinterpret_cast<const i32x4*>(static_cast<const TI*>(FWD ? a.x : a.dy) + t * (FWD ? a.x_rs : a.dy_rs) + c);
-      if constexpr (FWD) rb[u] = *reinterpret_cast<const i32x4*>(static_cast<const TI*>(a.i) + t * a.i_rs + c);
+      const int64_t row = t + u < q.t1 ? t + u : q.t1 - 1;
+      rr[u] = *reinterpret_cast<const i32x4*>(pr + row * a.r_rs);
+      rx[u] = *reinterpret_cast<const i32x4*>(px + row * x_rs);
+      if constexpr (FWD) ri[u] = *reinterpret_cast<const i32x4*>(pi + row * a.i_rs);
     }
+  };
+  load(FWD ? mine0 : mine0 + run - U);
+  for (int b = 0; b < run; b += U) {
+    const int64_t t = FWD ? mine0 + b : mine0 + run - U - b;
+    i32x4 cr[U], cx[U], ci4[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t t = FWD ? t0 + b + u : t1 - 1 - b - u;
-      if (t < t0 || t >= t1) continue;
-      float r[V], x[V], iv[V];
-      glr_cvt<TI, V>(rr[u], r);
-      glr_cvt<TI, V>(ra[u], x);
-      if constexpr (FWD) glr_cvt<TI, V>(rb[u], iv);
+      cr[u] = rr[u];
+      cx[u] = rx[u];
+      if constexpr (FWD) ci4[u] = ri[u];
+    }
+    if (b + U < run) load(FWD ? t + U : t - U);
+#pragma unroll
+    for (int w = 0; w < U; ++w) {
+      const int u = FWD ? w : U - 1 - w;
+      if (t + u >= q.t1) continue;
+      float r[V], x[V], iv[V], L[V], e[V];
+      glr_cvt<TI, V>(cr[u], r);
+      glr_cvt<TI, V>(cx[u], x);
+      if constexpr (FWD) glr_cvt<TI, V>(ci4[u], iv);
+#pragma unroll
+      for (int j = 0; j < V; ++j) L[j] = rate[j] * sigmoidf<TI>(r[j]);
+      one_minus_exp<TI, V>(L, deep, e);
+      if (fresh && t + u == q.lo)
+#pragma unroll
+        for (int j = 0; j < V; ++j) e[j] = 1.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float L = rate[j] * sigmoidf<TI>(r[j]);
-        float e, bb;
-        if constexpr (FWD) {
-          e = fresh && t == q.lo ? 1.f : one_minus_exp<TI>(L);
-          bb = glr_weight<TI>(e).w * sigmoidf<TI>(iv[j]) * x[j];
-        } else {
-          e = one_minus_exp<TI>(L);
-          bb = fmaf(-e, x[j], x[j]);
-        }
-        B[j] = fmaf(-e, B[j], B[j]) + bb;
-        E[j] = fmaf(-e, E[j], E[j]) + e;
+        if constexpr (FWD) B[j] = fmaf(1.f - e[j], B[j], glr_weight<TI>(e[j]) * (sigmoidf<TI>(iv[j]) * x[j]));
+        else B[j] = (1.f - e[j]) * (B[j] + x[j]);
+        E[j] = fmaf(-e[j], E[j], E[j]) + e[j];
       }
     }
   }
@@ -255,8 +285,9 @@ template <typename TI, bool FWD> __global__ __launch_bounds__(GNT) void k_glr_ma
 }
 
 // ------------------------------------------------------------------ forward
-template <typename TI, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_fwd(GlrArgs a, int seg, int per) {
+template <typename TI, int K, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_fwd(GlrArgs a, int seg, int per) {
   __shared__ float sE[GE][8 * glr_v<TI>()], sB[GE][8 * glr_v<TI>()], sh[GE][8 * glr_v<TI>()];
+  constexpr int TILE = GROWS * K, SUB = TILE / GTILE, GS = GE / SUB;  // states are saved every GTILE tokens
   GlrSeg q;
   GLR_BEGIN;
   if (!glr_seg(a, slot, seg, per, q)) return;
@@ -269,41 +300,51 @@ template <typename TI, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_f
       h = fmaf(-m[0], h, h) + m[a.ch];
     }
   }
-  i32x4 rx[GK], rr[GK], ri[GK];
+  const GlrView<TI> vx(a.x, a.x_rs, on, me.tt * K, c), vr(a.r, a.r_rs, on, me.tt * K, c), vi(a.i, a.i_rs, on, me.tt * K, c),
+      vy(a.y, a.y_rs, on, me.tt * K, c);
+  auto left = [&](int64_t t) { return (int)(q.t1 - t < TILE ? q.t1 - t : TILE); };
+  i32x4 rx[K], rr[K], ri[K];
   auto load = [&](int64_t t) {
+    const int n = left(t);
+    const auto sr = vr.rows(t, n), si = vi.rows(t, n), sx = vx.rows(t, n);
 #pragma unroll
-    for (int k = 0; k < GK; ++k) {
-      int64_t row = t + me.tt * GK + k;
-      row = row < q.t1 ? row : q.t1 - 1;
-      rx[k] = glr_ld<TI>(a.x, row * a.x_rs + c);
-      rr[k] = glr_ld<TI>(a.r, row * a.r_rs + c);
-      ri[k] = glr_ld<TI>(a.i, row * a.i_rs + c);
+    for (int k = 0; k < K; ++k) {
+      rr[k] = vr.template load<true>(sr, k);
+      ri[k] = vi.template load<true>(si, k);
+      rx[k] = vx.template load<true>(sx, k);
     }
   };
   if (q.t0 < q.t1) load(q.t0);
-  for (int64_t t = q.t0; t < q.t1; t += GTILE) {
-    float e[GK][V], b[GK][V], E[V], B[V], Ex[V], Bx[V];
+  for (int64_t t = q.t0; t < q.t1; t += TILE) {
+    float a1[K][V], b[K][V], E[V], B[V], Ex[V], Bx[V];  // a1 = 1 - e: what a map does to the tokens of this thread alone
+    const bool plain = t + TILE <= q.t1 && !(fresh && t == q.lo);
 #pragma unroll
-    for (int j = 0; j < V; ++j) E[j] = B[j] = 0.f;
-#pragma unroll
-    for (int k = 0; k < GK; ++k) {
-      const int64_t row = t + me.tt * GK + k;
-      const bool live = row < q.t1, open = fresh && row == q.lo;
-      float x[V], r[V], i[V];
+    for (int k = 0; k < K; ++k) {
+      float x[V], r[V], i[V], L[V], e[V];
       glr_cvt<TI, V>(rx[k], x);
       glr_cvt<TI, V>(rr[k], r);
       glr_cvt<TI, V>(ri[k], i);
 #pragma unroll
+      for (int j = 0; j < V; ++j) L[j] = rate[j] * sigmoidf<TI>(r[j]);
+      one_minus_exp<TI, V>(L, deep, e);
+      if (!plain) {
+        const int64_t row = t + me.tt * K + k;
+        if (fresh && row == q.lo)
+#pragma unroll
+          for (int j = 0; j < V; ++j) e[j] = 1.f;
+        if (row >= q.t1)  // a token that changes nothing
+#pragma unroll
+          for (int j = 0; j < V; ++j) e[j] = x[j] = 0.f;
+      }
+#pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float et = open ? 1.f : one_minus_exp<TI>(rate[j] * sigmoidf<TI>(r[j]));
-        const float bt = glr_weight<TI>(et).w * sigmoidf<TI>(i[j]) * x[j];
-        e[k][j] = live ? et : 0.f;
-        b[k][j] = live ? bt : 0.f;
-        B[j] = fmaf(-e[k][j], B[j], B[j]) + b[k][j];
-        E[j] = fmaf(-e[k][j], E[j], E[j]) + e[k][j];
+        b[k][j] = glr_weight<TI>(e[j]) * (sigmoidf<TI>(i[j]) * x[j]);
+        a1[k][j] = 1.f - e[j];
+        B[j] = k ? fmaf(a1[k][j], B[j], b[k][j]) : b[k][j];
+        E[j] = k ? fmaf(-e[j], E[j], E[j]) + e[j] : e[j];
       }
     }
-    if (t + GTILE < q.t1) load(t + GTILE);
+    if (t + TILE < q.t1) load(t + TILE);
     glr_scan4<true, V>(E, B, Ex, Bx);
     if (me.last)
 #pragma unroll
@@ -313,9 +354,10 @@ template <typename TI, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_f
       }
     lds_barrier();
     if (wave_id() == 0 && lane_id() < CB) {
-      if (SAVE && mine) a.sv[((q.lo / GTILE) + q.n + (t - q.lo) / GTILE) * a.ch + ci] = h;
 #pragma unroll
       for (int g = 0; g < GE; ++g) {
+        if (SAVE && g % GS == 0 && mine && t + g / GS * GTILE < q.t1)
+          a.sv[(q.lo / GTILE + q.n + (t - q.lo) / GTILE + g / GS) * a.ch + ci] = h;
         sh[g][lane_id()] = h;
         h = fmaf(-sE[g][lane_id()], h, h) + sB[g][lane_id()];
       }
@@ -327,12 +369,12 @@ template <typename TI, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_f
       const float hc = sh[me.g][me.cg * V + j];
       y[j] = fmaf(-Ex[j], hc, hc) + Bx[j];
     }
+    const auto out = vy.rows(t, left(t));
 #pragma unroll
-    for (int k = 0; k < GK; ++k) {
-      const int64_t row = t + me.tt * GK + k;
+    for (int k = 0; k < K; ++k) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) y[j] = fmaf(-e[k][j], y[j], y[j]) + b[k][j];
-      if (on && row < q.t1) glr_st<TI, V>(a.y, row * a.y_rs + c, y);
+      for (int j = 0; j < V; ++j) y[j] = fmaf(a1[k][j], y[j], b[k][j]);
+      vy.store(out, k, glr_raw<TI, V>(y));
     }
   }
   if (a.hT && wave_id() == 0 && mine && q.t1 == q.hi) a.hT[(int64_t)q.n * a.ch + ci] = h;
@@ -360,16 +402,20 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       cc = fmaf(-m[0], cc, cc) + m[a.ch];
     }
   }
+  const GlrView<TI> vx(a.x, a.x_rs, on, me.tt * GK, c), vr(a.r, a.r_rs, on, me.tt * GK, c), vi(a.i, a.i_rs, on, me.tt * GK, c),
+      vd(a.dy, a.dy_rs, on, me.tt * GK, c), ox(a.dx, a.dx_rs, on, me.tt * GK, c), orr(a.dr, a.dr_rs, on, me.tt * GK, c),
+      oi(a.di, a.di_rs, on, me.tt * GK, c);
+  auto left = [&](int64_t t) { return (int)(q.t1 - t < GTILE ? q.t1 - t : GTILE); };
   i32x4 rx[GK], rr[GK], ri[GK], rd[GK];
   auto load = [&](int64_t t) {
+    const int n = left(t);
+    const auto sr = vr.rows(t, n), si = vi.rows(t, n), sx = vx.rows(t, n), sd = vd.rows(t, n);
 #pragma unroll
     for (int k = 0; k < GK; ++k) {
-      int64_t row = t + me.tt * GK + k;
-      row = row < q.t1 ? row : q.t1 - 1;
-      rr[k] = glr_ld<TI>(a.r, row * a.r_rs + c);
-      ri[k] = glr_ld<TI>(a.i, row * a.i_rs + c);
-      rx[k] = glr_ld<TI>(a.x, row * a.x_rs + c);
-      rd[k] = glr_ld<TI>(a.dy, row * a.dy_rs + c);
+      rr[k] = vr.template load<true>(sr, k);
+      ri[k] = vi.template load<true>(si, k);
+      rx[k] = vx.template load<true>(sx, k);
+      rd[k] = vd.template load<true>(sd, k);
     }
   };
   float dl[V];
@@ -381,15 +427,12 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
     const int64_t t = q.t0 + tile * GTILE;
     float hs = 0.f;  // wave 0: the tile's saved start
     if (wave_id() == 0 && mine) hs = a.sv[((q.lo / GTILE) + q.n + (t - q.lo) / GTILE) * a.ch + ci];
+    const bool plain = t + GTILE <= q.t1 && !(fresh && t == q.lo);
     float e[GK][V], sr[GK][V], si[GK][V], E[V], B[V], Ex[V], Bx[V], F[V], C[V], Fx[V], Cx[V];
     i32x4 kx[GK], kd[GK];
 #pragma unroll
-    for (int j = 0; j < V; ++j) E[j] = B[j] = F[j] = C[j] = 0.f;
-#pragma unroll
     for (int k = 0; k < GK; ++k) {
-      const int64_t row = t + me.tt * GK + k;
-      const bool live = row < q.t1, open = fresh && row == q.lo;
-      float x[V], r[V], i[V];
+      float x[V], r[V], i[V], L[V];
       glr_cvt<TI, V>(rx[k], x);
       glr_cvt<TI, V>(rr[k], r);
       glr_cvt<TI, V>(ri[k], i);
@@ -399,22 +442,34 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       for (int j = 0; j < V; ++j) {
         sr[k][j] = sigmoidf<TI>(r[j]);
         si[k][j] = sigmoidf<TI>(i[j]);
-        const float et = open ? 1.f : one_minus_exp<TI>(rate[j] * sr[k][j]);
-        const float bt = glr_weight<TI>(et).w * si[k][j] * x[j];
-        e[k][j] = live ? et : 0.f;
-        B[j] = fmaf(-e[k][j], B[j], B[j]) + (live ? bt : 0.f);
-        E[j] = fmaf(-e[k][j], E[j], E[j]) + e[k][j];
+        L[j] = rate[j] * sr[k][j];
+      }
+      one_minus_exp<TI, V>(L, deep, e[k]);
+      if (!plain) {
+        const int64_t row = t + me.tt * GK + k;
+        if (fresh && row == q.lo)
+#pragma unroll
+          for (int j = 0; j < V; ++j) e[k][j] = 1.f;
+        if (row >= q.t1) {  // a token that changes nothing
+          kx[k] = kd[k] = i32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < V; ++j) e[k][j] = x[j] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float b = glr_weight<TI>(e[k][j]) * (si[k][j] * x[j]);
+        B[j] = k ? fmaf(1.f - e[k][j], B[j], b) : b;
+        E[j] = k ? fmaf(-e[k][j], E[j], E[j]) + e[k][j] : e[k][j];
       }
     }
 #pragma unroll
     for (int k = GK - 1; k >= 0; --k) {
-      const bool live = t + me.tt * GK + k < q.t1;
       float d[V];
       glr_cvt<TI, V>(kd[k], d);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float s = C[j] + (live ? d[j] : 0.f);
-        C[j] = fmaf(-e[k][j], s, s);
+        C[j] = (1.f - e[k][j]) * (k < GK - 1 ? C[j] + d[j] : d[j]);
         F[j] = E[j];
       }
     }
@@ -446,6 +501,13 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       }
     }
     lds_barrier();
+    // What follows from these is formed anew: kept over the barriers it would take (and spill) more registers than there are.
+#pragma unroll
+    for (int k = 0; k < GK; ++k) {
+      asm volatile("" : "+v"(kx[k]), "+v"(kd[k]));
+#pragma unroll
+      for (int j = 0; j < V; ++j) asm volatile("" : "+v"(e[k][j]), "+v"(sr[k][j]), "+v"(si[k][j]));
+    }
     float hp[GK][V], cg[V];  // the state in front of each token, the gradient from behind
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -453,45 +515,38 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       hp[0][j] = fmaf(-Ex[j], hc, hc) + Bx[j];
       cg[j] = fmaf(-Fx[j], gc, gc) + Cx[j];
     }
-    float w[GK][V], rw[GK][V];
 #pragma unroll
-    for (int k = 0; k < GK; ++k) {
+    for (int k = 0; k + 1 < GK; ++k) {
       float x[V];
       glr_cvt<TI, V>(kx[k], x);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const GlrWeight g = glr_weight<TI>(e[k][j]);
-        w[k][j] = g.w;
-        rw[k][j] = g.rw;
-        if (k + 1 < GK) hp[k + 1 < GK ? k + 1 : k][j] = fmaf(-e[k][j], hp[k][j], hp[k][j]) + w[k][j] * si[k][j] * x[j];
-      }
+      for (int j = 0; j < V; ++j)
+        hp[k + 1][j] = fmaf(1.f - e[k][j], hp[k][j], glr_weight<TI>(e[k][j]) * (si[k][j] * x[j]));
     }
+    const auto tx = ox.rows(t, left(t)), tr = orr.rows(t, left(t)), ti = oi.rows(t, left(t));
 #pragma unroll
     for (int k = GK - 1; k >= 0; --k) {
       const int64_t row = t + me.tt * GK + k;
-      const bool live = row < q.t1;
       float x[V], d[V], dx[V], dr[V], di[V];
       glr_cvt<TI, V>(kx[k], x);
       glr_cvt<TI, V>(kd[k], d);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float G = cg[j] + (live ? d[j] : 0.f), u = si[k][j] * x[j], L = rate[j] * sr[k][j];
-        // a, to its own last bits (zero for a fresh sequence's first token)
-        const float al = e[k][j] < 0.5f || (fresh && row == q.lo) ? 1.f - e[k][j] : glr_exp<TI>(L);
-        const float du = w[k][j] * G;
+        const float G = cg[j] + d[j], u = si[k][j] * x[j], L = rate[j] * sr[k][j], a1 = 1.f - e[k][j];
+        float al = a1;  // a to its own last bits
+        if (deep && !(fresh && row == q.lo)) al = L < 0.25f ? a1 : glr_exp<TI>(L);
+        const float rw = glr_inv_weight<TI>(e[k][j]), du = e[k][j] * (2.f - e[k][j]) * rw * G;
         dx[j] = si[k][j] * du;
         di[j] = u * (1.f - si[k][j]) * du;
         // L dL; a and L first, whose product stays finite
-        const float LdL = (al * L) * G * (u * al * rw[k][j] - hp[k][j]);
+        const float LdL = (al * L) * G * fmaf(u * al, rw, -hp[k][j]);
         dr[j] = LdL * (1.f - sr[k][j]);
-        if (live) dl[j] += LdL;
-        cg[j] = fmaf(-e[k][j], G, G);
+        dl[j] += row < q.t1 ? LdL : 0.f;
+        cg[j] = a1 * G;
       }
-      if (on && live) {
-        glr_st<TI, V>(a.dx, row * a.dx_rs + c, dx);
-        glr_st<TI, V>(a.dr, row * a.dr_rs + c, dr);
-        glr_st<TI, V>(a.di, row * a.di_rs + c, di);
-      }
+      ox.store(tx, k, glr_raw<TI, V>(dx));
+      orr.store(tr, k, glr_raw<TI, V>(dr));
+      oi.store(ti, k, glr_raw<TI, V>(di));
     }
   }
   if (a.dh0 && wave_id() == 1 && mine && q.k == 0) a.dh0[(int64_t)q.n * a.ch + ci] = fresh ? 0.f : cc;
@@ -499,8 +554,8 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < V; ++j) {  // the four thread rows, then the groups
-      dl[j] += dpp_or<0x114>(0.f, dl[j]);
-      dl[j] += dpp_or<0x118>(0.f, dl[j]);
+      dl[j] += dpp_or0<0x114>(dl[j]);
+      dl[j] += dpp_or0<0x118>(dl[j]);
       if (me.last) sE[me.g][me.cg * V + j] = dl[j];
     }
     __syncthreads();
@@ -529,11 +584,14 @@ template <typename TI> __global__ __launch_bounds__(64) void k_glr_decode(GlrArg
   const F8 lam = ld8<float>(a.lam + c);
   F8 h = fresh ? zero8() : ld8<float>(st);
   const F8 x = cvt8<TI>(rx), r = cvt8<TI>(rr), i = cvt8<TI>(ri);
+  float L[8], e[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) L[j] = glr_rate(a.rate, lam.v[j]) * sigmoidf<TI>(r.v[j]);
+  one_minus_exp<TI, 8>(L, true, e);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float e = one_minus_exp<TI>(glr_rate(a.rate, lam.v[j]) * sigmoidf<TI>(r.v[j]));
     const float u = sigmoidf<TI>(i.v[j]) * x.v[j];
-    h.v[j] = fresh ? u : fmaf(-e, h.v[j], h.v[j]) + glr_weight<TI>(e).w * u;
+    h.v[j] = fresh ? u : fmaf(-e[j], h.v[j], h.v[j]) + glr_weight<TI>(e[j]) * u;
   }
   st8<float>(st, h);
   st8<TI>((TI*)a.y + (int64_t)n * a.y_rs + c, h);
@@ -585,8 +643,8 @@ template <typename TI> static hipError_t glr_forward(const GlrArgs& a, int dtype
     if (e != hipSuccess) return e;
   }
   traced("k_glr_fwd", s, [&] {
-    if (a.sv) k_glr_fwd<TI, true><<<grid, GNT, 0, s>>>(a, p.seg, p.per);
-    else k_glr_fwd<TI, false><<<grid, GNT, 0, s>>>(a, p.seg, p.per);
+    if (a.sv) k_glr_fwd<TI, 4, true><<<grid, GNT, 0, s>>>(a, p.seg, p.per);
+    else k_glr_fwd<TI, 4, false><<<grid, GNT, 0, s>>>(a, p.seg, p.per);
   });
   return hipGetLastError();
 }

@@ -43,11 +43,17 @@ gdn::GlrArgs glr_args(const gdn_glr_problem* p) {
   return a;
 }
 
+// A row view of the recurrence: its kernels address the 256 rows of a tile with 31-bit byte offsets.
+gdn_status glr_view(const gdn_glr_problem* p, const void* v, int64_t rs) {
+  if (p->T_total > 0 && rs * esize(p->dtype) >= (int64_t)1 << 23) return GDN_EINVAL;
+  return check_view(v, rs, p->channels, p->dtype, p->T_total);
+}
+
 gdn_status glr_inputs(const gdn_glr_problem* p, const void* x, int64_t x_rs, const void* r, int64_t r_rs, const void* i,
                       int64_t i_rs, gdn::GlrArgs& a) {
-  GDN_TRY(check_view(x, x_rs, p->channels, p->dtype, p->T_total));
-  GDN_TRY(check_view(r, r_rs, p->channels, p->dtype, p->T_total));
-  GDN_TRY(check_view(i, i_rs, p->channels, p->dtype, p->T_total));
+  GDN_TRY(glr_view(p, x, x_rs));
+  GDN_TRY(glr_view(p, r, r_rs));
+  GDN_TRY(glr_view(p, i, i_rs));
   a.x = x; a.x_rs = x_rs; a.r = r; a.r_rs = r_rs; a.i = i; a.i_rs = i_rs;
   return GDN_OK;
 }
@@ -145,7 +151,7 @@ gdn_status gdn_glr_fwd(const gdn_glr_problem* p, const void* x, int64_t x_rs, co
   GDN_TRY(check_glr(p));
   gdn::GlrArgs a = glr_args(p);
   GDN_TRY(glr_inputs(p, x, x_rs, r, r_rs, i, i_rs, a));
-  GDN_TRY(check_view(y, y_rs, p->channels, p->dtype, p->T_total));
+  GDN_TRY(glr_view(p, y, y_rs));
   GDN_TRY(check_in_place(p->T_total, {{x, x_rs}, {r, r_rs}, {i, i_rs}}, {{y, y_rs}}));
   GDN_TRY(check_arr(h0, false, 16));
   GDN_TRY(check_arr(h_T, false, 16));
@@ -166,10 +172,10 @@ gdn_status gdn_glr_bwd(const gdn_glr_problem* p, const void* x, int64_t x_rs, co
   GDN_TRY(check_glr(p));
   gdn::GlrArgs a = glr_args(p);
   GDN_TRY(glr_inputs(p, x, x_rs, r, r_rs, i, i_rs, a));
-  GDN_TRY(check_view(dy, dy_rs, p->channels, p->dtype, p->T_total));
-  GDN_TRY(check_view(dx, dx_rs, p->channels, p->dtype, p->T_total));
-  GDN_TRY(check_view(dr, dr_rs, p->channels, p->dtype, p->T_total));
-  GDN_TRY(check_view(di, di_rs, p->channels, p->dtype, p->T_total));
+  GDN_TRY(glr_view(p, dy, dy_rs));
+  GDN_TRY(glr_view(p, dx, dx_rs));
+  GDN_TRY(glr_view(p, dr, dr_rs));
+  GDN_TRY(glr_view(p, di, di_rs));
   GDN_TRY(check_in_place(p->T_total, {{x, x_rs}, {r, r_rs}, {i, i_rs}, {dy, dy_rs}}, {{dx, dx_rs}, {dr, dr_rs}, {di, di_rs}}));
   GDN_TRY(check_arr(dh_T, false, 16));
   GDN_TRY(check_arr(dh0, false, 16));

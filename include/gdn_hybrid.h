@@ -27,8 +27,8 @@ extern "C" {
  *   h_t = a_t h_{t-1} + w_t s(i_t) x_t,  y_t = h_t
  *
  * starting from h0 (zero when NULL). The first token of a sequence that is `fresh` enters with weight
- * one and no decay, h = s(i) x (its h0 is not read). x, r, i, y: [rows][channels] in dtype; sums and
- * states are float32, 1 - a is formed without cancellation. rate softplus(lambda) counts up to 2^100.
+ * one and no decay, h = s(i) x (its h0 is not read). x, r, i, y: [rows][channels] in dtype, a row
+ * stride below 2^23 bytes; sums and states are float32, 1 - a is formed without cancellation. rate softplus(lambda) counts up to 2^100.
  */
 typedef struct {
   int32_t N;        /* sequences (>= 0) */

@@ -31,8 +31,9 @@ constexpr int GK = 2;              // tokens per thread and tile
 constexpr int GTILE = GROWS * GK;  // tokens per tile
 constexpr int GE = GNT / 32;       // groups of four thread rows
 
-// V adjacent values of a row (16 bytes).
+// V adjacent values of a row (16 bytes), and the same as float32.
 template <typename TI> constexpr int glr_v() { return 16 / (int)sizeof(TI); }
+
 // A thread's piece of the rows of a tensor, from row `row` of a tile on (kNowhere: of no row).
 template <typename TI> struct GlrView {
   const TI* p;
@@ -44,29 +45,21 @@ template <typename TI> struct GlrView {
   }
   // The `rows` rows from t on (a tile's at the most).
   __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(int64_t t, int rows) const { return rows_rsrc(p + t * rs, (uint32_t)rows * rsb); }
-  template <bool NT> __device__ __forceinline__ i32x4 load(__amdgpu_buffer_rsrc_t r, int k) const { return buf_ld16<NT>(r, voff + (uint32_t)k * rsb); }
+  __device__ __forceinline__ i32x4 load(__amdgpu_buffer_rsrc_t r, int k) const { return buf_ld16<true>(r, voff + (uint32_t)k * rsb); }
   __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, int k, i32x4 v) const { buf_st16<true>(r, voff + (uint32_t)k * rsb, v); }
 };
 template <typename TI, int V> __device__ __forceinline__ void glr_cvt(i32x4 r, float (&v)[V]) {
-  if constexpr (sizeof(TI) == 2) {
-    const bf16x8 b = __builtin_bit_cast(bf16x8, r);
+  typedef TI vec __attribute__((ext_vector_type(V)));
+  const vec b = __builtin_bit_cast(vec, r);
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = (float)b[j];
-  } else {
-    const f32x4 b = __builtin_bit_cast(f32x4, r);
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = b[j];
-  }
+  for (int j = 0; j < V; ++j) v[j] = (float)b[j];
 }
 template <typename TI, int V> __device__ __forceinline__ i32x4 glr_raw(const float (&v)[V]) {
-  if constexpr (sizeof(TI) == 2) {
-    bf16x8 b;
+  typedef TI vec __attribute__((ext_vector_type(V)));
+  vec b;
 #pragma unroll
-    for (int j = 0; j < V; ++j) b[j] = (__bf16)v[j];
-    return __builtin_bit_cast(i32x4, b);
-  } else {
-    return __builtin_bit_cast(i32x4, f32x4{v[0], v[1], v[2], v[3]});
-  }
+  for (int j = 0; j < V; ++j) b[j] = (TI)v[j];
+  return __builtin_bit_cast(i32x4, b);
 }
 
 // rate softplus(lambda), kept finite (an infinite exponent times a state would be NaN where a is zero).
@@ -80,45 +73,55 @@ template <typename TI> __device__ __forceinline__ float glr_exp(float L) {
   if constexpr (sizeof(TI) == 2) return __builtin_amdgcn_exp2f(L * -1.44269504f);
   else return expf(-L);
 }
-// 1 - exp(-L): its series up to L^6 below a quarter (the next term is 5e-8 of it). `deep` (wave-uniform): some L may
-// be more; where no channel's rate is, the exponentials are left out.
+// 1 - exp(-L): below a quarter L q(L) with q of degree 4 through (1 - exp(-L)) / L at the five Chebyshev points of
+// [0, 1/4] (5e-9 off). `deep` (wave-uniform): some L may be more; where no channel's rate is, the exponentials are left out.
 template <typename TI, int V> __device__ __forceinline__ void one_minus_exp(const float (&L)[V], bool deep, float (&e)[V]) {
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    float p = fmaf(L[j], -1.f / 720.f, 1.f / 120.f);
-    p = fmaf(L[j], p, -1.f / 24.f);
-    p = fmaf(L[j], p, 1.f / 6.f);
-    p = fmaf(L[j], p, -0.5f) * L[j];
-    e[j] = fmaf(L[j], p, L[j]);
+    float q = fmaf(L[j], 0.007513606f, -0.041490655f);
+    q = fmaf(L[j], q, 0.166651085f);
+    q = fmaf(L[j], q, -0.49999952f);
+    q = fmaf(L[j], q, 1.f);
+    e[j] = L[j] * q;
   }
   if (deep) {
-    asm volatile("");  // (a branch, not eight exponentials for nothing)
 #pragma unroll
-    for (int j = 0; j < V; ++j) e[j] = L[j] < 0.25f ? e[j] : 1.f - glr_exp<TI>(L[j]);
+    for (int j = 0; j < V; ++j) {
+      float x = L[j];
+      asm volatile("" : "+v"(x));  // (keeps the branch: not eight exponentials for nothing)
+      e[j] = x < 0.25f ? e[j] : 1.f - glr_exp<TI>(x);
+    }
   }
 }
 
-// w = sqrt(1 - a^2) of e = 1 - a. A w below 2^-63, whose square no float32 holds in full, may come out as less.
-template <typename TI> __device__ __forceinline__ float glr_weight(float e) {
-  if constexpr (sizeof(TI) == 2) return __builtin_amdgcn_sqrtf(e * (2.f - e));
-  else return sqrtf(e * (2.f - e));
+// w = sqrt(1 - a^2) = sqrt(e (1 + a)) of e and a1 = 1 - e. A w below 2^-63, whose square no float32 holds in full, may
+// come out as less.
+template <typename TI> __device__ __forceinline__ float glr_weight(float e, float a1) {
+  const float w2 = fmaf(e, a1, e);
+  if constexpr (sizeof(TI) == 2) return __builtin_amdgcn_sqrtf(w2);
+  else return sqrtf(w2);
 }
-// 1 / w, which ends at 2^63 (L / w is then zero where L is).
-template <typename TI> __device__ __forceinline__ float glr_inv_weight(float e) {
-  const float w2 = fmaxf(e * (2.f - e), 0x1p-126f);
-  if constexpr (sizeof(TI) == 2) return __builtin_amdgcn_rsqf(w2);
-  else return 1.f / sqrtf(w2);
-}
-
-// (E, B) <- first (E1, B1), then (E, B).
-__device__ __forceinline__ void glr_after(float E1, float B1, float& E, float& B) {
-  B = fmaf(-E, B1, B1) + B;
-  E = fmaf(-E1, E, E1) + E;
+// The same and 1 / w, which ends at 2^63 (L / w is then zero where L is).
+template <typename TI> __device__ __forceinline__ float2 glr_weights(float e, float a1) {
+  const float w2 = fmaf(e, a1, e), c = fmaxf(w2, 0x1p-126f);
+  if constexpr (sizeof(TI) == 2) {
+    const float r = __builtin_amdgcn_rsqf(c);
+    return float2{w2 * r, r};
+  } else {
+    return float2{sqrtf(w2), 1.f / sqrtf(c)};
+  }
 }
 
 // x of the lane that CTRL names, zero where it lies outside the row of 16 (e = 0, b = 0: the map that changes nothing).
 template <int CTRL> __device__ __forceinline__ float dpp_or0(float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
+}
+// (E, B) <- first (E1, B1), then (E, B): with A = 1 - E, E + E1 A and B + B1 A. E1 A is rounded relative to itself, so a sum of
+// small E keeps its bits.
+__device__ __forceinline__ void glr_after(float E1, float B1, float& E, float& B) {
+  const float A = 1.f - E;
+  E = fmaf(E1, A, E);
+  B = fmaf(B1, A, B);
 }
 // The four thread rows of a DPP row: (E, B) composed with those in front of it (FWD, row_shr) or behind it
 // (row_shl), and (Ex, Bx) that of the others alone.
@@ -148,49 +151,98 @@ struct GlrLane {
   }
 };
 
-// Segment `slot` of the launch: tokens [t0, t1), the k-th of sequence n (rows [lo, hi)). Without a table: segment
-// k of a packed sequence has slot lo / seg + n + k, below T_total / seg + N, and no two share one.
+// How a launch cuts its sequences: one of at most `keep` tokens is a segment, a longer one is cut into segments of `seg`
+// (a multiple of a tile; `per` of them to a sequence where there is no table).
+struct GlrPlan {
+  int seg, keep, per, slots, blocks;  // segment slots, channel blocks
+  bool cut;                           // some sequence may have more than one segment
+};
+
+// Segment `slot` of the launch: tokens [t0, t1), the k-th of sequence n's `segs` (rows [lo, hi)). The slots of a packed batch
+// of up to kGlrEven sequences are its segments, one after the other; of a larger one segment k has slot lo / seg + n + k, below
+// T_total / seg + N, and some are empty. (Empty workgroups among the others make the dispatcher put two of these on one
+// compute unit: 4 x 4096 x 2560 took 160 us instead of 97.)
+constexpr int kGlrEven = 256;
 struct GlrSeg {
-  int n, k;
+  int n, k, segs;
   int64_t lo, hi, t0, t1;
 };
-__device__ __forceinline__ bool glr_seg(const GlrArgs& a, int slot, int seg, int per, GlrSeg& q) {
+__device__ __forceinline__ int glr_size(const GlrPlan& p, int len) { return len <= p.keep ? p.keep : p.seg; }
+__device__ __forceinline__ int glr_segs(const GlrPlan& p, int len) {
+  const int size = glr_size(p, len);
+  return len <= size ? 1 : (len + size - 1) / size;
+}
+__device__ __forceinline__ bool glr_seg(const GlrArgs& a, const GlrPlan& p, int slot, GlrSeg& q) {
+  auto rows = [&](int n, int64_t& lo, int64_t& hi) {  // of a packed sequence, clamped into the caller's
+    const int64_t x = a.cu[n], y = a.cu[n + 1];
+    lo = x < 0 ? 0 : x > a.rows ? a.rows : x;
+    hi = y < lo ? lo : y > a.rows ? a.rows : y;
+  };
   if (!a.cu) {
-    q.n = slot / per;
-    q.k = slot - q.n * per;
+    q.n = slot / p.per;
+    q.k = slot - q.n * p.per;
     q.lo = (int64_t)q.n * a.T;
     q.hi = q.lo + a.T;
+  } else if (a.N <= kGlrEven) {
+    constexpr int U = kGlrEven / 64;  // lane l looks at sequences U l .. U l + U - 1
+    int cnt[U], sum = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      cnt[u] = 0;
+      if (lane_id() * U + u < a.N) {
+        int64_t lo, hi;
+        rows(lane_id() * U + u, lo, hi);
+        cnt[u] = glr_segs(p, (int)(hi - lo));
+      }
+      sum += cnt[u];
+    }
+    int at = wave_scan_incl_int(sum) - sum, n = -1, k = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (slot >= at && slot < at + cnt[u]) {
+        n = lane_id() * U + u;
+        k = slot - at;
+      }
+      at += cnt[u];
+    }
+    const uint64_t who = __ballot(n >= 0);
+    if (who == 0) return false;
+    const int l = __builtin_ctzll(who);
+    q.n = __builtin_amdgcn_readlane(n, l);
+    q.k = __builtin_amdgcn_readlane(k, l);
+    rows(q.n, q.lo, q.hi);
   } else {
-    auto clamp = [&](int64_t v) { return v < 0 ? 0 : v > a.rows ? a.rows : v; };
     int l = 0;
     for (int n = a.N; n > 1;) {  // the largest n whose first slot is at most `slot`, 64 probes at a time
       const int stride = (n + 63) / 64, i = lane_id() * stride;
-      const uint64_t m = __ballot(i < n && (int)((uint32_t)clamp(a.cu[l + (i < n ? i : 0)]) / (uint32_t)seg) + l + i <= slot);
+      int64_t lo, hi;
+      rows(l + (i < n ? i : 0), lo, hi);
+      const uint64_t m = __ballot(i < n && (int)((uint32_t)lo / (uint32_t)p.seg) + l + i <= slot);
       const int at = (m ? 63 - __builtin_clzll(m) : 0) * stride;
       l += at;
       n = n - at < stride ? n - at : stride;
     }
     q.n = __builtin_amdgcn_readfirstlane(l);
-    q.lo = clamp(a.cu[q.n]);
-    q.hi = clamp(a.cu[q.n + 1]);
-    if (q.hi < q.lo) q.hi = q.lo;
-    q.k = slot - (int)((uint32_t)q.lo / (uint32_t)seg) - q.n;
+    rows(q.n, q.lo, q.hi);
+    q.k = slot - (int)((uint32_t)q.lo / (uint32_t)p.seg) - q.n;
   }
-  if (q.k < 0 || (q.k > 0 && (int64_t)q.k * seg >= q.hi - q.lo)) return false;
-  q.t0 = q.lo + (int64_t)q.k * seg;
-  q.t1 = q.t0 + seg < q.hi ? q.t0 + seg : q.hi;
+  const int len = (int)(q.hi - q.lo), size = glr_size(p, len);
+  q.segs = glr_segs(p, len);
+  if (q.k < 0 || q.k >= q.segs) return false;
+  q.t0 = q.lo + (int64_t)q.k * size;
+  q.t1 = q.t0 + size < q.hi ? q.t0 + size : q.hi;
   return true;
 }
 
 // Workgroup -> (segment slot, first channel): channel blocks run fastest, so that workgroups in flight read whole rows.
-#define GLR_BEGIN                                                                        \
+#define GLR_PLACE                                                                        \
   constexpr int V = glr_v<TI>(), CB = 8 * V;                                             \
-  const int cbn = (a.ch + CB - 1) / CB, slot = (int)blockIdx.x / cbn;                    \
-  const int c0 = ((int)blockIdx.x - slot * cbn) * CB;                                    \
+  const int slot = (int)blockIdx.x / pl.blocks, c0 = ((int)blockIdx.x - slot * pl.blocks) * CB; \
   const GlrLane me;                                                                      \
   const bool on = c0 + me.cg * V < a.ch;                                                 \
   const int c = on ? c0 + me.cg * V : 0, ci = c0 + lane_id();                            \
-  const bool mine = lane_id() < CB && ci < a.ch; /* a channel of the scanning waves */   \
+  const bool mine = lane_id() < CB && ci < a.ch /* a channel of the scanning waves */
+#define GLR_RATES                                                                        \
   float rate[V];                                                                         \
   bool deep = false;                                                                     \
   _Pragma("unroll") for (int j = 0; j < V; ++j) {                                        \
@@ -202,62 +254,50 @@ __device__ __forceinline__ bool glr_seg(const GlrArgs& a, int slot, int seg, int
 // ------------------------------------------------------------------ maps of segments
 // The map of each segment that another one continues from: forward every one but a sequence's last, backward
 // every one but its first. A thread row takes a contiguous run of the tokens. [slot][E | B][ch].
-template <typename TI, bool FWD> __global__ __launch_bounds__(GNT) void k_glr_map(GlrArgs a, int seg, int per) {
-  __shared__ float sE[GE][8 * glr_v<TI>()], sB[GE][8 * glr_v<TI>()];
+template <typename TI, bool FWD> __global__ __launch_bounds__(GNT) void k_glr_map(GlrArgs a, GlrPlan pl) {
   GlrSeg q;
-  GLR_BEGIN;
-  if (!glr_seg(a, slot, seg, per, q) || (FWD ? q.t1 == q.hi : q.k == 0)) return;
-  constexpr int U = 4;  // tokens of a run in flight; a run is a multiple of them
-  const int run = (int)((q.t1 - q.t0 + GROWS * U - 1) / (GROWS * U)) * U;
+  GLR_PLACE;
+  __shared__ float sE[GE][CB], sB[GE][CB];
+  if (!glr_seg(a, pl, slot, q) || (FWD ? q.k == q.segs - 1 : q.k == 0)) return;
+  GLR_RATES;
+  // a thread row's run of the tokens, one of them ahead in flight (four took more registers, and then half the waves:
+  // 16384 x 4096 tokens 94 us, with one 83)
+  const int run = (int)((q.t1 - q.t0 + GROWS - 1) / GROWS);
   const bool fresh = FWD && a.fresh && q.k == 0 && a.fresh[q.n] != 0;
   float E[V], B[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) E[j] = B[j] = 0.f;
-  // the segment's rows in steps of U: thread row tt takes row tt run + b (backward: run - U - b) of it
-  const int64_t mine0 = q.t0 + (int64_t)me.tt * run;
+  const int64_t begin = q.t0 + (int64_t)me.tt * run;
   const TI *pr = static_cast<const TI*>(a.r) + c, *px = static_cast<const TI*>(FWD ? a.x : a.dy) + c, *pi = static_cast<const TI*>(a.i) + c;
   const int64_t x_rs = FWD ? a.x_rs : a.dy_rs;
-  i32x4 rr[U], rx[U], ri[U];
+  i32x4 rr, rx, ri;
   auto load = [&](int64_t t) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = t + u < q.t1 ? t + u : q.t1 - 1;
-      rr[u] = *reinterpret_cast<const i32x4*>(pr + row * a.r_rs);
-      rx[u] = *reinterpret_cast<const i32x4*>(px + row * x_rs);
-      if constexpr (FWD) ri[u] = *reinterpret_cast<const i32x4*>(pi + row * a.i_rs);
-    }
+    const int64_t row = t < q.t1 ? t : q.t1 - 1;
+    rr = *reinterpret_cast<const i32x4*>(pr + row * a.r_rs);
+    rx = *reinterpret_cast<const i32x4*>(px + row * x_rs);
+    if constexpr (FWD) ri = *reinterpret_cast<const i32x4*>(pi + row * a.i_rs);
   };
-  load(FWD ? mine0 : mine0 + run - U);
-  for (int b = 0; b < run; b += U) {
-    const int64_t t = FWD ? mine0 + b : mine0 + run - U - b;
-    i32x4 cr[U], cx[U], ci4[U];
+  load(FWD ? begin : begin + run - 1);
+  for (int b = 0; b < run; ++b) {
+    const int64_t t = FWD ? begin + b : begin + run - 1 - b;
+    float r[V], x[V], iv[V], L[V], e[V];
+    glr_cvt<TI, V>(rr, r);
+    glr_cvt<TI, V>(rx, x);
+    if constexpr (FWD) glr_cvt<TI, V>(ri, iv);
+    if (b + 1 < run) load(FWD ? t + 1 : t - 1);
+    if (t >= q.t1) continue;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      cr[u] = rr[u];
-      cx[u] = rx[u];
-      if constexpr (FWD) ci4[u] = ri[u];
-    }
-    if (b + U < run) load(FWD ? t + U : t - U);
+    for (int j = 0; j < V; ++j) L[j] = rate[j] * sigmoidf<TI>(r[j]);
+    one_minus_exp<TI, V>(L, deep, e);
+    if (fresh && t == q.lo)
 #pragma unroll
-    for (int w = 0; w < U; ++w) {
-      const int u = FWD ? w : U - 1 - w;
-      if (t + u >= q.t1) continue;
-      float r[V], x[V], iv[V], L[V], e[V];
-      glr_cvt<TI, V>(cr[u], r);
-      glr_cvt<TI, V>(cx[u], x);
-      if constexpr (FWD) glr_cvt<TI, V>(ci4[u], iv);
+      for (int j = 0; j < V; ++j) e[j] = 1.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j) L[j] = rate[j] * sigmoidf<TI>(r[j]);
-      one_minus_exp<TI, V>(L, deep, e);
-      if (fresh && t + u == q.lo)
-#pragma unroll
-        for (int j = 0; j < V; ++j) e[j] = 1.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if constexpr (FWD) B[j] = fmaf(1.f - e[j], B[j], glr_weight<TI>(e[j]) * (sigmoidf<TI>(iv[j]) * x[j]));
-        else B[j] = (1.f - e[j]) * (B[j] + x[j]);
-        E[j] = fmaf(-e[j], E[j], E[j]) + e[j];
-      }
+    for (int j = 0; j < V; ++j) {
+      const float a1 = 1.f - e[j];
+      if constexpr (FWD) B[j] = fmaf(a1, B[j], glr_weight<TI>(e[j], a1) * (sigmoidf<TI>(iv[j]) * x[j]));
+      else B[j] = a1 * (B[j] + x[j]);
+      E[j] = fmaf(E[j], a1, e[j]);
     }
   }
   float Ex[V], Bx[V];
@@ -285,12 +325,12 @@ template <typename TI, bool FWD> __global__ __launch_bounds__(GNT) void k_glr_ma
 }
 
 // ------------------------------------------------------------------ forward
-template <typename TI, int K, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_fwd(GlrArgs a, int seg, int per) {
-  __shared__ float sE[GE][8 * glr_v<TI>()], sB[GE][8 * glr_v<TI>()], sh[GE][8 * glr_v<TI>()];
-  constexpr int TILE = GROWS * K, SUB = TILE / GTILE, GS = GE / SUB;  // states are saved every GTILE tokens
+template <typename TI, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_fwd(GlrArgs a, GlrPlan pl) {
   GlrSeg q;
-  GLR_BEGIN;
-  if (!glr_seg(a, slot, seg, per, q)) return;
+  GLR_PLACE;
+  __shared__ float sE[GE][CB], sB[GE][CB], sh[GE][CB];
+  if (!glr_seg(a, pl, slot, q)) return;
+  GLR_RATES;
   const bool fresh = a.fresh && a.fresh[q.n] != 0;
   float h = 0.f;  // wave 0: the carried state of channel ci
   if (wave_id() == 0 && mine) {
@@ -300,26 +340,26 @@ template <typename TI, int K, bool SAVE> __global__ __launch_bounds__(GNT) void 
       h = fmaf(-m[0], h, h) + m[a.ch];
     }
   }
-  const GlrView<TI> vx(a.x, a.x_rs, on, me.tt * K, c), vr(a.r, a.r_rs, on, me.tt * K, c), vi(a.i, a.i_rs, on, me.tt * K, c),
-      vy(a.y, a.y_rs, on, me.tt * K, c);
-  auto left = [&](int64_t t) { return (int)(q.t1 - t < TILE ? q.t1 - t : TILE); };
-  i32x4 rx[K], rr[K], ri[K];
+  const GlrView<TI> vx(a.x, a.x_rs, on, me.tt * GK, c), vr(a.r, a.r_rs, on, me.tt * GK, c), vi(a.i, a.i_rs, on, me.tt * GK, c),
+      vy(a.y, a.y_rs, on, me.tt * GK, c);
+  auto left = [&](int64_t t) { return (int)(q.t1 - t < GTILE ? q.t1 - t : GTILE); };
+  i32x4 rx[GK], rr[GK], ri[GK];
   auto load = [&](int64_t t) {
     const int n = left(t);
     const auto sr = vr.rows(t, n), si = vi.rows(t, n), sx = vx.rows(t, n);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      rr[k] = vr.template load<true>(sr, k);
-      ri[k] = vi.template load<true>(si, k);
-      rx[k] = vx.template load<true>(sx, k);
+    for (int k = 0; k < GK; ++k) {
+      rr[k] = vr.load(sr, k);
+      ri[k] = vi.load(si, k);
+      rx[k] = vx.load(sx, k);
     }
   };
   if (q.t0 < q.t1) load(q.t0);
-  for (int64_t t = q.t0; t < q.t1; t += TILE) {
-    float a1[K][V], b[K][V], E[V], B[V], Ex[V], Bx[V];  // a1 = 1 - e: what a map does to the tokens of this thread alone
-    const bool plain = t + TILE <= q.t1 && !(fresh && t == q.lo);
+  for (int64_t t = q.t0; t < q.t1; t += GTILE) {
+    float a1[GK][V], b[GK][V], E[V], B[V], Ex[V], Bx[V];  // a1 = 1 - e: what a map does to the tokens of this thread alone
+    const bool plain = t + GTILE <= q.t1 && !(fresh && t == q.lo);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; k < GK; ++k) {
       float x[V], r[V], i[V], L[V], e[V];
       glr_cvt<TI, V>(rx[k], x);
       glr_cvt<TI, V>(rr[k], r);
@@ -328,7 +368,7 @@ template <typename TI, int K, bool SAVE> __global__ __launch_bounds__(GNT) void 
       for (int j = 0; j < V; ++j) L[j] = rate[j] * sigmoidf<TI>(r[j]);
       one_minus_exp<TI, V>(L, deep, e);
       if (!plain) {
-        const int64_t row = t + me.tt * K + k;
+        const int64_t row = t + me.tt * GK + k;
         if (fresh && row == q.lo)
 #pragma unroll
           for (int j = 0; j < V; ++j) e[j] = 1.f;
@@ -338,13 +378,13 @@ template <typename TI, int K, bool SAVE> __global__ __launch_bounds__(GNT) void 
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        b[k][j] = glr_weight<TI>(e[j]) * (sigmoidf<TI>(i[j]) * x[j]);
         a1[k][j] = 1.f - e[j];
+        b[k][j] = glr_weight<TI>(e[j], a1[k][j]) * (sigmoidf<TI>(i[j]) * x[j]);
         B[j] = k ? fmaf(a1[k][j], B[j], b[k][j]) : b[k][j];
-        E[j] = k ? fmaf(-e[j], E[j], E[j]) + e[j] : e[j];
+        E[j] = k ? fmaf(E[j], a1[k][j], e[j]) : e[j];
       }
     }
-    if (t + TILE < q.t1) load(t + TILE);
+    if (t + GTILE < q.t1) load(t + GTILE);
     glr_scan4<true, V>(E, B, Ex, Bx);
     if (me.last)
 #pragma unroll
@@ -354,10 +394,9 @@ template <typename TI, int K, bool SAVE> __global__ __launch_bounds__(GNT) void 
       }
     lds_barrier();
     if (wave_id() == 0 && lane_id() < CB) {
+      if (SAVE && mine) a.sv[(q.lo / GTILE + q.n + (t - q.lo) / GTILE) * a.ch + ci] = h;
 #pragma unroll
       for (int g = 0; g < GE; ++g) {
-        if (SAVE && g % GS == 0 && mine && t + g / GS * GTILE < q.t1)
-          a.sv[(q.lo / GTILE + q.n + (t - q.lo) / GTILE + g / GS) * a.ch + ci] = h;
         sh[g][lane_id()] = h;
         h = fmaf(-sE[g][lane_id()], h, h) + sB[g][lane_id()];
       }
@@ -371,33 +410,32 @@ template <typename TI, int K, bool SAVE> __global__ __launch_bounds__(GNT) void 
     }
     const auto out = vy.rows(t, left(t));
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; k < GK; ++k) {
 #pragma unroll
       for (int j = 0; j < V; ++j) y[j] = fmaf(a1[k][j], y[j], b[k][j]);
       vy.store(out, k, glr_raw<TI, V>(y));
     }
   }
-  if (a.hT && wave_id() == 0 && mine && q.t1 == q.hi) a.hT[(int64_t)q.n * a.ch + ci] = h;
+  if (a.hT && wave_id() == 0 && mine && q.k == q.segs - 1) a.hT[(int64_t)q.n * a.ch + ci] = h;
 }
 
 // ------------------------------------------------------------------ backward
 // Tiles from the last to the first; within a tile the states from its saved start and the gradients from
 // those behind it side by side. Partials of dlambda: [slot][ch].
-template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs a, int seg, int per, float* part) {
-  __shared__ float sE[GE][8 * glr_v<TI>()], sB[GE][8 * glr_v<TI>()], sC[GE][8 * glr_v<TI>()];
-  __shared__ float sh[GE][8 * glr_v<TI>()], sg[GE][8 * glr_v<TI>()];
+template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs a, GlrPlan pl, float* part) {
   GlrSeg q;
-  GLR_BEGIN;
-  if (!glr_seg(a, slot, seg, per, q)) {
+  GLR_PLACE;
+  __shared__ float sE[GE][CB], sB[GE][CB], sC[GE][CB], sh[GE][CB], sg[GE][CB];
+  if (!glr_seg(a, pl, slot, q)) {
     if (part && wave_id() == 0 && mine) part[(int64_t)slot * a.ch + ci] = 0.f;
     return;
   }
+  GLR_RATES;
   const bool fresh = a.fresh && a.fresh[q.n] != 0;
   float cc = 0.f;  // wave 1: the gradient that flows into the tile's end
   if (wave_id() == 1 && mine) {
     cc = a.dhT ? a.dhT[(int64_t)q.n * a.ch + ci] : 0.f;
-    const int segs = (int)((q.hi - q.lo + seg - 1) / seg);
-    for (int s = slot - q.k + segs - 1; s > slot; --s) {
+    for (int s = slot - q.k + q.segs - 1; s > slot; --s) {
       const float* m = a.ws + (int64_t)s * 2 * a.ch + ci;
       cc = fmaf(-m[0], cc, cc) + m[a.ch];
     }
@@ -412,10 +450,10 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
     const auto sr = vr.rows(t, n), si = vi.rows(t, n), sx = vx.rows(t, n), sd = vd.rows(t, n);
 #pragma unroll
     for (int k = 0; k < GK; ++k) {
-      rr[k] = vr.template load<true>(sr, k);
-      ri[k] = vi.template load<true>(si, k);
-      rx[k] = vx.template load<true>(sx, k);
-      rd[k] = vd.template load<true>(sd, k);
+      rr[k] = vr.load(sr, k);
+      ri[k] = vi.load(si, k);
+      rx[k] = vx.load(sx, k);
+      rd[k] = vd.load(sd, k);
     }
   };
   float dl[V];
@@ -458,9 +496,9 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float b = glr_weight<TI>(e[k][j]) * (si[k][j] * x[j]);
-        B[j] = k ? fmaf(1.f - e[k][j], B[j], b) : b;
-        E[j] = k ? fmaf(-e[k][j], E[j], E[j]) + e[k][j] : e[k][j];
+        const float a1 = 1.f - e[k][j], b = glr_weight<TI>(e[k][j], a1) * (si[k][j] * x[j]);
+        B[j] = k ? fmaf(a1, B[j], b) : b;
+        E[j] = k ? fmaf(E[j], a1, e[k][j]) : e[k][j];
       }
     }
 #pragma unroll
@@ -521,7 +559,7 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       glr_cvt<TI, V>(kx[k], x);
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        hp[k + 1][j] = fmaf(1.f - e[k][j], hp[k][j], glr_weight<TI>(e[k][j]) * (si[k][j] * x[j]));
+        hp[k + 1][j] = fmaf(1.f - e[k][j], hp[k][j], glr_weight<TI>(e[k][j], 1.f - e[k][j]) * (si[k][j] * x[j]));
     }
     const auto tx = ox.rows(t, left(t)), tr = orr.rows(t, left(t)), ti = oi.rows(t, left(t));
 #pragma unroll
@@ -534,12 +572,17 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       for (int j = 0; j < V; ++j) {
         const float G = cg[j] + d[j], u = si[k][j] * x[j], L = rate[j] * sr[k][j], a1 = 1.f - e[k][j];
         float al = a1;  // a to its own last bits
-        if (deep && !(fresh && row == q.lo)) al = L < 0.25f ? a1 : glr_exp<TI>(L);
-        const float rw = glr_inv_weight<TI>(e[k][j]), du = e[k][j] * (2.f - e[k][j]) * rw * G;
+        if (deep && !(fresh && row == q.lo)) {
+          float y = L;
+          asm volatile("" : "+v"(y));
+          al = y < 0.25f ? a1 : glr_exp<TI>(y);
+        }
+        const float2 w = glr_weights<TI>(e[k][j], a1);
+        const float du = w.x * G;
         dx[j] = si[k][j] * du;
         di[j] = u * (1.f - si[k][j]) * du;
         // L dL; a and L first, whose product stays finite
-        const float LdL = (al * L) * G * fmaf(u * al, rw, -hp[k][j]);
+        const float LdL = (al * L) * G * fmaf(u * al, w.y, -hp[k][j]);
         dr[j] = LdL * (1.f - sr[k][j]);
         dl[j] += row < q.t1 ? LdL : 0.f;
         cg[j] = a1 * G;
@@ -591,35 +634,36 @@ template <typename TI> __global__ __launch_bounds__(64) void k_glr_decode(GlrArg
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float u = sigmoidf<TI>(i.v[j]) * x.v[j];
-    h.v[j] = fresh ? u : fmaf(-e[j], h.v[j], h.v[j]) + glr_weight<TI>(e[j]) * u;
+    h.v[j] = fresh ? u : fmaf(-e[j], h.v[j], h.v[j]) + glr_weight<TI>(e[j], 1.f - e[j]) * u;
   }
   st8<float>(st, h);
   st8<TI>((TI*)a.y + (int64_t)n * a.y_rs + c, h);
 }
 
 // ------------------------------------------------------------------ launches
-struct GlrPlan {
-  int seg, per, slots, cbn;
-  bool cut;  // some sequence may have more than one segment
-};
+// A workgroup that walks down its sequence reads everything once, but a single chain takes 2.7 us a tile (gates of 2 x
+// 64 x 64 values in eight waves, half of it exponentials, reciprocals and roots): 16384 tokens x 4096 channels by 64
+// workgroups 331 us, cut into eighths by 512 177 with the pass for their maps; 4 x 4096 x 2560 by 160 workgroups 97 us, cut
+// into quarters 80 + 75. So a sequence is cut, finely, where it is longer than its share of 128 workgroups.
 static GlrPlan glr_plan(const GlrArgs& a, int dtype) {
   GlrPlan p;
   const int CB = dtype == 0 ? 32 : 64;
-  p.cbn = (a.ch + CB - 1) / CB;
-  const int64_t longest = a.cu ? a.rows : a.T;
-  int64_t seg = (longest + GTILE - 1) / GTILE * GTILE;
-  if ((int64_t)p.cbn * a.N < 256 || a.cu) {
-    const int64_t want = ((int64_t)p.cbn * a.rows / 512 + GTILE - 1) / GTILE * GTILE;
-    const int64_t s = want < 512 ? 512 : want;
-    if (s < seg) seg = s;
-  }
-  if (seg < GTILE) seg = GTILE;
-  p.seg = (int)seg;
-  p.per = a.cu ? 0 : (int)((a.T + seg - 1) / seg);
-  if (!a.cu && p.per < 1) p.per = 1;
-  p.slots = a.cu ? (int)(a.rows / seg) + a.N : a.N * p.per;
-  p.cut = longest > seg;
+  p.blocks = (a.ch + CB - 1) / CB;
+  const int64_t longest = a.cu ? a.rows : a.T, work = a.rows * p.blocks;
+  auto tiles = [](int64_t t, int64_t least) {  // (a batch has up to 2^28 tokens)
+    return ((t < least ? least : t < 1 << 28 ? t : 1 << 28) + GTILE - 1) / GTILE * GTILE;
+  };
+  p.keep = (int)tiles(work / 128, 1024);
+  p.seg = (int)tiles(work / 512, 512);
+  p.cut = longest > p.keep;
+  if (!p.cut) p.seg = p.keep;
+  p.per = a.cu ? 0 : p.cut ? (int)((a.T + p.seg - 1) / p.seg) : 1;
+  p.slots = a.cu ? (int)(a.rows / p.seg) + a.N : a.N * p.per;
   return p;
+}
+int64_t glr_blocks(const GlrArgs& a, int dtype) {
+  const GlrPlan p = glr_plan(a, dtype);
+  return (int64_t)p.slots * p.blocks;
 }
 
 size_t glr_fwd_ws_bytes(const GlrArgs& a, int dtype) {
@@ -635,31 +679,31 @@ size_t glr_saved_bytes(const GlrArgs& a) { return ((size_t)(a.rows / GTILE) + a.
 
 template <typename TI> static hipError_t glr_forward(const GlrArgs& a, int dtype, hipStream_t s) {
   const GlrPlan p = glr_plan(a, dtype);
-  const unsigned grid = (unsigned)p.slots * (unsigned)p.cbn;
+  const unsigned grid = (unsigned)p.slots * (unsigned)p.blocks;
   if (grid == 0) return hipSuccess;
   if (p.cut) {
-    traced("k_glr_map", s, [&] { k_glr_map<TI, true><<<grid, GNT, 0, s>>>(a, p.seg, p.per); });
+    traced("k_glr_map", s, [&] { k_glr_map<TI, true><<<grid, GNT, 0, s>>>(a, p); });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   traced("k_glr_fwd", s, [&] {
-    if (a.sv) k_glr_fwd<TI, 4, true><<<grid, GNT, 0, s>>>(a, p.seg, p.per);
-    else k_glr_fwd<TI, 4, false><<<grid, GNT, 0, s>>>(a, p.seg, p.per);
+    if (a.sv) k_glr_fwd<TI, true><<<grid, GNT, 0, s>>>(a, p);
+    else k_glr_fwd<TI, false><<<grid, GNT, 0, s>>>(a, p);
   });
   return hipGetLastError();
 }
 
 template <typename TI> static hipError_t glr_backward(const GlrArgs& a, int dtype, hipStream_t s) {
   const GlrPlan p = glr_plan(a, dtype);
-  const unsigned grid = (unsigned)p.slots * (unsigned)p.cbn;
+  const unsigned grid = (unsigned)p.slots * (unsigned)p.blocks;
   hipError_t e = hipSuccess;
   if (p.cut && grid) {
-    traced("k_glr_map", s, [&] { k_glr_map<TI, false><<<grid, GNT, 0, s>>>(a, p.seg, p.per); });
+    traced("k_glr_map", s, [&] { k_glr_map<TI, false><<<grid, GNT, 0, s>>>(a, p); });
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   float* part = a.dlam ? a.ws + (p.cut ? (int64_t)p.slots * 2 * a.ch : 0) : nullptr;
-  if (grid) traced("k_glr_bwd", s, [&] { k_glr_bwd<TI><<<grid, GNT, 0, s>>>(a, p.seg, p.per, part); });
+  if (grid) traced("k_glr_bwd", s, [&] { k_glr_bwd<TI><<<grid, GNT, 0, s>>>(a, p, part); });
   e = hipGetLastError();
   if (e == hipSuccess && part) e = launch_colsum(part, p.slots, a.ch, ColsumOut{{a.dlam, nullptr, nullptr}}, 1, s);
   return e;

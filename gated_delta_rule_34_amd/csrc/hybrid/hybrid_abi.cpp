@@ -18,18 +18,6 @@ bool known_dtype(int d) { return d == GDN_F32 || d == GDN_BF16; }
 
 // ------------------------------------------------------------------ gated linear recurrence
 
-gdn_status check_glr(const gdn_glr_problem* p) {
-  if (!p || p->channels <= 0 || p->channels % 8) return GDN_EINVAL;
-  if (!known_dtype(p->dtype)) return GDN_EUNSUPPORTED;
-  if (!std::isfinite(p->rate) || p->rate <= 0.f) return GDN_EINVAL;
-  GDN_TRY(check_seqs(p->N, p->T, p->T_total, p->cu_seqlens));
-  // one workgroup of 512 threads per segment of at least 128 tokens and 32 or 64 channels; of a token, per row and 512
-  const int64_t cb = ((int64_t)p->channels + 31) / 32;
-  if (p->T_total / 128 + p->N + 1 > (kMaxBlocks / 2) / cb || p->channels / 512 >= 65535) return GDN_EINVAL;
-  GDN_TRY(check_arr(p->lambda, true, 16));
-  return check_arr(p->fresh, false);
-}
-
 gdn::GlrArgs glr_args(const gdn_glr_problem* p) {
   gdn::GlrArgs a{};
   a.N = p->N;
@@ -41,6 +29,18 @@ gdn::GlrArgs glr_args(const gdn_glr_problem* p) {
   a.lam = p->lambda;
   a.fresh = p->fresh;
   return a;
+}
+
+gdn_status check_glr(const gdn_glr_problem* p) {
+  if (!p || p->channels <= 0 || p->channels % 8) return GDN_EINVAL;
+  if (!known_dtype(p->dtype)) return GDN_EUNSUPPORTED;
+  if (!std::isfinite(p->rate) || p->rate <= 0.f) return GDN_EINVAL;
+  GDN_TRY(check_seqs(p->N, p->T, p->T_total, p->cu_seqlens));
+  GDN_TRY(check_arr(p->lambda, true, 16));
+  GDN_TRY(check_arr(p->fresh, false));
+  // launch limits: workgroups of 512 threads, and of a token per row and 512 channels
+  if (p->N > kMaxBlocks / 2 || p->channels / 512 >= 65535) return GDN_EINVAL;
+  return gdn::glr_blocks(glr_args(p), p->dtype) <= kMaxBlocks / 2 ? GDN_OK : GDN_EINVAL;
 }
 
 // A row view of the recurrence: its kernels address the 256 rows of a tile with 31-bit byte offsets.

@@ -5,6 +5,7 @@
 #include "hybrid/hybrid_internal.h"
 
 namespace gdn {
+int64_t glr_blocks(const GlrArgs& a, int) { return (a.rows / 512 + a.N) * ((a.ch + 31) / 32); }
 size_t glr_fwd_ws_bytes(const GlrArgs&, int) { return 4096; }
 size_t glr_bwd_ws_bytes(const GlrArgs&, int) { return 4096; }
 size_t glr_saved_bytes(const GlrArgs&) { return 4096; }

@@ -65,7 +65,7 @@ def test_recurrence_refusals(G):
                      (dict(rate=-1.0), E), (dict(rate=float("nan")), E), (dict(rate=float("inf")), E), (dict(N=-1), E), (dict(T=63), E),
                      (dict(T_total=-1), E), ({"lambda": None}, E), ({"lambda": A + 4}, L), (dict(fresh=A + 2), L), (dict(cu_seqlens=A + 2), L),
                      (dict(N=0, T_total=5, cu_seqlens=A), E), (dict(N=1, T=1 << 29, T_total=1 << 29), E), (dict(N=1 << 23, T=0, T_total=0), E),
-                     (dict(N=2**31 - 1, T=0, T_total=0), E), (dict(N=1, T=1 << 28, T_total=1 << 28), E), (dict(channels=2**31 - 8), E)):
+                     (dict(N=2**31 - 1, T=0, T_total=0), E), (dict(N=1 << 21, T=0, T_total=0), E), (dict(channels=2**31 - 8), E)):
         p = glr(G, **kw)
         assert glr_fwd(G, p) == want, kw
         assert glr_bwd(G, p) == want, kw

@@ -94,23 +94,10 @@ template <typename TI, int V> __device__ __forceinline__ void one_minus_exp(cons
   }
 }
 
-// w = sqrt(1 - a^2) = sqrt(e (1 + a)) of e and a1 = 1 - e. A w below 2^-63, whose square no float32 holds in full, may
-// come out as less.
-template <typename TI> __device__ __forceinline__ float glr_weight(float e, float a1) {
-  const float w2 = fmaf(e, a1, e);
-  if constexpr (sizeof(TI) == 2) return __builtin_amdgcn_sqrtf(w2);
-  else return sqrtf(w2);
-}
-// The same and 1 / w, which ends at 2^63 (L / w is then zero where L is).
-template <typename TI> __device__ __forceinline__ float2 glr_weights(float e, float a1) {
-  const float w2 = fmaf(e, a1, e), c = fmaxf(w2, 0x1p-126f);
-  if constexpr (sizeof(TI) == 2) {
-    const float r = __builtin_amdgcn_rsqf(c);
-    return float2{w2 * r, r};
-  } else {
-    return float2{sqrtf(w2), 1.f / sqrtf(c)};
-  }
-}
+// w = sqrt(1 - a^2) = sqrt(e (1 + a)) of e and a1 = 1 - e, by the hardware's root (1 ulp), and 1 / w, which ends at 2^63 (L / w
+// is then zero where L is). A w below 2^-63, whose square no float32 holds in full, may come out as less.
+__device__ __forceinline__ float glr_weight(float e, float a1) { return __builtin_amdgcn_sqrtf(fmaf(e, a1, e)); }
+__device__ __forceinline__ float glr_inv_weight(float e, float a1) { return __builtin_amdgcn_rsqf(fmaxf(fmaf(e, a1, e), 0x1p-126f)); }
 
 // x of the lane that CTRL names, zero where it lies outside the row of 16 (e = 0, b = 0: the map that changes nothing).
 template <int CTRL> __device__ __forceinline__ float dpp_or0(float x) {
@@ -295,7 +282,7 @@ template <typename TI, bool FWD> __global__ __launch_bounds__(GNT) void k_glr_ma
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float a1 = 1.f - e[j];
-      if constexpr (FWD) B[j] = fmaf(a1, B[j], glr_weight<TI>(e[j], a1) * (sigmoidf<TI>(iv[j]) * x[j]));
+      if constexpr (FWD) B[j] = fmaf(a1, B[j], glr_weight(e[j], a1) * (sigmoidf<TI>(iv[j]) * x[j]));
       else B[j] = a1 * (B[j] + x[j]);
       E[j] = fmaf(E[j], a1, e[j]);
     }
@@ -379,7 +366,7 @@ template <typename TI, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_f
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         a1[k][j] = 1.f - e[j];
-        b[k][j] = glr_weight<TI>(e[j], a1[k][j]) * (sigmoidf<TI>(i[j]) * x[j]);
+        b[k][j] = glr_weight(e[j], a1[k][j]) * (sigmoidf<TI>(i[j]) * x[j]);
         B[j] = k ? fmaf(a1[k][j], B[j], b[k][j]) : b[k][j];
         E[j] = k ? fmaf(E[j], a1[k][j], e[j]) : e[j];
       }
@@ -466,7 +453,7 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
     float hs = 0.f;  // wave 0: the tile's saved start
     if (wave_id() == 0 && mine) hs = a.sv[((q.lo / GTILE) + q.n + (t - q.lo) / GTILE) * a.ch + ci];
     const bool plain = t + GTILE <= q.t1 && !(fresh && t == q.lo);
-    float e[GK][V], sr[GK][V], si[GK][V], E[V], B[V], Ex[V], Bx[V], F[V], C[V], Fx[V], Cx[V];
+    float e[GK][V], sr[GK][V], si[GK][V], rw[GK][V], E[V], B[V], Ex[V], Bx[V], F[V], C[V], Fx[V], Cx[V];
     i32x4 kx[GK], kd[GK];
 #pragma unroll
     for (int k = 0; k < GK; ++k) {
@@ -496,7 +483,9 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float a1 = 1.f - e[k][j], b = glr_weight<TI>(e[k][j], a1) * (si[k][j] * x[j]);
+        const float a1 = 1.f - e[k][j];
+        rw[k][j] = glr_inv_weight(e[k][j], a1);
+        const float b = fmaf(e[k][j], a1, e[k][j]) * rw[k][j] * (si[k][j] * x[j]);
         B[j] = k ? fmaf(a1, B[j], b) : b;
         E[j] = k ? fmaf(E[j], a1, e[k][j]) : e[k][j];
       }
@@ -544,7 +533,7 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
     for (int k = 0; k < GK; ++k) {
       asm volatile("" : "+v"(kx[k]), "+v"(kd[k]));
 #pragma unroll
-      for (int j = 0; j < V; ++j) asm volatile("" : "+v"(e[k][j]), "+v"(sr[k][j]), "+v"(si[k][j]));
+      for (int j = 0; j < V; ++j) asm volatile("" : "+v"(e[k][j]), "+v"(sr[k][j]), "+v"(si[k][j]), "+v"(rw[k][j]));
     }
     float hp[GK][V], cg[V];  // the state in front of each token, the gradient from behind
 #pragma unroll
@@ -559,7 +548,7 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       glr_cvt<TI, V>(kx[k], x);
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        hp[k + 1][j] = fmaf(1.f - e[k][j], hp[k][j], glr_weight<TI>(e[k][j], 1.f - e[k][j]) * (si[k][j] * x[j]));
+        hp[k + 1][j] = fmaf(1.f - e[k][j], hp[k][j], fmaf(e[k][j], 1.f - e[k][j], e[k][j]) * rw[k][j] * (si[k][j] * x[j]));
     }
     const auto tx = ox.rows(t, left(t)), tr = orr.rows(t, left(t)), ti = oi.rows(t, left(t));
 #pragma unroll
@@ -577,12 +566,11 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
           asm volatile("" : "+v"(y));
           al = y < 0.25f ? a1 : glr_exp<TI>(y);
         }
-        const float2 w = glr_weights<TI>(e[k][j], a1);
-        const float du = w.x * G;
+        const float du = fmaf(e[k][j], a1, e[k][j]) * rw[k][j] * G;
         dx[j] = si[k][j] * du;
         di[j] = u * (1.f - si[k][j]) * du;
         // L dL; a and L first, whose product stays finite
-        const float LdL = (al * L) * G * fmaf(u * al, w.y, -hp[k][j]);
+        const float LdL = (al * L) * G * fmaf(u * al, rw[k][j], -hp[k][j]);
         dr[j] = LdL * (1.f - sr[k][j]);
         dl[j] += row < q.t1 ? LdL : 0.f;
         cg[j] = a1 * G;
@@ -634,7 +622,7 @@ template <typename TI> __global__ __launch_bounds__(64) void k_glr_decode(GlrArg
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float u = sigmoidf<TI>(i.v[j]) * x.v[j];
-    h.v[j] = fresh ? u : fmaf(-e[j], h.v[j], h.v[j]) + glr_weight<TI>(e[j], 1.f - e[j]) * u;
+    h.v[j] = fresh ? u : fmaf(-e[j], h.v[j], h.v[j]) + glr_weight(e[j], 1.f - e[j]) * u;
   }
   st8<float>(st, h);
   st8<TI>((TI*)a.y + (int64_t)n * a.y_rs + c, h);

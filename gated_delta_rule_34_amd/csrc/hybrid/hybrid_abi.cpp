@@ -64,7 +64,7 @@ gdn_status check_rope(const gdn_qk_rope_problem* p) {
   if (!p || p->rows < 0 || p->Hq <= 0 || p->Hk <= 0 || p->D <= 0 || p->rot < 0 || p->rot > p->D) return GDN_EINVAL;
   if (!known_dtype(p->dtype) || p->D > 256 || p->D % 16 || p->rot % 16) return GDN_EUNSUPPORTED;
   const int64_t heads = (int64_t)p->Hq + 2 * (int64_t)p->Hk;
-  if (heads > INT32_MAX / 1024 || p->rows > INT32_MAX / heads || p->rows > kMaxBlocks * 4) return GDN_EINVAL;
+  if (heads > INT32_MAX / 1024 || p->rows > INT32_MAX / heads || p->rows > kMaxBlocks * 2) return GDN_EINVAL;
   if (!std::isfinite(p->eps) || p->eps < 0.f || !std::isfinite(p->rope_scale)) return GDN_EINVAL;
   const bool turned = p->rot > 0 && p->rows > 0;
   GDN_TRY(check_arr(p->positions, turned));

@@ -16,7 +16,7 @@
 namespace gdn {
 
 constexpr int RNT = 256;
-constexpr int RROWS = 4;  // rows of a workgroup at the most
+constexpr int RROWS = 2;  // rows of a workgroup at the most
 
 // (cos, sin) of the angle pos f, times scale. The quarter turn that is nearest leaves at most pi / 4, whose series
 // end with z^5 (2e-8 of the sum).
@@ -102,6 +102,7 @@ __device__ __forceinline__ F8 rope_weight(const float* w, int c, bool live) {
 template <typename TI, int LH, bool ADJ, bool CACHE> __global__ __launch_bounds__(RNT) void k_rope_fwd(RopeArgs a, int rb) {
 #pragma clang fp contract(off)
   __shared__ float2 cs[RROWS * 128];
+  __shared__ int64_t rows_at[RROWS];  // of a row's first key head among the pool's rows, or -1: not cached
   const RopePlace me(LH, a.D, a.R, ADJ);
   const int64_t row0 = (int64_t)blockIdx.x * rb;
   const int nrows = (int)(a.rows - row0 < rb ? a.rows - row0 : rb);
@@ -124,6 +125,11 @@ template <typename TI, int LH, bool ADJ, bool CACHE> __global__ __launch_bounds_
     oq = rope_weight(a.wq, me.c + me.away * 8, me.live);
     ok = rope_weight(a.wk, me.c + me.away * 8, me.live);
   }
+  if (CACHE && (int)threadIdx.x < nrows) {
+    const int64_t w = a.where[row0 + threadIdx.x];
+    const uint32_t page = (uint32_t)w / (uint32_t)a.page;
+    rows_at[threadIdx.x] = w < 0 || w >= a.places ? -1 : (int64_t)page * a.Hk * a.page + (w - (int64_t)page * a.page);
+  }
   rope_angles(a, row0, nrows, cs);
   __syncthreads();
   for (; it < items; it += SLOTS) {
@@ -134,11 +140,9 @@ template <typename TI, int LH, bool ADJ, bool CACHE> __global__ __launch_bounds_
     const bool key = h >= a.Hq;
     int64_t place = 0;
     if (CACHE && key) {
-      place = a.where[t];
-      if (place < 0 || place >= a.places) continue;  // (a head's lanes together)
-      const int hk = h - a.Hq - (h >= a.Hq + a.Hk ? a.Hk : 0);
-      const uint32_t page = (uint32_t)place / (uint32_t)a.page;
-      place = ((int64_t)page * a.Hk + hk) * a.page + (place - (int64_t)page * a.page);
+      place = rows_at[row];
+      if (place < 0) continue;  // (a head's lanes together)
+      place += (int64_t)(h - a.Hq - (h >= a.Hq + a.Hk ? a.Hk : 0)) * a.page;
       if (h >= a.Hq + a.Hk) {
         if (me.live) straw8<TI>((TI*)a.vp + place * a.D + me.c, raw);
         continue;
@@ -279,8 +283,9 @@ template <typename TI, int LH, bool ADJ> __global__ __launch_bounds__(RNT) void 
 }
 
 // ------------------------------------------------------------------ launches
-// Rows of a workgroup: several share nothing but their launch, one spreads small batches.
-static int rope_rows(const RopeArgs& a) { return a.rows >= 4096 ? RROWS : 1; }
+// Rows of a workgroup: two keep more loads in flight (16384 rows of 28 heads of 256: forward 87 us, backward 126; with one 90
+// and 135, with four 92 and 131), one spreads small batches.
+static int rope_rows(const RopeArgs& a) { return a.rows >= 2048 ? RROWS : 1; }
 static int rope_bwd_grid(const RopeArgs& a) {
   const int64_t blocks = (a.rows + rope_rows(a) - 1) / rope_rows(a);
   return (int)(blocks < 2048 ? (blocks < 1 ? 1 : blocks) : 2048);

@@ -121,6 +121,15 @@ def test_sequences_cut_into_segments(dtype, lens, C, cu):
     check(v, g, dtype, cu=cu)
 
 
+def test_many_sequences():
+    """More than 256 of them, two long enough to be cut."""
+    rng = np.random.default_rng(36)
+    lens = [int(v) for v in rng.integers(0, 12, 300)]
+    lens[40], lens[299] = 2100, 1500
+    v, g = case(lens, 16, "f32", 37)
+    check(v, g, "f32")
+
+
 def test_forward_without_backward_and_parts_skipped():
     import torch
     import gated_delta_rule_34_amd as G
@@ -230,16 +239,16 @@ def test_rows_of_no_sequence_stay():
     import torch
     import gated_delta_rule_34_amd as G
 
-    for C, T in ((64, 300), (8, 2600)):
+    for C, T in ((64, 300), (8, 5000)):
         x, r, i, dy = (torch.randn(T, C, device="cuda") for _ in range(4))
         lam = torch.zeros(C, device="cuda")
-        for cu, touched in (([40, 100, T - 50], (40, T - 50)), ([0, T // 2, T * 4], None), ([0, T, 5], None), ([-7, T // 3, -9], None)):
-            p = G.make_glr_problem(2, T, C, lam=lam, cu_seqlens=i32(cu), dtype="f32")
+        for cu, touched in (([40, 100, T - 50], (40, T - 50)), ([0, T // 2, T * 4], None), ([0, T, 5], None), ([-7, T // 3, -9], None), ([0, T, 5, T, 0, T], None)):
+            p = G.make_glr_problem(len(cu) - 1, T, C, lam=lam, cu_seqlens=i32(cu), dtype="f32")
             outs = [torch.full((T, C), 7.0, device="cuda") for _ in range(4)]
             saved = torch.zeros(G.gdn_glr_state_bytes(p), dtype=torch.uint8, device="cuda")
             ws = torch.zeros(max(G.gdn_glr_fwd_workspace_bytes(p), G.gdn_glr_bwd_workspace_bytes(p)), dtype=torch.uint8, device="cuda")
-            G.gdn_glr_fwd(p, x, r, i, None, outs[0], torch.empty(2, C, device="cuda"), saved, ws)
-            G.gdn_glr_bwd(p, x, r, i, saved, dy, None, *outs[1:], torch.empty(C, device="cuda"), torch.empty(2, C, device="cuda"), ws)
+            G.gdn_glr_fwd(p, x, r, i, None, outs[0], torch.empty(p.N, C, device="cuda"), saved, ws)
+            G.gdn_glr_bwd(p, x, r, i, saved, dy, None, *outs[1:], torch.empty(C, device="cuda"), torch.empty(p.N, C, device="cuda"), ws)
             torch.cuda.synchronize()
             if touched:
                 for o in outs:
@@ -258,6 +267,10 @@ def test_no_tokens():
         g = G.glr_backward(p, x, x, x, saved, x, dhT)
         keep = torch.tensor([1, 0, 1][:N], device="cuda")[:, None]
         assert torch.equal(hT, h0 * keep) and torch.equal(g["dh0"], dhT * keep) and not g["dlam"].any()
+        if N == 0:  # without a workspace
+            dlam = torch.full((16,), 3.0, device="cuda")
+            G.gdn_glr_bwd(p, x, x, x, None, x, None, x, x, x, dlam, None, None)
+            assert not dlam.any()
 
 
 def test_continued_prompt_and_tokens_follow_the_whole():

@@ -43,9 +43,9 @@ gdn_status check_glr(const gdn_glr_problem* p) {
   return gdn::glr_blocks(glr_args(p), p->dtype) <= kMaxBlocks / 2 ? GDN_OK : GDN_EINVAL;
 }
 
-// A row view of the recurrence: its kernels address the 256 rows of a tile with 31-bit byte offsets.
+// A row view of the recurrence: its kernels address the rows of two tiles of 128 with 31-bit byte offsets.
 gdn_status glr_view(const gdn_glr_problem* p, const void* v, int64_t rs) {
-  if (p->T_total > 0 && rs * esize(p->dtype) >= (int64_t)1 << 23) return GDN_EINVAL;
+  if (p->T_total > 0 && rs >= ((int64_t)1 << 23) / esize(p->dtype)) return GDN_EINVAL;
   return check_view(v, rs, p->channels, p->dtype, p->T_total);
 }
 
@@ -126,7 +126,7 @@ gdn_status check_paged(const gdn_paged_problem* p) {
   GDN_TRY(check_pool(p->n_pages, p->page_size, p->Hk));
   if (p->max_pages < 0 || p->max_pages > INT32_MAX / p->page_size) return GDN_EINVAL;
   if (p->max_len < 0 || p->max_len > p->max_pages * p->page_size || p->window < 0 || !std::isfinite(p->scale)) return GDN_EINVAL;
-  if (p->max_len > INT32_MAX - (1 << 20)) return GDN_EINVAL;  // tokens past a chunk's end are counted too
+  if (p->max_len > 1 << 30) return GDN_EINVAL;  // tokens past a chunk's end are counted in 31 bits too
   // launch limits: a workgroup per query head and sequence, and per chunk of a key head
   if ((int64_t)p->N * p->Hq > kMaxBlocks || gdn::paged_blocks(paged_args(p), p->dtype) > kMaxBlocks) return GDN_EINVAL;
   GDN_TRY(check_arr(p->page_table, p->N > 0 && p->max_len > 0));

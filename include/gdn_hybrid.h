@@ -8,7 +8,10 @@
  * kernels on `stream` (of the current device), row views with strides in elements and 16-byte aligned
  * address and stride, contiguous arrays named [..], checks on the host before anything is enqueued.
  * Malformed cu_seqlens, slots, page tables or lengths give wrong results but no access outside the
- * caller's buffers. Results are the same bits on every run (no atomics).
+ * caller's buffers. Results are the same bits on every run (no atomics). Rows of no sequence are left as they
+ * were. A NaN stays in its channel and sequence (and its channel of dlambda), in its row and
+ * head (and dwq or dwk), or in its sequence and the query heads that read it. Calls that may run at the same time need workspaces of
+ * their own.
  */
 #ifndef GDN_HYBRID_H
 #define GDN_HYBRID_H
@@ -140,7 +143,7 @@ typedef struct {
   int32_t page_size;   /* tokens per page (>= 1) */
   int32_t n_pages;     /* pages of the pool (>= 0); n_pages * page_size * Hk < 2^32, n_pages * page_size < 2^31 */
   int32_t max_pages;   /* entries per row of page_table; max_pages * page_size < 2^31 */
-  int32_t max_len;     /* upper bound of lens, 0 .. max_pages * page_size: sizes the launch */
+  int32_t max_len;     /* upper bound of lens, 0 .. max_pages * page_size, up to 2^30: sizes the launch */
   int32_t window;      /* tokens seen, or 0 = all */
   float scale;         /* finite */
   int32_t dtype;       /* gdn_dtype of q, out and the pages */

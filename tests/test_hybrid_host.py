@@ -74,6 +74,8 @@ def test_recurrence_refusals(G):
     assert glr_fwd(G, p, x=(None, 256)) == E and glr_fwd(G, p, r=(A, 255)) == E and glr_fwd(G, p, y=(A * 2, 260)) == L
     assert glr_fwd(G, p, i=(A + 8, 256)) == L and glr_fwd(G, p, x=(A, 1 << 60)) == E and glr_fwd(G, p, y=(A, 512)) == E
     assert glr_fwd(G, p, h0=A + 4) == L and glr_fwd(G, p, hT=A + 8) == L and glr_fwd(G, p, h0=A, hT=A) == E and glr_fwd(G, p, sv=A + 4) == L
+    for rs in (1 << 22, 1 << 61, 1 << 62, -8):
+        assert glr_fwd(G, p, x=(A, rs)) == E and glr_bwd(G, p, dy=(A, rs)) == E
     one = glr(G, N=1, T=1 << 16, T_total=1 << 16)
     need = G.gdn_glr_fwd_workspace_bytes(one)  # one sequence of few channels is cut into segments
     assert need > 0 and glr_fwd(G, one, ws=(None, 0)) == W and glr_fwd(G, one, ws=(A, need - 1)) == W and glr_fwd(G, one, ws=(A + 16, need)) == L
@@ -145,7 +147,7 @@ def test_attention_refusals(G):
                      (dict(max_len=81), E), (dict(max_len=-1), E), (dict(window=-1), E), (dict(scale=float("nan")), E), (dict(page_table=None), E),
                      (dict(lens=None), E), (dict(page_table=A + 2), L), (dict(lens=A + 1), L), (dict(N=1 << 24), E),
                      (dict(Hk=8, n_pages=1 << 29, page_size=2), E), (dict(N=1 << 21), E),
-                     (dict(N=1, max_pages=2**27 - 1, max_len=2**31 - 16), E)):
+                     (dict(N=1, max_pages=2**27 - 1, max_len=2**31 - 16), E), (dict(N=1, max_pages=2**27 - 1, max_len=2**30 + 1), E)):
         p = paged(G, **kw)
         assert run(p) == want, kw
         assert G.gdn_paged_attn_workspace_bytes(p) == 0

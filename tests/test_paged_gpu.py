@@ -95,6 +95,22 @@ def test_long_ones_are_split_and_joined(dtype, D, page):
     assert G.gdn_paged_attn_workspace_bytes(p) > 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_sequences(dtype):
+    """More than 256 of them: all of one chunk, and of several."""
+    import gated_delta_rule_34_amd as G
+
+    lens = [int(v) for v in np.random.default_rng(68).integers(0, 90, 300)]
+    _, _, p = check(case(lens, 3, 1, 32, 16, dtype, 68), dtype)
+    assert G.gdn_paged_attn_workspace_bytes(p) == 0
+    lens[7], lens[299], lens[130] = 700, 650, 256
+    c = case(lens, 3, 1, 32, 16, dtype, 69)
+    _, _, p = check(c, dtype)
+    assert G.gdn_paged_attn_workspace_bytes(p) > 0
+    check(c, dtype, window=300)
+    check(case(lens, 2, 2, 64, 20, dtype, 69), dtype)
+
+
 @pytest.mark.parametrize("window", [1, 15, 16, 17, 100, 255, 512, 5000])
 def test_window(window):
     for page in (16, 10):

@@ -231,14 +231,13 @@ __device__ __forceinline__ bool glr_seg(const GlrArgs& a, const GlrPlan& p, int 
   const bool on = c0 + me.cg * V < a.ch;                                                 \
   const int c = on ? c0 + me.cg * V : 0, ci = c0 + lane_id();                            \
   const bool mine = lane_id() < CB && ci < a.ch /* a channel of the scanning waves */
+// Rates of a thread's channels, each found by one lane of the wave; a lane of no channel has that of the last.
 #define GLR_RATES                                                                        \
+  const int cl = c0 + lane_id() % CB;                                                    \
+  const float its = glr_rate(a.rate, a.lam[cl < a.ch ? cl : a.ch - 1]);                  \
   float rate[V];                                                                         \
-  bool deep = false;                                                                     \
-  _Pragma("unroll") for (int j = 0; j < V; ++j) {                                        \
-    rate[j] = glr_rate(a.rate, a.lam[c + j]);                                            \
-    deep |= !(rate[j] < 0.25f);                                                          \
-  }                                                                                      \
-  deep = __any(deep)
+  _Pragma("unroll") for (int j = 0; j < V; ++j) rate[j] = __shfl(its, me.cg * V + j);    \
+  const bool deep = __any(!(its < 0.25f))
 
 // ------------------------------------------------------------------ maps of segments
 // The map of each segment that another one continues from: forward every one but a sequence's last, backward
@@ -644,8 +643,8 @@ static GlrPlan glr_plan(const GlrArgs& a, int dtype) {
   auto tiles = [](int64_t t, int64_t least) {  // (a batch has up to 2^28 tokens)
     return ((t < least ? least : t < 1 << 28 ? t : 1 << 28) + GTILE - 1) / GTILE * GTILE;
   };
-  p.keep = (int)tiles(work / 128, 1024);
-  p.seg = (int)tiles(work / 512, 512);
+  p.keep = (int)tiles(work / 128, 512);
+  p.seg = (int)tiles(work / 512, 256);
   p.cut = longest > p.keep;
   if (!p.cut) p.seg = p.keep;
   p.per = a.cu ? 0 : p.cut ? (int)((a.T + p.seg - 1) / p.seg) : 1;

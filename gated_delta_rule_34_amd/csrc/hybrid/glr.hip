@@ -230,11 +230,12 @@ __device__ __forceinline__ bool glr_seg(const GlrArgs& a, const GlrPlan& p, int 
   const GlrLane me;                                                                      \
   const bool on = c0 + me.cg * V < a.ch;                                                 \
   const int c = on ? c0 + me.cg * V : 0, ci = c0 + lane_id();                            \
-  const bool mine = lane_id() < CB && ci < a.ch /* a channel of the scanning waves */
+  const bool mine = lane_id() < CB && ci < a.ch; /* a channel of the scanning waves */   \
+  const int cl = c0 + lane_id() % CB;                                                    \
+  const float lam = a.lam[cl < a.ch ? cl : a.ch - 1]
 // Rates of a thread's channels, each found by one lane of the wave; a lane of no channel has that of the last.
 #define GLR_RATES                                                                        \
-  const int cl = c0 + lane_id() % CB;                                                    \
-  const float its = glr_rate(a.rate, a.lam[cl < a.ch ? cl : a.ch - 1]);                  \
+  const float its = glr_rate(a.rate, lam);                                               \
   float rate[V];                                                                         \
   _Pragma("unroll") for (int j = 0; j < V; ++j) rate[j] = __shfl(its, me.cg * V + j);    \
   const bool deep = __any(!(its < 0.25f))
@@ -318,16 +319,6 @@ template <typename TI, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_f
   GLR_PLACE;
   __shared__ float sE[GE][CB], sB[GE][CB], sh[GE][CB];
   if (!glr_seg(a, pl, slot, q)) return;
-  GLR_RATES;
-  const bool fresh = a.fresh && a.fresh[q.n] != 0;
-  float h = 0.f;  // wave 0: the carried state of channel ci
-  if (wave_id() == 0 && mine) {
-    h = fresh || !a.h0 ? 0.f : a.h0[(int64_t)q.n * a.ch + ci];
-    for (int s = slot - q.k; s < slot; ++s) {
-      const float* m = a.ws + (int64_t)s * 2 * a.ch + ci;
-      h = fmaf(-m[0], h, h) + m[a.ch];
-    }
-  }
   const GlrView<TI> vx(a.x, a.x_rs, on, me.tt * GK, c), vr(a.r, a.r_rs, on, me.tt * GK, c), vi(a.i, a.i_rs, on, me.tt * GK, c),
       vy(a.y, a.y_rs, on, me.tt * GK, c);
   auto left = [&](int64_t t) { return (int)(q.t1 - t < GTILE ? q.t1 - t : GTILE); };
@@ -343,6 +334,16 @@ template <typename TI, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_f
     }
   };
   if (q.t0 < q.t1) load(q.t0);
+  GLR_RATES;
+  const bool fresh = a.fresh && a.fresh[q.n] != 0;
+  float h = 0.f;  // wave 0: the carried state of channel ci
+  if (wave_id() == 0 && mine) {
+    h = fresh || !a.h0 ? 0.f : a.h0[(int64_t)q.n * a.ch + ci];
+    for (int s = slot - q.k; s < slot; ++s) {
+      const float* m = a.ws + (int64_t)s * 2 * a.ch + ci;
+      h = fmaf(-m[0], h, h) + m[a.ch];
+    }
+  }
   for (int64_t t = q.t0; t < q.t1; t += GTILE) {
     float a1[GK][V], b[GK][V], E[V], B[V], Ex[V], Bx[V];  // a1 = 1 - e: what a map does to the tokens of this thread alone
     const bool plain = t + GTILE <= q.t1 && !(fresh && t == q.lo);
@@ -418,17 +419,6 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
     if (part && wave_id() == 0 && mine) part[(int64_t)slot * a.ch + ci] = 0.f;
     return;
   }
-  GLR_RATES;
-  const bool fresh = a.fresh && a.fresh[q.n] != 0;
-  float cc = 0.f;  // wave 1: the gradient that flows into the tile's end
-  if (wave_id() == 1 && mine) {
-    cc = a.dhT ? a.dhT[(int64_t)q.n * a.ch + ci] : 0.f;
-    const int end = slot - q.k + q.segs;  // (of sequences that overlap, in a malformed table, more than the slots hold)
-    for (int s = (end < pl.slots ? end : pl.slots) - 1; s > slot; --s) {
-      const float* m = a.ws + (int64_t)s * 2 * a.ch + ci;
-      cc = fmaf(-m[0], cc, cc) + m[a.ch];
-    }
-  }
   const GlrView<TI> vx(a.x, a.x_rs, on, me.tt * GK, c), vr(a.r, a.r_rs, on, me.tt * GK, c), vi(a.i, a.i_rs, on, me.tt * GK, c),
       vd(a.dy, a.dy_rs, on, me.tt * GK, c), ox(a.dx, a.dx_rs, on, me.tt * GK, c), orr(a.dr, a.dr_rs, on, me.tt * GK, c),
       oi(a.di, a.di_rs, on, me.tt * GK, c);
@@ -445,11 +435,22 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       rd[k] = vd.load(sd, k);
     }
   };
+  const int64_t tiles = (q.t1 - q.t0 + GTILE - 1) / GTILE;
+  if (tiles) load(q.t0 + (tiles - 1) * GTILE);
+  GLR_RATES;
+  const bool fresh = a.fresh && a.fresh[q.n] != 0;
+  float cc = 0.f;  // wave 1: the gradient that flows into the tile's end
+  if (wave_id() == 1 && mine) {
+    cc = a.dhT ? a.dhT[(int64_t)q.n * a.ch + ci] : 0.f;
+    const int end = slot - q.k + q.segs;  // (of sequences that overlap, in a malformed table, more than the slots hold)
+    for (int s = (end < pl.slots ? end : pl.slots) - 1; s > slot; --s) {
+      const float* m = a.ws + (int64_t)s * 2 * a.ch + ci;
+      cc = fmaf(-m[0], cc, cc) + m[a.ch];
+    }
+  }
   float dl[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) dl[j] = 0.f;
-  const int64_t tiles = (q.t1 - q.t0 + GTILE - 1) / GTILE;
-  if (tiles) load(q.t0 + (tiles - 1) * GTILE);
   for (int64_t tile = tiles - 1; tile >= 0; --tile) {
     const int64_t t = q.t0 + tile * GTILE;
     float hs = 0.f;  // wave 0: the tile's saved start

@@ -16,10 +16,10 @@
 //
 // Every element is read and written once where one workgroup takes a whole sequence; where that
 // leaves compute units idle, sequences are cut into segments, whose maps an extra pass over the inputs
-// finds first. Measured (bf16): 4 x 4096 tokens x 2560 forward 98 us, backward 174 us, bound by the gates (five
+// finds first. Measured (bf16): 4 x 4096 tokens x 2560 forward 95 us, backward 167 us, bound by the gates (five
 // instructions of a quarter of the rate and some 30 others a value, in the 160 compute units that have a workgroup); one prompt of
-// 16384 x 4096 82 us for the maps and 97 for the states, bound by HBM (4.9 and 5.5 TB/s); float32 in
-// 1336 ragged tokens x 1032 25 and 35 us, a chain of 7 tiles. 256 rows x 2560 of one token 6.8 us.
+// 16384 x 4096 77 us for the maps and 91 for the states, bound by HBM (5.2 and 5.9 TB/s); float32, 1336
+// ragged tokens x 1032, 8 us for the maps, 18 forward and 22 backward: the latency of a few tiles one after the other.
 #include "../gdn_common.h"
 #include "../layer/rows.h"
 #include "../layer/vec8.h"
@@ -641,8 +641,10 @@ template <typename TI> __global__ __launch_bounds__(64) void k_glr_decode(GlrArg
 // ------------------------------------------------------------------ launches
 // A workgroup that walks down its sequence reads everything once, but a single chain takes 2.7 us a tile (gates of 2 x
 // 64 x 64 values in eight waves, half of it exponentials, reciprocals and roots): 16384 tokens x 4096 channels by 64
-// workgroups 331 us, cut into eighths by 512 177 with the pass for their maps; 4 x 4096 x 2560 by 160 workgroups 97 us, cut
-// into quarters 80 + 75. So a sequence is cut, finely, where it is longer than its share of 128 workgroups.
+// workgroups 331 us, cut into eighths by 512 169 with the pass for their maps; 4 x 4096 x 2560 by 160 workgroups 95 us, cut
+// into quarters 80 + 75. So a sequence is cut, finely, where it is longer than its share of 128 workgroups, down to two tiles
+// (a training step of 1024 x 2560, whole 73 us, by two tiles 51; of 3800 float32 tokens x 512, by two tiles 43, by one 50) but
+// not up to 512 tokens (500 and 300 tokens x 2560 44 us, with 256 for 512 42, one prompt of 300 x 1024 12.8 and 17.7).
 static GlrPlan glr_plan(const GlrArgs& a, int dtype) {
   GlrPlan p;
   const int CB = dtype == 0 ? 32 : 64;

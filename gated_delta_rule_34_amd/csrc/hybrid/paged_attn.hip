@@ -393,15 +393,18 @@ template <typename TI, int D, int SG> __global__ __launch_bounds__(256) void k_p
 // Chunks: as many as the chip holds workgroups at once, so that equal ones end together (one sequence of 131072 tokens, 4 heads
 // of 256: 93 us with 512 of them, 99 with 1024, 114 with 2048), and four more for every sequence, whose last chunks are
 // of unequal lengths (64 sequences of up to 8192 tokens, 8 heads of 128: 217 us with 1024, 195 with 2048, 190 with
-// 4096). None of less than 128 tokens, two tiles for each wave.
+// 4096). None of less than 128 tokens, two tiles for each wave. A launch for the join is not worth it for a few tiles more: up to
+// 512 tokens (256 of heads past 256 bytes) are one chunk (64 sequences of up to 500 tokens, 8 heads of 128: 23 us, with a join 26; 16
+// of 300, heads of 64: 12 and 17; one of 500: 14 and 17; but one of 1000 24 and 17, 9 of 500, heads of 256: 25 and 17).
 static PagedPlan paged_plan(const PagedArgs& a, int dtype) {
   PagedPlan p;
   p.gt = (a.Hq / a.Hk + 15) / 16;
   const int64_t span = a.window > 0 && a.window < a.max_len ? (int64_t)a.window + PT - 1 : a.max_len;
-  const int64_t heads = (int64_t)a.Hk * p.gt, full = 256 * paged_resident(a.D * (dtype == 0 ? 4 : 2));
+  const int head_bytes = a.D * (dtype == 0 ? 4 : 2);
+  const int64_t heads = (int64_t)a.Hk * p.gt, full = 256 * paged_resident(head_bytes), one = head_bytes <= 256 ? 512 : 256;
   const int64_t want = (full + heads - 1) / heads + 4 * (int64_t)a.N;
   constexpr int least = 128;
-  p.even = a.N <= kPagedEven && span > least;
+  p.even = a.N <= kPagedEven && span > one;
   if (p.even) {
     const int64_t most = a.N * ((span + least - 1) / least);
     p.chunk = least;
@@ -409,7 +412,7 @@ static PagedPlan paged_plan(const PagedArgs& a, int dtype) {
     p.slots = (int)(want < most ? want : most) + a.N;
   } else {
     const int64_t each = (want + a.N - 1) / (a.N > 0 ? a.N : 1);
-    int64_t chunk = (span + each - 1) / each;
+    int64_t chunk = span <= one ? span : (span + each - 1) / each;
     chunk = chunk < least ? least : (chunk + PT * PW - 1) / (PT * PW) * (PT * PW);
     p.chunk = (int)(chunk < (1 << 30) ? chunk : 1 << 30);
     p.splits = span > 0 ? (int)((span + p.chunk - 1) / p.chunk) : 1;

@@ -13,6 +13,7 @@ import math
 
 import numpy as np
 import pytest
+import torch  # noqa: F401  (in front of the package, which then has torch's HIP runtime)
 
 from layer_gpu import HALF, cu_of, dev, host, rounded, torch_dtype
 
@@ -110,7 +111,8 @@ def test_equal_lengths_without_table(dtype):
     check(v, g, dtype, cu=False)
 
 
-@pytest.mark.parametrize("dtype,lens,C,cu", [("bf16", [5000], 16, False), ("f32", [3000, 2999], 24, True), ("bf16", [40, 2600, 0, 1500, 511, 513], 72, True)])
+@pytest.mark.parametrize("dtype,lens,C,cu", [("bf16", [5000], 16, False), ("f32", [3000, 2999], 24, True), ("bf16", [40, 2600, 0, 1500, 511, 513], 72, True),
+                                             ("f32", [9000, 30, 4400], 8, True)])
 def test_sequences_cut_into_segments(dtype, lens, C, cu):
     import gated_delta_rule_34_amd as G
     import torch

@@ -5,6 +5,7 @@ and a training step through the same blocks. Each operator's outputs are held to
 (so the tolerances are those of the operators' own tests). Then what the binding refuses."""
 import numpy as np
 import pytest
+import torch  # noqa: F401  (in front of the package, which then has torch's HIP runtime)
 
 from layer_gpu import dev, host, rounded
 from test_glr_gpu import i32

@@ -9,6 +9,7 @@ import math
 
 import numpy as np
 import pytest
+import torch  # noqa: F401  (in front of the package, which then has torch's HIP runtime)
 
 from layer_gpu import HALF, dev, host, rounded, torch_dtype
 from test_glr_gpu import i32, view
@@ -93,6 +94,17 @@ def test_long_ones_are_split_and_joined(dtype, D, page):
     c = case([3000, 0, 257, 256, 1], 4, 2, D, page, dtype, D)
     _, _, p = check(c, dtype)
     assert G.gdn_paged_attn_workspace_bytes(p) > 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_chunk_or_several(dtype):
+    """At the longest cache that one chunk takes, and one token behind it."""
+    import gated_delta_rule_34_amd as G
+
+    for D, most in ((64, 512), (256, 256)):
+        for more in (0, 1):
+            _, _, p = check(case([most + more, 3, most - 1], 3, 1, D, 1, dtype, D + more), dtype)
+            assert (G.gdn_paged_attn_workspace_bytes(p) > 0) == bool(more)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -7,6 +7,7 @@ in a tree and its root some 32 2^-24, the weight, the cosine and sine (their ser
 absolute terms. Sums over rows (dwq, dwk): 64 2^-24 of the sum of the terms' sizes."""
 import numpy as np
 import pytest
+import torch  # noqa: F401  (in front of the package, which then has torch's HIP runtime)
 
 from layer_gpu import HALF, dev, host, rounded, torch_dtype
 from test_glr_gpu import i32, view

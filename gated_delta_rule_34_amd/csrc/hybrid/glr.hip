@@ -19,7 +19,7 @@
 // finds first. Measured (bf16): 4 x 4096 tokens x 2560 forward 95 us, backward 167 us, bound by the gates (five
 // instructions of a quarter of the rate and some 30 others a value, in the 160 compute units that have a workgroup); one prompt of
 // 16384 x 4096 77 us for the maps and 91 for the states, bound by HBM (5.2 and 5.9 TB/s); float32, 1336
-// ragged tokens x 1032, 8 us for the maps, 18 forward and 22 backward: the latency of a few tiles one after the other.
+// ragged tokens x 1032, 8 us for the maps, 16 forward and 21 backward: the latency of a few tiles one after the other.
 #include "../gdn_common.h"
 #include "../layer/rows.h"
 #include "../layer/vec8.h"
@@ -68,6 +68,23 @@ template <typename TI, int V> __device__ __forceinline__ i32x4 glr_raw(const flo
 __device__ __forceinline__ float glr_rate(float rate, float lam) {
   const float c = rate * softplusf(lam);
   return c > 0x1p100f ? 0x1p100f : c;
+}
+
+// The sigmoid. Of float32 rows: exp(-z) = 2^(t + lo), the product with log2(e) in two parts, the hardware's power (1 ulp), and its
+// reciprocal with a Newton step, together 3 ulp; below -87 zero (float32 keeps no more there), past 87 one. With expf and a division
+// a prompt of 8192 x 4096 took 170 us, so 145.
+template <typename TI> __device__ __forceinline__ float glr_sigmoid(float z) {
+  if constexpr (sizeof(TI) == 2) {
+    return sigmoidf<TI>(z);
+  } else {
+    const bool gone = z < -87.f;
+    z = gone ? -87.f : z;  // (a NaN stays)
+    z = z > 87.f ? 87.f : z;
+    const float t = z * -1.44269504f, lo = fmaf(z, -1.92596299e-8f, fmaf(z, -1.44269504f, -t));
+    const float x = __builtin_amdgcn_exp2f(t), d = fmaf(x, lo * 0.693147181f, x) + 1.f;
+    const float r = __builtin_amdgcn_rcpf(d);
+    return gone ? 0.f : fmaf(fmaf(-d, r, 1.f), r, r);
+  }
 }
 
 // exp(-L), for L >= 0.
@@ -276,7 +293,7 @@ template <typename TI, bool FWD> __global__ __launch_bounds__(GNT) void k_glr_ma
     if (b + 1 < run) load(FWD ? t + 1 : t - 1);
     if (t >= q.t1) continue;
 #pragma unroll
-    for (int j = 0; j < V; ++j) L[j] = rate[j] * sigmoidf<TI>(r[j]);
+    for (int j = 0; j < V; ++j) L[j] = rate[j] * glr_sigmoid<TI>(r[j]);
     one_minus_exp<TI, V>(L, deep, e);
     if (fresh && t == q.lo)
 #pragma unroll
@@ -284,7 +301,7 @@ template <typename TI, bool FWD> __global__ __launch_bounds__(GNT) void k_glr_ma
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float a1 = 1.f - e[j];
-      if constexpr (FWD) B[j] = fmaf(a1, B[j], glr_weight(e[j], a1) * (sigmoidf<TI>(iv[j]) * x[j]));
+      if constexpr (FWD) B[j] = fmaf(a1, B[j], glr_weight(e[j], a1) * (glr_sigmoid<TI>(iv[j]) * x[j]));
       else B[j] = a1 * (B[j] + x[j]);
       E[j] = fmaf(E[j], a1, e[j]);
     }
@@ -371,7 +388,7 @@ template <typename TI, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_f
       glr_cvt<TI, V>(rr[k], r);
       glr_cvt<TI, V>(ri[k], i);
 #pragma unroll
-      for (int j = 0; j < V; ++j) L[j] = rate[j] * sigmoidf<TI>(r[j]);
+      for (int j = 0; j < V; ++j) L[j] = rate[j] * glr_sigmoid<TI>(r[j]);
       one_minus_exp<TI, V>(L, deep, e);
       if (!plain) {
         const int64_t row = t + me.tt * GK + k;
@@ -385,7 +402,7 @@ template <typename TI, bool SAVE> __global__ __launch_bounds__(GNT) void k_glr_f
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         a1[k][j] = 1.f - e[j];
-        b[k][j] = glr_weight(e[j], a1[k][j]) * (sigmoidf<TI>(i[j]) * x[j]);
+        b[k][j] = glr_weight(e[j], a1[k][j]) * (glr_sigmoid<TI>(i[j]) * x[j]);
         B[j] = k ? fmaf(a1[k][j], B[j], b[k][j]) : b[k][j];
         E[j] = k ? fmaf(E[j], a1[k][j], e[j]) : e[j];
       }
@@ -483,8 +500,8 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       kd[k] = rd[k];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        sr[k][j] = sigmoidf<TI>(r[j]);
-        si[k][j] = sigmoidf<TI>(i[j]);
+        sr[k][j] = glr_sigmoid<TI>(r[j]);
+        si[k][j] = glr_sigmoid<TI>(i[j]);
         L[j] = rate[j] * sr[k][j];
       }
       one_minus_exp<TI, V>(L, deep, e[k]);
@@ -640,12 +657,12 @@ template <typename TI> __global__ __launch_bounds__(64) void k_glr_decode(GlrArg
   if (!fresh) h = *st;
   float L[GD], e[GD];
 #pragma unroll
-  for (int j = 0; j < GD; ++j) L[j] = glr_rate(a.rate, lam[j]) * sigmoidf<TI>((float)r[j]);
+  for (int j = 0; j < GD; ++j) L[j] = glr_rate(a.rate, lam[j]) * glr_sigmoid<TI>((float)r[j]);
   one_minus_exp<TI, GD>(L, true, e);
   vec y;
 #pragma unroll
   for (int j = 0; j < GD; ++j) {
-    const float u = sigmoidf<TI>((float)i[j]) * (float)x[j];
+    const float u = glr_sigmoid<TI>((float)i[j]) * (float)x[j];
     h[j] = fresh ? u : fmaf(-e[j], h[j], h[j]) + glr_weight(e[j], 1.f - e[j]) * u;
     y[j] = (TI)h[j];
   }

@@ -157,7 +157,7 @@ __global__ __launch_bounds__(64 * PW, paged_resident(D * (int)sizeof(TI))) void 
     q[p] = i32x4{0, 0, 0, 0};
     if (j < nh) q[p] = *reinterpret_cast<const i32x4*>((const TI*)a.q + (int64_t)n * a.q_rs + (int64_t)(h0 + j) * D + (p * 64 + g * 16) / (int)sizeof(TI));
   }
-  const float sc = a.scale * 1.44269504f;
+  const float sc = a.scale * 1.44269504f, sc_lo = fmaf(a.scale, 1.44269504f, -sc) + a.scale * 1.92596299e-8f;
   f32x4 o[VE];
 #pragma unroll
   for (int e = 0; e < VE; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -220,11 +220,14 @@ __global__ __launch_bounds__(64 * PW, paged_resident(D * (int)sizeof(TI))) void 
       for (int c = 0; c < KP; ++c)
         s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[c]), __builtin_bit_cast(bf16x8, q[c]), s, 0, 0, 0);
     } else {
+      // four sums side by side: one chain of D products rounds twice as far (heads of 256: 1.1e-6 off the result in all, so 3.6e-7)
+      f32x4 part[4] = {s, s, s, s};
 #pragma unroll
       for (int c = 0; c < KP; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          s = __builtin_amdgcn_mfma_f32_16x16x4f32(__int_as_float(k[c][e]), __int_as_float(q[c][e]), s, 0, 0, 0);
+          part[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(__int_as_float(k[c][e]), __int_as_float(q[c][e]), part[e], 0, 0, 0);
+      s = (part[0] + part[1]) + (part[2] + part[3]);
     }
     return s;
   };
@@ -251,7 +254,9 @@ __global__ __launch_bounds__(64 * PW, paged_resident(D * (int)sizeof(TI))) void 
     float p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(z[i] - ref);
+      // (float32: the score times sc in two parts, without the product's rounding)
+      if constexpr (sizeof(TI) == 4) p[i] = z[i] == kNone ? 0.f : __builtin_amdgcn_exp2f(fmaf(s[i], sc, fmaf(s[i], sc_lo, -ref)));
+      else p[i] = __builtin_amdgcn_exp2f(z[i] - ref);
       l += p[i];
     }
     if (!x.full)  // what lies in a place that does not count may be anything, NaN too

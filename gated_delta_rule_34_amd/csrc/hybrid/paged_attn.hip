@@ -29,6 +29,7 @@ constexpr float kNone = -__builtin_inff();
 constexpr int kPagedEven = 256;
 struct PagedPlan {
   int gt, splits, slots, chunk;
+  float share;  // even: chunks of up to 256 tokens are not below this part of all tokens
   bool even;
 };
 
@@ -77,7 +78,9 @@ template <bool ROWS> __device__ __forceinline__ PagedChunk paged_chunk(const Pag
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
   // at most total / chunk + N chunks
-  const int64_t want = (total + p.slots - a.N - 1) / (p.slots - a.N);
+  int64_t want = (total + p.slots - a.N - 1) / (p.slots - a.N);
+  const int round = (int)fminf((float)total * p.share, 256.f);
+  want = want > round ? want : round;
   c.chunk = want <= p.chunk ? p.chunk : (int)((want + PT * PW - 1) / (PT * PW)) * (PT * PW);
   int cnt[U], sum = 0;
 #pragma unroll
@@ -398,12 +401,14 @@ template <typename TI, int D, int SG> __global__ __launch_bounds__(256) void k_p
 // Chunks: as many as the chip holds workgroups at once, so that equal ones end together (one sequence of 131072 tokens, 4 heads
 // of 256: 93 us with 512 of them, 99 with 1024, 114 with 2048), and four more for every sequence, whose last chunks are
 // of unequal lengths (64 sequences of up to 8192 tokens, 8 heads of 128: 217 us with 1024, 195 with 2048, 190 with
-// 4096). None of less than 128 tokens, two tiles for each wave. A launch for the join is not worth it for a few tiles more: up to
+// 4096), but of less than 256 tokens no more than the chip holds (32 sequences of 1000 tokens, 8 heads of 128: 34 us, with four more 38;
+// 128 of up to 1500, 4 heads: 51 and 56). None of less than 128 tokens, two tiles for each wave. A launch for the join is not worth it for a few tiles more: up to
 // 512 tokens (256 of heads past 256 bytes) are one chunk (64 sequences of up to 500 tokens, 8 heads of 128: 23 us, with a join 26; 16
 // of 300, heads of 64: 12 and 17; one of 500: 14 and 17; but one of 1000 24 and 17, 9 of 500, heads of 256: 25 and 17).
 static PagedPlan paged_plan(const PagedArgs& a, int dtype) {
   PagedPlan p;
   p.gt = (a.Hq / a.Hk + 15) / 16;
+  p.share = 0.f;
   const int64_t span = a.window > 0 && a.window < a.max_len ? (int64_t)a.window + PT - 1 : a.max_len;
   const int head_bytes = a.D * (dtype == 0 ? 4 : 2);
   const int64_t heads = (int64_t)a.Hk * p.gt, full = 256 * paged_resident(head_bytes), one = head_bytes <= 256 ? 512 : 256;
@@ -414,6 +419,7 @@ static PagedPlan paged_plan(const PagedArgs& a, int dtype) {
     const int64_t most = a.N * ((span + least - 1) / least);
     p.chunk = least;
     p.splits = 0;
+    p.share = (float)heads / (float)full;
     p.slots = (int)(want < most ? want : most) + a.N;
   } else {
     const int64_t each = (want + a.N - 1) / (a.N > 0 ? a.N : 1);

@@ -290,11 +290,13 @@ def gdn_paged_attn_decode(p, q, k_pages, v_pages, out, lse, workspace, stream=No
     device, dtype = _begin(p, q, "q")
     v = (p.N, p.Hq * p.D, device, dtype)
     kp, vp, n, _ = _pages(k_pages, v_pages, p.Hk, p.page_size, p.D, device, dtype)
-    if getattr(p, "_any", False):
-        p.n_pages = n
+    own = p
+    if getattr(p, "_any", False):  # (a copy: calls at the same time may bring other pools)
+        own = gdn_paged_problem.from_buffer_copy(p)
+        own.n_pages = n
     elif p.n_pages != n:
         raise ValueError(f"k_pages: expected {p.n_pages} pages, got {n}")
-    _call("gdn_paged_attn_decode", p, *_rows(q, "q", *v), kp, vp, *_rows(out, "out", *v),
+    _call("gdn_paged_attn_decode", own, *_rows(q, "q", *v), kp, vp, *_rows(out, "out", *v),
           None if lse is None else _array(lse, "lse", (p.N, p.Hq), device, _l._f32), *_scratch(workspace, device), _on(stream, device))
 
 

@@ -16,10 +16,10 @@
 //
 // Every element is read and written once where one workgroup takes a whole sequence; where that
 // leaves compute units idle, sequences are cut into segments, whose maps an extra pass over the inputs
-// finds first. Measured (bf16): 4 x 4096 tokens x 2560 forward 95 us, backward 167 us, bound by the gates (five
+// finds first. Measured (bf16): 4 x 4096 tokens x 2560 forward 95 us, backward 176 us, bound by the gates (five
 // instructions of a quarter of the rate and some 30 others a value, in the 160 compute units that have a workgroup); one prompt of
 // 16384 x 4096 77 us for the maps and 91 for the states, bound by HBM (5.2 and 5.9 TB/s); float32, 1336
-// ragged tokens x 1032, 8 us for the maps, 16 forward and 21 backward: the latency of a few tiles one after the other.
+// ragged tokens x 1032, 8 us for the maps, 16 forward and 22 backward: the latency of a few tiles one after the other.
 #include "../gdn_common.h"
 #include "../layer/rows.h"
 #include "../layer/vec8.h"
@@ -85,6 +85,29 @@ template <typename TI> __device__ __forceinline__ float glr_sigmoid(float z) {
     const float r = __builtin_amdgcn_rcpf(d);
     return gone ? 0.f : fmaf(fmaf(-d, r, 1.f), r, r);
   }
+}
+
+// s(z) and its complement 1 - s(z) = s(-z) of float32 rows, as in glr_sigmoid from x = exp(-|z|): 1 / (1 + x) and x / (1 + x). (One minus
+// the rounded s keeps 2^-24 of one: at z = 12 1% of itself is wrong, at 17 all.)
+__device__ __forceinline__ void glr_sides(float z, float& s, float& c) {
+  const bool gone = fabsf(z) > 87.f;
+  const float y = gone ? 87.f : fabsf(z);  // (a NaN stays)
+  const float t = y * -1.44269504f, lo = fmaf(y, -1.92596299e-8f, fmaf(y, -1.44269504f, -t));
+  const float p = __builtin_amdgcn_exp2f(t), x = fmaf(p, lo * 0.693147181f, p), d = x + 1.f;
+  const float r = __builtin_amdgcn_rcpf(d), big = fmaf(fmaf(-d, r, 1.f), r, r), small = gone ? 0.f : x * big;
+  s = z > 0.f ? big : small;
+  c = z > 0.f ? small : big;
+}
+// Whether some gate of a wave's bfloat16 rows is past 7 (or a NaN), from where on 1 - s of the rounded s is more than 2e-4 of itself off.
+template <int K> __device__ __forceinline__ bool glr_open(const i32x4 (&r)[K], const i32x4 (&i)[K]) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  s16x2 m{0, 0};  // (positive values are ordered as their bits are, negative ones below zero)
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      m = __builtin_elementwise_max(m, __builtin_elementwise_max(__builtin_bit_cast(s16x2, r[k][j]), __builtin_bit_cast(s16x2, i[k][j])));
+  return __any((m[0] > m[1] ? m[0] : m[1]) > 0x40E0);
 }
 
 // exp(-L), for L >= 0.
@@ -449,6 +472,7 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
   GlrSeg q;
   GLR_PLACE;
   __shared__ float sE[GE][CB], sB[GE][CB], sC[GE][CB], sh[GE][CB], sg[GE][CB];
+  __shared__ i32x4 raw[sizeof(TI) == 2 ? 2 * GK : 1][GNT];
   if (!glr_seg(a, pl, slot, q)) {
     if (part && wave_id() == 0 && mine) part[(int64_t)slot * a.ch + ci] = 0.f;
     return;
@@ -488,8 +512,20 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
     float hs = 0.f;  // wave 0: the tile's saved start
     if (wave_id() == 0 && mine) hs = a.sv[((q.lo / GTILE) + q.n + (t - q.lo) / GTILE) * a.ch + ci];
     const bool plain = t + GTILE <= q.t1 && !(fresh && t == q.lo);
+    // The gates' complements. For those of bfloat16 rows there are not registers enough: they are formed at their use, as 1 - s, and where
+    // a gate is too open for that from its rows, kept in LDS. (4 x 4096 x 2560 176 us, without complements 170, with s(-|z|) under the
+    // sign of z in the place of s 188; gates past 7 in every tile take 30 more.)
+    float cr[GK][V], ci[GK][V];
     float e[GK][V], sr[GK][V], si[GK][V], rw[GK][V], E[V], B[V], Ex[V], Bx[V], F[V], C[V], Fx[V], Cx[V];
     i32x4 kx[GK], kd[GK];
+    bool open = false;
+    if constexpr (sizeof(TI) == 2) open = glr_open(rr, ri);
+    if (open)  // (read by the thread that writes it)
+#pragma unroll
+      for (int k = 0; k < GK; ++k) {
+        raw[2 * k][threadIdx.x] = rr[k];
+        raw[2 * k + 1][threadIdx.x] = ri[k];
+      }
 #pragma unroll
     for (int k = 0; k < GK; ++k) {
       float x[V], r[V], i[V], L[V];
@@ -500,8 +536,13 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       kd[k] = rd[k];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        sr[k][j] = glr_sigmoid<TI>(r[j]);
-        si[k][j] = glr_sigmoid<TI>(i[j]);
+        if constexpr (sizeof(TI) == 2) {
+          sr[k][j] = glr_sigmoid<TI>(r[j]);
+          si[k][j] = glr_sigmoid<TI>(i[j]);
+        } else {
+          glr_sides(r[j], sr[k][j], cr[k][j]);
+          glr_sides(i[j], si[k][j], ci[k][j]);
+        }
         L[j] = rate[j] * sr[k][j];
       }
       one_minus_exp<TI, V>(L, deep, e[k]);
@@ -592,6 +633,23 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
       float x[V], d[V], dx[V], dr[V], di[V];
       glr_cvt<TI, V>(kx[k], x);
       glr_cvt<TI, V>(kd[k], d);
+      if constexpr (sizeof(TI) == 2) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          cr[k][j] = 1.f - sr[k][j];
+          ci[k][j] = 1.f - si[k][j];
+        }
+        if (open) {
+          float r[V], i[V];
+          glr_cvt<TI, V>(raw[2 * k][threadIdx.x], r);
+          glr_cvt<TI, V>(raw[2 * k + 1][threadIdx.x], i);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            cr[k][j] = glr_sigmoid<TI>(-r[j]);
+            ci[k][j] = glr_sigmoid<TI>(-i[j]);
+          }
+        }
+      }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float G = cg[j] + d[j], u = si[k][j] * x[j], L = rate[j] * sr[k][j], a1 = 1.f - e[k][j];
@@ -603,10 +661,10 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
         }
         const float du = fmaf(e[k][j], a1, e[k][j]) * rw[k][j] * G;
         dx[j] = si[k][j] * du;
-        di[j] = u * (1.f - si[k][j]) * du;
+        di[j] = u * ci[k][j] * du;
         // L dL; a and L first, whose product stays finite
         const float LdL = (al * L) * G * fmaf(u * al, rw[k][j], -hp[k][j]);
-        dr[j] = LdL * (1.f - sr[k][j]);
+        dr[j] = LdL * cr[k][j];
         dl[j] += row < q.t1 ? LdL : 0.f;
         cg[j] = a1 * G;
       }

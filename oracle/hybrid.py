@@ -47,7 +47,7 @@ def glr_fwd(cu, x, r, i, lam, rate, h0=None, fresh=None):
 def glr_bwd(cu, x, r, i, lam, rate, h0, fresh, dy, dhT):
     """Gradients of glr_fwd for dy and dhT (None: zeros): dict dx, dr, di, dlam, dh0."""
     L, a, w = glr_gates(r, lam, rate)
-    si, sr = sigmoid(i), sigmoid(r)
+    si, sr, ci = sigmoid(i), sigmoid(r), sigmoid(-i)  # (one minus a sigmoid next to one would be all rounding)
     u = si * x
     y, _ = glr_fwd(cu, x, r, i, lam, rate, h0, fresh)
     g = {k: np.zeros_like(u) for k in ("dx", "dr", "di")}
@@ -59,14 +59,14 @@ def glr_bwd(cu, x, r, i, lam, rate, h0, fresh, dy, dhT):
             first = new and t == lo
             du = G if first else w[t] * G
             g["dx"][t] = si[t] * du
-            g["di"][t] = du * x[t] * si[t] * (1 - si[t])
+            g["di"][t] = du * x[t] * si[t] * ci[t]
             if not first:
                 before = y[t - 1] if t > lo else (0.0 if h0 is None else h0[n])
                 with np.errstate(divide="ignore", invalid="ignore"):
                     dL[t] = np.where(w[t] > 0, G * (u[t] * a[t] ** 2 / w[t] - a[t] * before), 0.0)
             c = np.zeros_like(G) if first else a[t] * G
         dh0[n] = 0.0 if new else c
-    g["dr"] = dL * L * (1 - sr)
+    g["dr"] = dL * L * sigmoid(-r)
     g["dlam"] = (dL * sr).sum(0) * rate * sigmoid(lam)
     g["dh0"] = dh0
     return g

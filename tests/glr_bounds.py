@@ -24,6 +24,7 @@ roundings (sum, product, 1 - e: 6 with those of 8 tokens, 12) count as kb.
 """
 import numpy as np
 
+from layer_gpu import HALF, cu_of, rounded
 from oracle import hybrid as O
 
 E = 2.0 ** -24
@@ -81,10 +82,17 @@ def bounds(cu, x, r, i, lam, rate, h0, fresh, dy, dhT, dtype):
     return {k: 1.01 * v for k, v in out.items()}  # (products of two errors)
 
 
+# (type, lengths, channels, table): one workgroup per sequence, sequences cut into segments of 256 tokens and more, with a table, without one,
+# and more than 256 of them.
+MANY = [int(n) for n in np.random.default_rng(90).integers(0, 12, 300)]
+MANY[40], MANY[41], MANY[299] = 2100, 600, 1500
+CASES = [("f32", [127, 128, 129], 32, True), ("bf16", [515, 1, 130], 72, True), ("f32", [3000, 2999], 24, True),
+         ("bf16", [40, 2600, 0, 1500, 511, 513], 72, True), ("f32", [9000, 30, 4400], 8, True), ("bf16", [9000, 30, 4400], 8, True),
+         ("bf16", [5000], 16, False), ("f32", [1300] * 3, 40, False), ("f32", MANY, 16, True), ("bf16", MANY, 16, True)]
+
+
 def draw(lens, C, seed, dtype, init=True, fresh="some", gates=1.5, near_one=0.999):
     """Inputs that are nowhere negative, rounded to the type that the kernels read."""
-    from layer_gpu import cu_of, rounded
-
     rng = np.random.default_rng(seed)
     T, N = sum(lens), len(lens)
     v = dict(cu=cu_of(lens), x=rounded(rng.uniform(0.1, 2, (T, C)), dtype), r=rounded(gates * rng.standard_normal((T, C)), dtype),
@@ -108,8 +116,6 @@ ROWS = ("y", "dx", "dr", "di")
 
 def beyond(got, want, bound, dtype):
     """By name: the largest difference over its bound."""
-    from layer_gpu import HALF
-
     off = {}
     for k in want:
         tol = bound[k] + 2.0 ** -126

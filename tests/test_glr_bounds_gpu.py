@@ -19,6 +19,19 @@ def check(v, g, dtype, **kw):
     assert max(off.values()) <= 1, off
 
 
+@pytest.mark.parametrize("k", range(len(B.CASES)), ids=lambda k: f"{B.CASES[k][0]}-{len(B.CASES[k][1])}x{sum(B.CASES[k][1])}")
+def test_cases(k):
+    """Outputs and all gradients, of whole sequences and of ones cut into segments."""
+    dtype, lens, C, table = B.CASES[k]
+    check(*B.draw(lens, C, 91 + k, dtype), dtype, cu=table)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("init,fresh", [(True, "none"), (True, "all"), (False, "none")])
+def test_starts(dtype, init, fresh):
+    check(*B.draw([5, 0, 140, 600, 2100], 40, 89, dtype, init, fresh), dtype)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("lens", [[1, 1, 1, 1], [40, 1, 0, 7, 200], [300, 777]])
 def test_gradients_of_open_gates(dtype, lens):

@@ -688,8 +688,10 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
 #pragma unroll
       for (int g = 0; g < GE; ++g) s += sE[g][lane_id()];
       const float lam = a.lam[ci], sp = softplusf(lam);
-      // sigmoid / softplus; both vanish together, and with them the sum
-      part[(int64_t)slot * a.ch + ci] = sp > 0.f ? s * ((1.f / (1.f + expf(-lam))) / sp) : 0.f;
+      // sigmoid / softplus: one to float32 below -20 (and expf(-lam) ends at -88, where softplus does not); where softplus is zero, so
+      // are the exponents
+      const float q = lam < -20.f ? 1.f : 1.f / (1.f + expf(-lam)) / sp;
+      part[(int64_t)slot * a.ch + ci] = sp > 0.f ? s * q : 0.f;
     }
   }
 }

@@ -71,3 +71,16 @@ def test_gates_without_a_complement(dtype, z):
     out = run(v, g, dtype)
     assert all(bool(torch.isfinite(t).all()) for t in out.values())
     assert not out["dr"][:, :8].any() and not out["di"][:, 8:].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dlambda_of_very_small_rates(dtype):
+    """lambda down to -92, where the softplus is a float32 below 2^-126 (off by up to 2^-149) and exp(-lambda) is none: with a rate of 1e5
+    the exponents and dlambda are ordinary numbers."""
+    v, g = B.draw([300, 40, 700], 24, 85, dtype, fresh="none")
+    v["lam"], v["rate"] = rounded(np.repeat([-20.5, -60.0, -88.0, -89.0, -90.5, -92.0], 4), "f32"), 1e5
+    got, want = host(run(v, g, dtype)["dlam"]), B.wanted(v, g)["dlam"]
+    bound = B.bounds(*[v[k] for k in ("cu", "x", "r", "i", "lam", "rate", "h0", "fresh")], *g.values(), dtype)["dlam"]
+    step = 2.0 ** -149 * np.exp(-v["lam"])  # of the softplus, relative
+    assert (np.abs(want) > 2.0 ** -100).all() and (bound < 1e-3 * np.abs(want)).all() and (step < 1e-4).all()
+    assert (np.abs(got - want) <= bound + step * np.abs(want)).all()

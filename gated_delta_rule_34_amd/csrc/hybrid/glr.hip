@@ -699,7 +699,7 @@ template <typename TI> __global__ __launch_bounds__(GNT) void k_glr_bwd(GlrArgs 
 // ------------------------------------------------------------------ one token
 // Two channels per thread: softplus takes some 100 instructions, and the calls are short (one row of 2560 2.9 us, 256 rows 5.0; with
 // eight channels 4.8 and 6.8). Many rows are bound by HBM either way: 4096 x 4096 60 and 58 us.
-constexpr int GD = 2;
+constexpr int GD = kGlrTokenChannels / 64;
 template <typename TI> __global__ __launch_bounds__(64) void k_glr_decode(GlrArgs a) {
   typedef TI vec __attribute__((ext_vector_type(GD)));
   typedef float fvec __attribute__((ext_vector_type(GD)));
@@ -809,7 +809,7 @@ hipError_t launch_glr_backward(const GlrArgs& a, int dtype, hipStream_t s) {
 }
 hipError_t launch_glr_decode(const GlrArgs& a, int dtype, hipStream_t s) {
   if (a.N == 0) return hipSuccess;
-  const dim3 grid((unsigned)a.N, (unsigned)((a.ch / GD + 63) / 64));
+  const dim3 grid((unsigned)a.N, (unsigned)((a.ch + kGlrTokenChannels - 1) / kGlrTokenChannels));
   traced("k_glr_decode", s, [&] {
     if (dtype == 0) k_glr_decode<float><<<grid, 64, 0, s>>>(a);
     else k_glr_decode<__bf16><<<grid, 64, 0, s>>>(a);

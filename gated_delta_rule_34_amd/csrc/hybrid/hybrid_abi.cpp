@@ -31,6 +31,8 @@ gdn::GlrArgs glr_args(const gdn_glr_problem* p) {
   return a;
 }
 
+constexpr int64_t kGlrRowBytes = 1 << 23;
+
 gdn_status check_glr(const gdn_glr_problem* p) {
   if (!p || p->channels <= 0 || p->channels % 8) return GDN_EINVAL;
   if (!known_dtype(p->dtype)) return GDN_EUNSUPPORTED;
@@ -38,14 +40,17 @@ gdn_status check_glr(const gdn_glr_problem* p) {
   GDN_TRY(check_seqs(p->N, p->T, p->T_total, p->cu_seqlens));
   GDN_TRY(check_arr(p->lambda, true, 16));
   GDN_TRY(check_arr(p->fresh, false));
-  // launch limits: workgroups of 512 threads, and of a token per row and 512 channels
-  if (p->N > kMaxBlocks / 2 || p->channels / 512 >= 65535) return GDN_EINVAL;
+  // a row's stride is below 2^23 bytes (glr_view), and so are its channels, rows or none; the token kernel's grid then ends far below 65536
+  if (p->channels >= kGlrRowBytes / esize(p->dtype)) return GDN_EINVAL;
+  static_assert(kGlrRowBytes / 2 / gdn::kGlrTokenChannels < 65535, "grid.y of k_glr_decode");
+  // launch limit: workgroups of 512 threads
+  if (p->N > kMaxBlocks / 2) return GDN_EINVAL;
   return gdn::glr_blocks(glr_args(p), p->dtype) <= kMaxBlocks / 2 ? GDN_OK : GDN_EINVAL;
 }
 
 // A row view of the recurrence: its kernels address the rows of two tiles of 128 with 31-bit byte offsets.
 gdn_status glr_view(const gdn_glr_problem* p, const void* v, int64_t rs) {
-  if (p->T_total > 0 && rs >= ((int64_t)1 << 23) / esize(p->dtype)) return GDN_EINVAL;
+  if (p->T_total > 0 && rs >= kGlrRowBytes / esize(p->dtype)) return GDN_EINVAL;
   return check_view(v, rs, p->channels, p->dtype, p->T_total);
 }
 

@@ -26,6 +26,7 @@ struct GlrArgs {
   int n_slots;
   const int* idx;
 };
+constexpr int kGlrTokenChannels = 128;  // of a workgroup of the token kernel
 int64_t glr_blocks(const GlrArgs& a, int dtype);  // workgroups of a launch
 size_t glr_fwd_ws_bytes(const GlrArgs& a, int dtype);
 size_t glr_bwd_ws_bytes(const GlrArgs& a, int dtype);

@@ -38,7 +38,7 @@ typedef struct {
   int32_t T;        /* tokens per sequence when cu_seqlens is NULL; ignored otherwise */
   int64_t T_total;  /* rows, up to 2^28 */
   const int32_t* cu_seqlens; /* DEVICE int32 [N + 1] as in gdn_problem, or NULL; empty sequences allowed */
-  int32_t channels; /* a positive multiple of 8; (T_total / 512 + N) channels / 32 below 2^23 */
+  int32_t channels; /* a positive multiple of 8, below 2^23 bytes; (N + 1) ceil(channels / 32) + 512 up to 2^23 */
   int32_t dtype;    /* gdn_dtype of x, r, i, y and their gradients */
   float rate;       /* finite, > 0 */
   const float* lambda;   /* [channels], 16-byte aligned */

@@ -93,7 +93,7 @@ gdn_status gdn_glr_decode(const gdn_glr_problem* p, const void* x, int64_t x_rs,
  * the values behind stay. Angles and their reduction are float64.
  */
 typedef struct {
-  int64_t rows;       /* rows (Hq + 2 Hk) < 2^31 */
+  int64_t rows;       /* up to 2^25 - 2; rows (Hq + 2 Hk) < 2^31, Hq + 2 Hk < 2^21 */
   int32_t Hq, Hk, D;  /* heads and head size: a multiple of 16 up to 256 */
   int32_t rot;        /* values of a head that are rotated: a multiple of 16, 0 .. D */
   int32_t adjacent;   /* 0: pairs (j, j + rot / 2); else (2 j, 2 j + 1) */
@@ -138,7 +138,7 @@ gdn_status gdn_qk_rope_cache(const gdn_qk_rope_problem* p, const void* q, int64_
  * lse minus infinity. Weights and sums are float32.
  */
 typedef struct {
-  int32_t N;           /* sequences (>= 0) */
+  int32_t N;           /* sequences (>= 0); N Hq < 2^24, 6 N Hk ceil(Hq / (16 Hk)) < 2^24 - 1024 */
   int32_t Hq, Hk, D;   /* Hq % Hk == 0; head size 32, 64, 128 or 256 */
   int32_t page_size;   /* tokens per page (>= 1) */
   int32_t n_pages;     /* pages of the pool (>= 0); n_pages * page_size * Hk < 2^32, n_pages * page_size < 2^31 */

@@ -29,3 +29,41 @@ def test_recurrence_takes_what_the_header_says(G, table, bf16):
         assert not glr(G, 1 << 23, 0, channels, dtype, table) and not glr(G, 1 << 23, 1 << 23, channels, dtype, table)
     for channels in ((1 << 23) // size, 1 << 23, 1 << 28, 2**31 - 8):
         assert not glr(G, 1, 0, channels, dtype, table) and not glr(G, 1, 1, channels, dtype, table), channels
+
+
+def rope(G, rows, Hq, Hk):
+    p = G.gdn_qk_rope_problem(rows=rows, Hq=Hq, Hk=Hk, D=16, rope_scale=1.0)
+    return G.gdn_qk_rope_bwd_workspace_bytes(p) > 0
+
+
+def test_rotation_takes_what_the_header_says(G):
+    """rows up to 2^25 - 2, rows (Hq + 2 Hk) below 2^31, Hq + 2 Hk below 2^21."""
+    for Hq, Hk in ((1, 1), (24, 4), (50, 8), (63, 1), (4095, 4096)):
+        most = min((1 << 25) - 2, (2**31 - 1) // (Hq + 2 * Hk))
+        assert rope(G, most, Hq, Hk) and not rope(G, most + 1, Hq, Hk), (Hq, Hk)
+    assert rope(G, 0, (1 << 21) - 3, 1) and not rope(G, 0, (1 << 21) - 2, 1)
+
+
+def paged(G, N, Hq, Hk, D, most, window, bf16):
+    """Whether the problem is taken: its call then misses the workspace, or (none needed) the rows of q."""
+    import ctypes
+
+    p = G.gdn_paged_problem(N=N, Hq=Hq, Hk=Hk, D=D, page_size=16, n_pages=1, max_pages=-(-most // 16), max_len=most, window=window, scale=1.0,
+                            dtype=G.GDN_BF16 if bf16 else G.GDN_F32, page_table=A, lens=A)
+    q = 0 if G.gdn_paged_attn_workspace_bytes(p) == 0 else A
+    st = G.layer._fn("gdn_paged_attn_decode")(ctypes.byref(p), q, Hq * D, A * 2, A * 3, A * 4, Hq * D, None, None, 0, None)
+    return st == G.GDN_EWORKSPACE if q else None
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (8, 8), (16, 1), (17, 1), (24, 3), (64, 2), (200, 1)])
+def test_attention_takes_what_the_header_says(G, bf16, Hq, Hk):
+    """N Hq below 2^24, and 6 N Hk ceil(Hq / (16 Hk)) below 2^24 - 1024, at every length; N Hq past it never."""
+    heads = Hk * -(-Hq // (16 * Hk))
+    N = min(((1 << 24) - 1) // Hq, ((1 << 24) - 1025) // (6 * heads))
+    for D in (32, 64, 128, 256):
+        for n in (1, 2, 255, 256, 257, 1000, 70001, N):
+            for most in (1000, 4097, 1 << 20, 1 << 30):
+                for window in (0, 700, 100000):
+                    assert paged(G, n, Hq, Hk, D, most, window, bf16), (D, n, most, window)
+        assert not paged(G, -(-(1 << 24) // Hq), Hq, Hk, D, 5000, 0, bf16)

@@ -736,7 +736,8 @@ template <typename TI> __global__ __launch_bounds__(64) void k_glr_decode(GlrArg
 // workgroups 331 us, cut into eighths by 512 169 with the pass for their maps; 4 x 4096 x 2560 by 160 workgroups 95 us, cut
 // into quarters 80 + 75. So a sequence is cut, finely, where it is longer than its share of 128 workgroups, down to two tiles
 // (a training step of 1024 x 2560, whole 73 us, by two tiles 51; of 3800 float32 tokens x 512, by two tiles 43, by one 50) but
-// not up to 512 tokens (500 and 300 tokens x 2560 44 us, with 256 for 512 42, one prompt of 300 x 1024 12.8 and 17.7).
+// not up to 512 tokens (500 and 300 tokens x 2560 44 us, with 256 for 512 42, one prompt of 300 x 1024 12.8 and 17.7). On either side of the
+// 128 (training steps of sequences of 4096 x 2560): three are cut, 216 us, whole 267; four are not, 282, cut 288; five 302 and 382.
 static GlrPlan glr_plan(const GlrArgs& a, int dtype) {
   GlrPlan p;
   const int CB = dtype == 0 ? 32 : 64;

@@ -2,9 +2,11 @@
 //
 //   z_t = scale q . k_t,  out = sum_t exp(z_t - lse) v_t,  lse = log sum_t exp(z_t)
 //
-// One pass over the cache with the running maximum m and sum l of the softmax, in log2 units. Every key and value is
-// read once: bound by HBM. A workgroup takes a chunk of one sequence's tokens for up to 16 query heads of a key head,
-// its waves tiles of 16 tokens in turn. Nothing passes through LDS inside a tile:
+// One pass over the cache with the running maximum m and sum l of the softmax, in log2 units. A workgroup takes a chunk of one
+// sequence's tokens for up to 16 query heads of a key head, its waves tiles of 16 tokens in turn: every key and value is read once for
+// each 16 query heads of its key head, and the kernel is bound by HBM (64 sequences of up to 8192 tokens, 4 key heads of 128, 16 query
+// heads to each: bfloat16 120 us, float32 210; 17 to 32 of them, two reads: 216 to 228 and 388 to 408; 33: bfloat16 313).
+// Nothing passes through LDS inside a tile:
 //   S = K Q^T with the tokens as rows (16x16x32 bf16, or 16x16x4 float32): lane (g, j) = (l / 16, l % 16) reads 16 bytes of
 //   token j as its operand and receives S of tokens 4g .. 4g + 3 for head j;
 //   O += P V by 16x16x4 float32 instructions, step i over the tokens 4g + i: P's operand is the very register that S left
@@ -25,7 +27,9 @@ constexpr float kNone = -__builtin_inff();
 // How a launch cuts its sequences into chunks, each a workgroup per key head and 16 query heads.
 //   even: chunks of one length, found on the device from the lengths as they are, so that there are at most `slots`
 //     of them (up to kPagedEven sequences); chunk c takes slot c of the workspace;
-//   else: `chunk` tokens each, `splits` of them to every sequence, in use or not; slot n splits + split.
+//   else: `chunk` tokens each, `splits` of them to every sequence, in use or not; slot n splits + split. Sequences of like lengths run
+//     as fast (256 of up to 8000 tokens, 4 key heads of 128: 363 us, 257 365; of up to 1500 89 and 81), but a long one among short ones has
+//     only its own few workgroups (one of 131072 among others of 200, 8 heads: 256 of them 185 us, 257 642).
 constexpr int kPagedEven = 256;
 struct PagedPlan {
   int gt, splits, slots, chunk;

@@ -31,7 +31,9 @@ extern "C" {
  *
  * starting from h0 (zero when NULL). The first token of a sequence that is `fresh` enters with weight
  * one and no decay, h = s(i) x (its h0 is not read). x, r, i, y: [rows][channels] in dtype, a row
- * stride below 2^23 bytes; sums and states are float32, 1 - a is formed without cancellation. rate softplus(lambda) counts up to 2^100.
+ * stride below 2^23 bytes; sums and states are float32, 1 - a and 1 - s are formed without cancellation. What strong decays
+ * leave of a state (or of a gradient from behind) is off by some 2^-24 of the state in front of them, not of itself. rate
+ * softplus(lambda) counts up to 2^100.
  */
 typedef struct {
   int32_t N;        /* sequences (>= 0) */
@@ -119,8 +121,9 @@ gdn_status gdn_qk_rope_bwd(const gdn_qk_rope_problem* p, const void* q, int64_t 
                            void* stream);
 
 /*
- * The serving form: queries to rows, keys (normalised and rotated) and values (as they are) into pages
- * [n_pages][Hk][page_size][D] (dtype, 16-byte aligned; k_pages and v_pages are different buffers). v:
+ * The serving form: queries to rows, keys (normalised and rotated) and values (as they are) into pages, and nowhere else,
+ * [n_pages][Hk][page_size][D] (dtype, 16-byte aligned; k_pages and v_pages are different buffers; of the head sizes,
+ * gdn_paged_attn_decode reads 32, 64, 128 and 256). v:
  * [rows][Hk*D]. where: int32 [rows], a row's place page * page_size + offset; a row whose place is outside
  * [0, n_pages * page_size), -1 for instance, is not cached (its query is written all the same). Two rows
  * of one place race. n_pages * page_size * Hk < 2^32, n_pages * page_size < 2^31.
@@ -135,7 +138,7 @@ gdn_status gdn_qk_rope_cache(const gdn_qk_rope_problem* p, const void* q, int64_
  *   z_t = scale q . k_t,  out = sum_t exp(z_t - lse) v_t,  lse = log sum_t exp(z_t)
  * over the last `window` of its tokens (all when window is 0). A length counts as at least 0 and at most
  * max_len; tokens of a page outside [0, n_pages) are left out. Where nothing is left, out is zero and
- * lse minus infinity. Weights and sums are float32.
+ * lse minus infinity. Weights and sums are float32. The cache is read once for every 16 query heads of a key head.
  */
 typedef struct {
   int32_t N;           /* sequences (>= 0); N Hq < 2^24, 6 N Hk ceil(Hq / (16 Hk)) < 2^24 - 1024 */
